@@ -11,6 +11,9 @@ from ._binding import (  # noqa: F401
     Q8Error,
     abi_version,
     lib,
+    lora_add,
+    lora_gate_up_silu,
+    lora_workspace_bytes,
     moe_route_topk,
     probe_empty,
     probe_shape_count,
@@ -27,9 +30,14 @@ from ._binding import (  # noqa: F401
     q8_linear,
     q8_linear_fused_gate_up_silu,
     q8_linear_fused_gate_up_silu_q8act,
+    q8_linear_fused_gate_up_silu_lora,
+    q8_linear_lora,
+    q8_linear_lora_workspace_bytes,
     q8_linear_q8act,
     q8_moe_grouped_linear,
     q8_moe_grouped_linear_noalloc,
+    q8_moe_layer,
+    q8_moe_layer_workspace_bytes,
     q8_moe_workspace_bytes,
     q8_quantize_act,
 )

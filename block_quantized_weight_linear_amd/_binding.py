@@ -72,6 +72,32 @@ lib.q8_moe_grouped_linear_noalloc.restype = ctypes.c_int
 lib.q8_moe_grouped_linear_noalloc.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _vp,
                                               _i64, _vp]
 
+
+
+class _Lora(ctypes.Structure):
+    """struct q8_lora"""
+    _fields_ = [("a", _vp), ("b", _vp), ("ranks", _vp), ("scale", _vp), ("adapter", _vp),
+                ("section_rows", _i64 * 4), ("type", _i32), ("n_adapters", _i32), ("rank", _i32),
+                ("n_sections", _i32)]
+
+
+_lp = ctypes.POINTER(_Lora)
+lib.q8_linear_lora_workspace_bytes.restype = _sz
+lib.q8_linear_lora_workspace_bytes.argtypes = [_i64, _i64, _i64, _lp]
+for _name in ("q8_linear_lora", "q8_linear_fused_gate_up_silu_lora"):
+    getattr(lib, _name).restype = ctypes.c_int
+    getattr(lib, _name).argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _lp, _vp, _i64, _vp, _sz, _vp]
+lib.lora_workspace_bytes.restype = _sz
+lib.lora_workspace_bytes.argtypes = [_i64, _lp]
+for _name in ("lora_add", "lora_gate_up_silu"):
+    getattr(lib, _name).restype = ctypes.c_int
+    getattr(lib, _name).argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _lp, _vp, _i64, _vp, _sz, _vp]
+lib.q8_moe_layer_workspace_bytes.restype = _sz
+lib.q8_moe_layer_workspace_bytes.argtypes = [_i64, _i32, _i64, _i64, _i64]
+lib.q8_moe_layer.restype = ctypes.c_int
+lib.q8_moe_layer.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i32, _i32, ctypes.c_float, _vp, _i64,
+                             _vp, _sz, _vp]
+
 # measurement aids (include/q8_probe.h)
 lib.q8_probe_shape_count.restype = _i32
 lib.q8_probe_shape_count.argtypes = []
@@ -376,6 +402,149 @@ def q8_moe_grouped_linear_noalloc(w_gate_up_exps, w_down_exps, n_exp: int, f: in
     _call(dev, lib.q8_moe_grouped_linear_noalloc, w_gate_up_exps.data_ptr(), w_down_exps.data_ptr(), n_exp, f, h,
           x.data_ptr(), m, _ld(x, h), topk_idx.data_ptr(), topk_w.data_ptr(), k, out.data_ptr(), _ld(out, h),
           _stream(x))
+    return out
+
+
+# ---------------------------------------------------------- low-rank adapters
+
+_LORA_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _lora(a, b, adapter, scale, ranks, sections, n, k, m, device):
+    """The q8_lora of one call (its tensors must stay alive until the call returns)."""
+    if not isinstance(a, torch.Tensor) or a.dtype not in _LORA_TYPES:
+        raise ValueError("a must be a float32, float16 or bfloat16 tensor")
+    _dev(a, a.dtype, "a", device)
+    _dev(b, a.dtype, "b", device)
+    sections = (n,) if sections is None else tuple(sections)
+    if not 1 <= len(sections) <= 4 or sum(sections) != n or min(sections) < 0:
+        raise ValueError(f"sections must be 1 to 4 sizes that sum to {n}, got {sections}")
+    if b.dim() != 3 or b.shape[1] != n or not b.is_contiguous():
+        raise ValueError(f"b must be a contiguous [n_adapters][{n}][rank] tensor, got {tuple(b.shape)}")
+    count, _, rank = b.shape
+    _contig_out(a, (count, len(sections) * rank, k), "a", a.dtype, device)
+    _contig_out(adapter, (m,), "adapter", torch.int32, device)
+    if scale is not None:
+        _contig_out(scale, (count,), "scale", torch.float32, device)
+    if ranks is not None:
+        _contig_out(ranks, (count,), "ranks", torch.int32, device)
+    return _Lora(a.data_ptr(), b.data_ptr(), None if ranks is None else ranks.data_ptr(),
+                 None if scale is None else scale.data_ptr(), adapter.data_ptr(), sections, _LORA_TYPES[a.dtype],
+                 count, rank, len(sections))
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return _bytes(workspace, 0, "workspace", device)
+
+
+def q8_linear_lora_workspace_bytes(m: int, n: int, k: int, rank: int, n_sections: int = 1) -> int:
+    """Workspace bytes of q8_linear_lora (q8_linear_fused_gate_up_silu_lora: n = 2f)."""
+    return int(lib.q8_linear_lora_workspace_bytes(m, n, k, _Lora(rank=rank, n_sections=n_sections)))
+
+
+def lora_workspace_bytes(m: int, rank: int, n_sections: int = 1) -> int:
+    """Workspace bytes of lora_add and lora_gate_up_silu."""
+    return int(lib.lora_workspace_bytes(m, _Lora(rank=rank, n_sections=n_sections)))
+
+
+def _linear_lora(fn, w, n_w, n_out, k, x, a, b, adapter, scale, ranks, sections, out, workspace):
+    _dev(x, torch.float32, "x")
+    dev = x.device
+    m = _rows_in(x, k, "x")
+    lo = _lora(a, b, adapter, scale, ranks, sections, n_w, k, m, dev)
+    _bytes(w, _quant_bytes(n_w, k, Q8_0_BYTES) if n_out and m else 0, "w", dev)
+    if out is None:
+        out = torch.empty((m, n_out), dtype=torch.float32, device=dev)
+    _rows_out(out, m, n_out, "out", torch.float32, dev)
+    workspace = _workspace(workspace, lib.q8_linear_lora_workspace_bytes(m, n_w, k, lo), dev)
+    _call(dev, fn, w.data_ptr(), n_out, k, x.data_ptr(), m, _ld(x, k), lo, out.data_ptr(), _ld(out, n_out),
+          workspace.data_ptr(), workspace.numel(), _stream(x))
+    return out
+
+
+def q8_linear_lora(w, n: int, k: int, x, a, b, adapter, scale=None, ranks=None, sections=None, out=None,
+                   workspace=None):
+    """y = x . W^T + D for a Q8_0 weight W [n][k]; D is each row's low-rank correction,
+    D[t] = scale[e] * B[e] (A[e] x[t]) with e = adapter[t] (outside [0, n_adapters): none).
+
+    a [n_adapters][len(sections) * rank][k] and b [n_adapters][n][rank] in float32, float16
+    or bfloat16 (rank a multiple of 8), adapter int32 [m], scale float32 [n_adapters],
+    ranks int32 [n_adapters] (each adapter's own rank, at most `rank`); sections: the row
+    counts of a fused matrix's parts, each with its own `rank` rows of a."""
+    return _linear_lora(lib.q8_linear_lora, w, n, n, k, x, a, b, adapter, scale, ranks, sections, out, workspace)
+
+
+def q8_linear_fused_gate_up_silu_lora(w, f: int, k: int, x, a, b, adapter, scale=None, ranks=None, sections=None,
+                                      out=None, workspace=None):
+    """h = SiLU(g) * u with [g u] = x . W^T + D, W Q8_0 [2f][k], gate rows first; the
+    adapters as for q8_linear_lora with n = 2f (sections (f, f): gate and up apart)."""
+    return _linear_lora(lib.q8_linear_fused_gate_up_silu_lora, w, 2 * f, f, k, x, a, b, adapter, scale, ranks,
+                        sections, out, workspace)
+
+
+def _lora_beside(fn, y, n_in, n_out, x, a, b, adapter, scale, ranks, sections, out, workspace):
+    _dev(x, torch.float32, "x")
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [m][k]")
+    m, k = x.shape
+    _rows_in(x, k, "x")
+    _rows_out(y, m, n_in, "the product", torch.float32, dev)
+    lo = _lora(a, b, adapter, scale, ranks, sections, n_in, k, m, dev)
+    if out is None:
+        out = torch.empty((m, n_out), dtype=torch.float32, device=dev)
+    _rows_out(out, m, n_out, "out", torch.float32, dev)
+    workspace = _workspace(workspace, lib.lora_workspace_bytes(m, lo), dev)
+    _call(dev, fn, y.data_ptr(), n_out, y.stride(0) if m > 1 else n_in, x.data_ptr(), m, k, _ld(x, k), lo,
+          out.data_ptr(), out.stride(0) if m > 1 else n_out, workspace.data_ptr(), workspace.numel(), _stream(x))
+    return out
+
+
+def lora_add(y, x, a, b, adapter, scale=None, ranks=None, sections=None, out=None, workspace=None):
+    """y + D beside a product y float32 [m][n] of any format (out may be y itself); D, x
+    float32 [m][k] and the adapters as for q8_linear_lora."""
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        raise ValueError("y must be an [m][n] tensor")
+    n = y.shape[1]
+    return _lora_beside(lib.lora_add, y, n, n, x, a, b, adapter, scale, ranks, sections, out, workspace)
+
+
+def lora_gate_up_silu(gu, x, a, b, adapter, scale=None, ranks=None, sections=None, out=None, workspace=None):
+    """SiLU(g) * u with [g u] = gu + D beside a fused gate_up product gu float32 [m][2f] of
+    any format; the adapters as for q8_linear_lora with n = 2f."""
+    if not isinstance(gu, torch.Tensor) or gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu must be an [m][2f] tensor")
+    n = gu.shape[1]
+    return _lora_beside(lib.lora_gate_up_silu, gu, n, n // 2, x, a, b, adapter, scale, ranks, sections, out,
+                        workspace)
+
+
+# ------------------------------------------------- the whole mixture-of-experts layer
+
+
+def q8_moe_layer_workspace_bytes(m: int, k: int, n_exp: int, f: int, h: int) -> int:
+    return int(lib.q8_moe_layer_workspace_bytes(m, k, n_exp, f, h))
+
+
+def q8_moe_layer(w_router, w_gate_up_exps, w_down_exps, n_exp: int, f: int, h: int, x, k: int,
+                 normalize: bool = True, top_p=None, out=None, workspace=None):
+    """The whole MoE layer: softmax top-k routing of x [m][h] (moe_route_topk) and the
+    chosen experts' SwiGLU mixture (q8_moe_grouped_linear); returns y float32 [m][h]."""
+    _dev(x, torch.float32, "x")
+    dev = x.device
+    m = _rows_in(x, h, "x")
+    _contig_out(w_router, (n_exp, h), "w_router", torch.float32, dev)
+    _bytes(w_gate_up_exps, _quant_bytes(n_exp * 2 * f, h, Q8_0_BYTES) if m else 0, "w_gate_up_exps", dev)
+    _bytes(w_down_exps, _quant_bytes(n_exp * h, f, Q8_0_BYTES) if m else 0, "w_down_exps", dev)
+    if out is None:
+        out = torch.empty((m, h), dtype=torch.float32, device=dev)
+    _rows_out(out, m, h, "out", torch.float32, dev)
+    workspace = _workspace(workspace, q8_moe_layer_workspace_bytes(m, k, n_exp, f, h), dev)
+    _call(dev, lib.q8_moe_layer, w_router.data_ptr(), w_gate_up_exps.data_ptr(), w_down_exps.data_ptr(), n_exp, f, h,
+          x.data_ptr(), m, _ld(x, h), k, 1 if normalize else 0, 1.0 if top_p is None else float(top_p),
+          out.data_ptr(), _ld(out, h), workspace.data_ptr(), workspace.numel(), _stream(x))
     return out
 
 

@@ -27,7 +27,7 @@ q8_status device_fail(const char* where, hipError_t e) {
 }
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kPrefillRows = 256;  // from this many activation rows on: bf16 matrix-core path
+using q8v::kPrefillRows;  // from this many activation rows on: bf16 matrix-core path
 std::mutex g_dev_mu;
 q8k::DeviceInfo g_dev[kMaxDevices];
 
@@ -381,6 +381,134 @@ q8_status q8_moe_grouped_linear_noalloc(const void* w_gate_up_exps, const void* 
                                 static_cast<const uint8_t*>(w_down_exps), n_exp, f, h, x, m, ldx, topk_idx, topk_w, k,
                                 y, ldy, ws, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return device_fail("q8_moe_grouped_linear_noalloc", e);
+    return Q8_OK;
+}
+
+size_t lora_workspace_bytes(int64_t m, const q8_lora* lora) {
+    if (!lora || m < 0 || q8v::check_lora_rows(m, nullptr, 0) != Q8_OK || !q8v::lora_sizes_valid(*lora)) return 0;
+    return q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, 0).total;
+}
+
+static q8_status lora_add_common(const char* name, const float* y, int64_t n_in, int64_t ldy, bool silu,
+                                 const float* x, int64_t m, int64_t k, int64_t ldx, const q8_lora* lora, float* out,
+                                 int64_t n_out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    q8_status s = q8v::check_lora_add(y, n_in, ldy, x, m, k, ldx, lora, out, n_out, ldo, msg, sizeof msg);
+    if (s == Q8_OK && m > 0 && n_in > 0)
+        s = q8v::check_workspace(q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, 0).total, workspace,
+                                 workspace_bytes, msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("%s: %s", name, msg);
+        return s;
+    }
+    if (m == 0 || n_in == 0) return Q8_OK;
+    q8k::DeviceInfo dev;
+    hipError_t e = q8k::current_device_info(&dev);
+    if (e != hipSuccess) return device_fail(name, e);
+    e = q8k::launch_lora_add(dev, y, n_in, ldy, silu, x, m, k, ldx, *lora, out, ldo, workspace,
+                             static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return device_fail(name, e);
+    return Q8_OK;
+}
+
+q8_status lora_add(const float* y, int64_t n, int64_t ldy, const float* x, int64_t m, int64_t k, int64_t ldx,
+                   const q8_lora* lora, float* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+    return lora_add_common("lora_add", y, n, ldy, false, x, m, k, ldx, lora, out, n, ldo, workspace, workspace_bytes,
+                           stream);
+}
+
+q8_status lora_gate_up_silu(const float* gu, int64_t f, int64_t ldgu, const float* x, int64_t m, int64_t k,
+                            int64_t ldx, const q8_lora* lora, float* h, int64_t ldh, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    // an f out of range stays out of range when doubled
+    const int64_t n = f > q8v::kMaxDim ? f : 2 * f;
+    return lora_add_common("lora_gate_up_silu", gu, n, ldgu, true, x, m, k, ldx, lora, h, f, ldh, workspace,
+                           workspace_bytes, stream);
+}
+
+size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_lora* lora) {
+    if (!lora || m < 0 || n < 0 || n > q8v::kMaxDim || q8v::check_k("k", k, nullptr, 0) != Q8_OK ||
+        q8v::check_lora_rows(m, nullptr, 0) != Q8_OK || !q8v::lora_sizes_valid(*lora))
+        return 0;
+    return q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n)).total;
+}
+
+static q8_status linear_lora_common(const char* name, const void* w, int64_t n_out, int64_t k, bool silu,
+                                    const float* x, int64_t m, int64_t ldx, const q8_lora* lora, float* y,
+                                    int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    q8_status s = q8v::check_linear(w, n_out, k, x, m, ldx, y, ldy, msg, sizeof msg);
+    const int64_t n = silu && s == Q8_OK ? 2 * n_out : n_out;
+    if (s == Q8_OK) s = q8v::check_dim("n", n, msg, sizeof msg);
+    if (s == Q8_OK) s = q8v::check_lora_rows(m, msg, sizeof msg);
+    if (s == Q8_OK) s = q8v::check_lora(lora, n, m, msg, sizeof msg);
+    if (s == Q8_OK && m > 0 && n_out > 0)
+        s = q8v::check_workspace(
+            q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n)).total, workspace,
+            workspace_bytes, msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("%s: %s", name, msg);
+        return s;
+    }
+    if (m == 0 || n_out == 0) return Q8_OK;
+    q8k::DeviceInfo dev;
+    hipError_t e = q8k::current_device_info(&dev);
+    if (e != hipSuccess) return device_fail(name, e);
+    const uint8_t* wq = static_cast<const uint8_t*>(w);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const q8v::LoraWorkspace L =
+        q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n));
+    float* base = silu ? reinterpret_cast<float*>(static_cast<char*>(workspace) + L.base_off) : y;
+    const int64_t ldb = silu ? n : ldy;
+    e = m >= kPrefillRows ? q8k::launch_gemm_q8_mfma(dev, wq, n, k, false, x, m, ldx, base, ldb, st)
+                          : q8k::launch_gemv_q8(dev, wq, n, k, false, x, m, ldx, base, ldb, st);
+    if (e == hipSuccess)
+        e = q8k::launch_lora_add(dev, base, n, ldb, silu, x, m, k, ldx, *lora, y, ldy, workspace, st);
+    if (e != hipSuccess) return device_fail(name, e);
+    return Q8_OK;
+}
+
+q8_status q8_linear_lora(const void* w_q8, int64_t n, int64_t k, const float* x, int64_t m, int64_t ldx,
+                         const q8_lora* lora, float* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    return linear_lora_common("q8_linear_lora", w_q8, n, k, false, x, m, ldx, lora, y, ldy, workspace,
+                              workspace_bytes, stream);
+}
+
+q8_status q8_linear_fused_gate_up_silu_lora(const void* w_gate_up_q8, int64_t f, int64_t k, const float* x,
+                                            int64_t m, int64_t ldx, const q8_lora* lora, float* h, int64_t ldh,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+    return linear_lora_common("q8_linear_fused_gate_up_silu_lora", w_gate_up_q8, f, k, true, x, m, ldx, lora, h, ldh,
+                              workspace, workspace_bytes, stream);
+}
+
+size_t q8_moe_layer_workspace_bytes(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {
+    if (q8_moe_workspace_bytes(m, k, n_exp, f, h) == 0) return 0;
+    return q8v::moe_layer_workspace_layout(m, k, n_exp, f, h).total;
+}
+
+q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const void* w_down_exps, int64_t n_exp,
+                       int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, int32_t normalize,
+                       float top_p, float* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    q8_status s = q8v::check_moe_layer(w_router, w_gate_up_exps, w_down_exps, n_exp, f, h, x, m, ldx, k, top_p, y, ldy,
+                                       workspace, workspace_bytes, msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("q8_moe_layer: %s", msg);
+        return s;
+    }
+    if (m == 0) return Q8_OK;
+    q8k::DeviceInfo dev;
+    hipError_t e = q8k::current_device_info(&dev);
+    if (e != hipSuccess) return device_fail("q8_moe_layer", e);
+    e = q8k::launch_moe_layer(dev, w_router, static_cast<const uint8_t*>(w_gate_up_exps),
+                              static_cast<const uint8_t*>(w_down_exps), n_exp, f, h, x, m, ldx, k, normalize != 0,
+                              top_p, y, ldy, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return device_fail("q8_moe_layer", e);
     return Q8_OK;
 }
 

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/q8_linear.h"
+
 namespace q8k {
 
 // Per-device facts the launchers size their grids with.
@@ -68,6 +70,23 @@ hipError_t launch_route_topk(const DeviceInfo& dev, const float* x, int64_t m, i
 hipError_t launch_moe_grouped(const DeviceInfo& dev, const uint8_t* wgu, const uint8_t* wdn, int64_t n_exp, int64_t f,
                               int64_t h, const float* x, int64_t m, int64_t ldx, const int32_t* idx, const float* wts,
                               int k, float* y, int64_t ldy, void* workspace, hipStream_t stream);
+
+// Counting sort of n_pairs expert (or adapter) ids idx < n_exp <= 256: offsets [n_exp + 1],
+// sorted positions -> pair, inv pair -> position (-1: id out of range), the ids with pairs
+// and their number (active[n_exp]), and each id's first 128-pair tile.
+hipError_t launch_route_plan(const int32_t* idx, int n_pairs, int n_exp, int32_t* offsets, int32_t* sorted,
+                             int32_t* inv, int32_t* active, int32_t* tile_start, hipStream_t stream);
+
+// Low-rank adapters beside a product y [m][n] that is there (n = 2f with silu_pairs: out is
+// then SiLU(gate) * up [m][f]); workspace laid out by q8v::lora_workspace_layout.
+hipError_t launch_lora_add(const DeviceInfo& dev, const float* y, int64_t n, int64_t ldy, bool silu_pairs,
+                           const float* x, int64_t m, int64_t k, int64_t ldx, const q8_lora& lora, float* out,
+                           int64_t ldo, void* workspace, hipStream_t stream);
+
+// The whole mixture-of-experts layer; workspace laid out by q8v::moe_layer_workspace_layout.
+hipError_t launch_moe_layer(const DeviceInfo& dev, const float* w_router, const uint8_t* wgu, const uint8_t* wdn,
+                            int64_t n_exp, int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int k,
+                            bool normalize, float top_p, float* y, int64_t ldy, void* workspace, hipStream_t stream);
 
 // Measurement aids (include/q8_probe.h): a plain streaming read of `bytes` (a multiple
 // of 4096) in launch shape `shape`, one xor word per lane into sink; an empty launch.

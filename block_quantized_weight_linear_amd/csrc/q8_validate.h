@@ -195,4 +195,132 @@ inline q8_status check_moe(const void* wgu, const void* wdn, int64_t n_exp, int6
     return Q8_OK;
 }
 
+// ------------------------------------------------------------- low-rank adapters
+
+constexpr int32_t kLoraMaxAdapters = 256;  // the row sort's bins are the route plan's
+constexpr int32_t kLoraMaxRank = 256;
+
+// The adapter stack beside a matrix of n rows and width k, for m rows of x.
+inline q8_status check_lora(const q8_lora* lo, int64_t n, int64_t m, char* msg, size_t cap) {
+    if (!lo) return fail(msg, cap, Q8_ERR_NULL, "lora is NULL");
+    if (lo->type < Q8_LORA_F32 || lo->type > Q8_LORA_BF16) return fail(msg, cap, Q8_ERR_SHAPE, "lora type=%lld is none of Q8_LORA_*", lo->type);
+    if (lo->n_adapters < 0 || lo->n_adapters > kLoraMaxAdapters)
+        return fail(msg, cap, Q8_ERR_SHAPE, "n_adapters=%lld out of range [0, 256]", lo->n_adapters);
+    if (lo->rank < 8 || lo->rank > kLoraMaxRank || lo->rank % 8 != 0)
+        return fail(msg, cap, Q8_ERR_SHAPE, "rank=%lld must be a multiple of 8 in [8, 256]", lo->rank);
+    if (lo->n_sections < 1 || lo->n_sections > Q8_LORA_MAX_SECTIONS)
+        return fail(msg, cap, Q8_ERR_SHAPE, "n_sections=%lld out of range [1, 4]", lo->n_sections);
+    int64_t sum = 0;
+    for (int s = 0; s < lo->n_sections; ++s) {
+        if (lo->section_rows[s] < 0 || lo->section_rows[s] > n)
+            return fail(msg, cap, Q8_ERR_SHAPE, "a section has %lld rows of %lld", lo->section_rows[s], n);
+        sum += lo->section_rows[s];
+    }
+    if (sum != n) return fail(msg, cap, Q8_ERR_SHAPE, "the sections have %lld rows, the matrix %lld", sum, n);
+    if (m == 0 || n == 0 || lo->n_adapters == 0) return Q8_OK;
+    if (!lo->a || !lo->b || !lo->adapter) return fail(msg, cap, Q8_ERR_NULL, "null pointer (lora a, b or adapter)");
+    if (!aligned(lo->a, 16) || !aligned(lo->b, 16)) return fail(msg, cap, Q8_ERR_ALIGN, "lora a or b not 16-byte aligned");
+    if (!aligned(lo->adapter, 4) || !aligned(lo->ranks, 4) || !aligned(lo->scale, 4))
+        return fail(msg, cap, Q8_ERR_ALIGN, "lora adapter, ranks or scale not 4-byte aligned");
+    return Q8_OK;
+}
+
+// What the workspace sizes depend on.
+inline bool lora_sizes_valid(const q8_lora& lo) {
+    return lo.rank >= 8 && lo.rank <= kLoraMaxRank && lo.rank % 8 == 0 && lo.n_sections >= 1 &&
+           lo.n_sections <= Q8_LORA_MAX_SECTIONS;
+}
+
+// Rows up to which the packed adapter calls keep float32 accuracy; from here on their
+// shared product is q8_linear's, on the bf16 matrix cores.
+constexpr int64_t kPrefillRows = 256;
+
+// Workspace of the adapter calls: the inner products u [m][n_sections * rank], the rows
+// sorted by adapter; the packed calls add what their shared product needs.
+struct LoraWorkspace {
+    size_t u_off, offsets_off, sorted_off, inv_off, active_off, tiles_off, base_off, total;
+};
+
+inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_t rank, size_t base_bytes) {
+    LoraWorkspace w{};
+    const size_t ints = sizeof(int32_t) * size_t(kLoraMaxAdapters + 1);
+    size_t off = 0;
+    w.u_off = off;       off = round_up(off + sizeof(float) * size_t(m) * size_t(n_sections) * size_t(rank), 256);
+    w.offsets_off = off; off = round_up(off + ints, 256);
+    w.sorted_off = off;  off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+    w.inv_off = off;     off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+    w.active_off = off;  off = round_up(off + ints, 256);
+    w.tiles_off = off;   off = round_up(off + ints, 256);
+    w.base_off = off;    off = round_up(off + base_bytes, 256);
+    w.total = off;
+    return w;
+}
+
+inline size_t lora_base_bytes(int64_t m, int64_t n) { return sizeof(float) * size_t(m) * size_t(n); }
+
+inline q8_status check_workspace(size_t need, const void* ws, size_t ws_bytes, char* msg, size_t cap) {
+    if (!ws) return fail(msg, cap, Q8_ERR_WORKSPACE, "workspace is NULL");
+    if (ws_bytes < need) return fail(msg, cap, Q8_ERR_WORKSPACE, "workspace %lld bytes < required %lld", (long long)ws_bytes, (long long)need);
+    if (!aligned(ws, 256)) return fail(msg, cap, Q8_ERR_ALIGN, "workspace not 256-byte aligned");
+    return Q8_OK;
+}
+
+// Sizes the row sort and the grids of the adapter calls take.
+inline q8_status check_lora_rows(int64_t m, char* msg, size_t cap) {
+    if (m > (int64_t(1) << 22)) return fail(msg, cap, Q8_ERR_SHAPE, "m=%lld above 2^22 rows", m);
+    return Q8_OK;
+}
+
+// lora_add (n_out = n, n_in = n) and lora_gate_up_silu (n_out = f, n_in = 2f).
+inline q8_status check_lora_add(const float* y, int64_t n_in, int64_t ldy, const float* x, int64_t m, int64_t k,
+                                int64_t ldx, const q8_lora* lo, const float* out, int64_t n_out, int64_t ldo,
+                                char* msg, size_t cap) {
+    q8_status s;
+    if ((s = check_dim("n", n_in, msg, cap)) != Q8_OK) return s;
+    if ((s = check_dim("m", m, msg, cap)) != Q8_OK) return s;
+    if ((s = check_k("k", k, msg, cap)) != Q8_OK) return s;
+    if ((s = check_lora_rows(m, msg, cap)) != Q8_OK) return s;
+    if (ldx < k || ldx > kMaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "ldx=%lld < k=%lld, or above 2^30", ldx, k);
+    if (ldy < n_in || ldy > 2 * kMaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "leading dimension %lld of the product < %lld, or above 2^31", ldy, n_in);
+    if (ldo < n_out || ldo > kMaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "leading dimension %lld of the output < %lld, or above 2^30", ldo, n_out);
+    if ((s = check_lora(lo, n_in, m, msg, cap)) != Q8_OK) return s;
+    if (m == 0 || n_in == 0) return Q8_OK;
+    if (!y || !x || !out) return fail(msg, cap, Q8_ERR_NULL, "null pointer (the product, x or the output)");
+    if (!aligned(x, 16)) return fail(msg, cap, Q8_ERR_ALIGN, "x pointer not 16-byte aligned");
+    if (ldx % 4 != 0) return fail(msg, cap, Q8_ERR_ALIGN, "ldx=%lld not a multiple of 4", ldx);
+    if (!aligned(y, 4) || !aligned(out, 4)) return fail(msg, cap, Q8_ERR_ALIGN, "the product or the output not 4-byte aligned");
+    return Q8_OK;
+}
+
+// ----------------------------------------------------- the whole mixture-of-experts layer
+
+// Workspace of q8_moe_layer: logits, the routing and the mixture's own.
+struct MoeLayerWorkspace {
+    size_t logits_off, idx_off, w_off, moe_off, total;
+};
+
+inline MoeLayerWorkspace moe_layer_workspace_layout(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {
+    MoeLayerWorkspace w{};
+    size_t off = 0;
+    w.logits_off = off; off = round_up(off + route_workspace_bytes(m, n_exp), 256);
+    w.idx_off = off;    off = round_up(off + sizeof(int32_t) * size_t(m) * size_t(k), 256);
+    w.w_off = off;      off = round_up(off + sizeof(float) * size_t(m) * size_t(k), 256);
+    w.moe_off = off;    off += moe_workspace_layout(m, k, n_exp, f, h).total;
+    w.total = off;
+    return w;
+}
+
+inline q8_status check_moe_layer(const float* wr, const void* wgu, const void* wdn, int64_t n_exp, int64_t f,
+                                 int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, float top_p,
+                                 const float* y, int64_t ldy, const void* ws, size_t ws_bytes, char* msg, size_t cap) {
+    // the routing lives in the workspace: x stands for its pointers in the mixture's checks
+    q8_status s = check_moe_args(wgu, wdn, n_exp, f, h, x, m, ldx, reinterpret_cast<const int32_t*>(x), x, k, y, ldy, msg, cap);
+    if (s != Q8_OK) return s;
+    if (!(top_p > 0.0f && top_p <= 1.0f)) return fail(msg, cap, Q8_ERR_SHAPE, "top_p must be in (0, 1]");
+    if (m == 0) return Q8_OK;
+    if (!wr) return fail(msg, cap, Q8_ERR_NULL, "w_router is NULL");
+    if (!aligned(wr, 16)) return fail(msg, cap, Q8_ERR_ALIGN, "w_router not 16-byte aligned");
+    return check_workspace(moe_layer_workspace_layout(m, k, n_exp, f, h).total, ws, ws_bytes, msg, cap);
+}
+
 }  // namespace q8v

@@ -322,6 +322,110 @@ q8_status q8_moe_grouped_linear_noalloc(const void* w_gate_up_exps, const void* 
                                         const int32_t* topk_idx, const float* topk_w, int32_t k,
                                         float* y, int64_t ldy, void* stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared packed projection.  Every
+ * activation row t may name one adapter a = adapter[t] of a stack; its correction
+ *   D[t][i] = scale[a] * sum_{j < r_a} B[a][i][j] * (sum_c A[a][s(i) * rank + j][c] x[t][c])
+ * is added to output i of the shared product.  A fused matrix (q/k/v, gate/up) keeps the
+ * adapters of its parts apart: its rows are n_sections consecutive sections, and row i
+ * uses the `rank` rows of A that belong to its section s(i).
+ *   a            : [n_adapters][n_sections * rank][k], b : [n_adapters][n][rank], both of
+ *                  element type `type`, contiguous, 16-byte aligned
+ *   n_adapters   : 0 .. 256 (0: no row is corrected; a and b may then be NULL)
+ *   rank         : a multiple of 8 in 8 .. 256 (the stack's padded rank)
+ *   n_sections   : 1 .. 4, section_rows[0 .. n_sections) their sizes (>= 0), summing to n
+ *                  (the gate_up calls: to 2f)
+ *   ranks        : int32 [n_adapters] device, each adapter's own rank r_a, taken as clamped
+ *                  to 0 .. rank; entries of A and B at or past it are not used (they may
+ *                  hold anything).  NULL: rank for all.
+ *   scale        : float32 [n_adapters] device; NULL: 1 for all
+ *   adapter      : int32 [m] device; an entry outside 0 .. n_adapters - 1 (-1 by custom)
+ *                  leaves its row without a correction
+ * The struct is read during the call only.  Types: A and B elements are widened to
+ * float32 exactly; both products accumulate in float32.
+ */
+typedef enum q8_lora_type { Q8_LORA_F32 = 0, Q8_LORA_F16 = 1, Q8_LORA_BF16 = 2 } q8_lora_type;
+#define Q8_LORA_MAX_SECTIONS 4
+typedef struct q8_lora {
+    const void* a;
+    const void* b;
+    const int32_t* ranks;
+    const float* scale;
+    const int32_t* adapter;
+    int64_t section_rows[Q8_LORA_MAX_SECTIONS];
+    int32_t type; /* q8_lora_type */
+    int32_t n_adapters;
+    int32_t rank;
+    int32_t n_sections;
+} q8_lora;
+
+/* Workspace bytes of the two packed calls below for m rows and a matrix of n rows (the
+ * gate_up call: n = 2f); 0 on invalid sizes.  Of lora, only rank and n_sections count. */
+size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_lora* lora);
+
+/*
+ * The packed linears with adapters:
+ *   q8_linear_lora                    : y = x . W^T + D,  W = Q8_0 [n][k]
+ *   q8_linear_fused_gate_up_silu_lora : h = SiLU(g) * u with [g u] = x . W^T + D, W = Q8_0 [2f][k]
+ * Arguments and errors as for q8_linear / q8_linear_fused_gate_up_silu;
+ *   workspace : device memory of at least q8_linear_lora_workspace_bytes(...) bytes,
+ *               256-byte aligned; its contents on entry do not matter.  Calls that can
+ *               overlap (other streams, or captured graphs replayed side by side) need
+ *               workspaces of their own.
+ * A row of x that holds a NaN or an infinity gives outputs that are not finite; other rows
+ * are not touched by it.  Below 256 rows the arithmetic is of float32 accuracy; from 256
+ * rows on the shared product takes the bf16 matrix-core tiles of q8_linear, the
+ * correction stays in float32.
+ */
+q8_status q8_linear_lora(const void* w_q8, int64_t n, int64_t k, const float* x, int64_t m, int64_t ldx,
+                         const q8_lora* lora, float* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                         void* stream);
+q8_status q8_linear_fused_gate_up_silu_lora(const void* w_gate_up_q8, int64_t f, int64_t k, const float* x,
+                                            int64_t m, int64_t ldx, const q8_lora* lora, float* h, int64_t ldh,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_add and lora_gate_up_silu for m rows (0 on invalid sizes). */
+size_t lora_workspace_bytes(int64_t m, const q8_lora* lora);
+
+/*
+ * The adapters alone, beside a shared product of any format that has been computed:
+ *   lora_add          : out[t][i] = y[t][i] + D[t][i],  i < n
+ *   lora_gate_up_silu : h[t][j] = SiLU(g) * u with g = gu[t][j] + D[t][j], u = gu[t][f + j] + D[t][f + j], j < f
+ *   y  : float32 [m][ldy], gu : float32 [m][ldgu] (ldgu >= 2f), 4-byte aligned
+ *   x  : float32 [m][ldx], the projection's input (rules as for q8_linear)
+ *   out may be y itself (same pointer and leading dimension); otherwise the outputs must
+ *   not overlap the inputs.
+ *   workspace : at least lora_workspace_bytes(m, lora) bytes, rules as above.
+ * Float32 accuracy at any m.
+ */
+q8_status lora_add(const float* y, int64_t n, int64_t ldy, const float* x, int64_t m, int64_t k, int64_t ldx,
+                   const q8_lora* lora, float* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                   void* stream);
+q8_status lora_gate_up_silu(const float* gu, int64_t f, int64_t ldgu, const float* x, int64_t m, int64_t k,
+                            int64_t ldx, const q8_lora* lora, float* h, int64_t ldh, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes q8_moe_layer needs for these sizes (0 on invalid sizes). */
+size_t q8_moe_layer_workspace_bytes(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h);
+
+/*
+ * The whole mixture-of-experts layer: softmax top-k routing of x (as moe_route_topk_top_p:
+ * the same experts, order and weights) followed by the expert mixture (as
+ * q8_moe_grouped_linear) of the chosen experts.
+ *   w_router, k, normalize, top_p : as for moe_route_topk_top_p (top_p = 1: plain top-k)
+ *   w_gate_up_exps, w_down_exps, n_exp, f, h, x, m, ldx, y, ldy : as for q8_moe_grouped_linear
+ *   workspace : device memory of at least q8_moe_layer_workspace_bytes(m, k, n_exp, f, h)
+ *               bytes, 256-byte aligned; its contents on entry do not matter.  Calls that
+ *               can overlap need workspaces of their own.
+ * A token whose router probabilities are not finite (a NaN or an infinity in its row)
+ * gets NaN in every output; other tokens are not touched by it.  Below 8 routed pairs per
+ * expert on average (m * k < 8 * n_exp) the results are of float32 accuracy; from there on
+ * the expert products run on the bf16 tiles of q8_moe_grouped_linear.
+ */
+q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const void* w_down_exps, int64_t n_exp,
+                       int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, int32_t normalize,
+                       float top_p, float* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
