@@ -432,7 +432,7 @@ size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_
     if (!lora || m < 0 || n < 0 || n > q8v::kMaxDim || q8v::check_k("k", k, nullptr, 0) != Q8_OK ||
         q8v::check_lora_rows(m, nullptr, 0) != Q8_OK || !q8v::lora_sizes_valid(*lora))
         return 0;
-    return q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n)).total;
+    return q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n, k)).total;
 }
 
 static q8_status linear_lora_common(const char* name, const void* w, int64_t n_out, int64_t k, bool silu,
@@ -447,7 +447,7 @@ static q8_status linear_lora_common(const char* name, const void* w, int64_t n_o
     if (s == Q8_OK) s = q8v::check_lora(lora, n, m, msg, sizeof msg);
     if (s == Q8_OK && m > 0 && n_out > 0)
         s = q8v::check_workspace(
-            q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n)).total, workspace,
+            q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n, k)).total, workspace,
             workspace_bytes, msg, sizeof msg);
     if (s != Q8_OK) {
         set_err("%s: %s", name, msg);
@@ -459,14 +459,7 @@ static q8_status linear_lora_common(const char* name, const void* w, int64_t n_o
     if (e != hipSuccess) return device_fail(name, e);
     const uint8_t* wq = static_cast<const uint8_t*>(w);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const q8v::LoraWorkspace L =
-        q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n));
-    float* base = silu ? reinterpret_cast<float*>(static_cast<char*>(workspace) + L.base_off) : y;
-    const int64_t ldb = silu ? n : ldy;
-    e = m >= kPrefillRows ? q8k::launch_gemm_q8_mfma(dev, wq, n, k, false, x, m, ldx, base, ldb, st)
-                          : q8k::launch_gemv_q8(dev, wq, n, k, false, x, m, ldx, base, ldb, st);
-    if (e == hipSuccess)
-        e = q8k::launch_lora_add(dev, base, n, ldb, silu, x, m, k, ldx, *lora, y, ldy, workspace, st);
+    e = q8k::launch_linear_lora(dev, wq, n_out, k, silu, x, m, ldx, *lora, y, ldy, workspace, st);
     if (e != hipSuccess) return device_fail(name, e);
     return Q8_OK;
 }

@@ -83,6 +83,12 @@ hipError_t launch_lora_add(const DeviceInfo& dev, const float* y, int64_t n, int
                            const float* x, int64_t m, int64_t k, int64_t ldx, const q8_lora& lora, float* out,
                            int64_t ldo, void* workspace, hipStream_t stream);
 
+// The packed linears with adapters; workspace laid out by q8v::lora_workspace_layout with
+// q8v::lora_base_bytes.
+hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu,
+                              const float* x, int64_t m, int64_t ldx, const q8_lora& lora, float* y, int64_t ldy,
+                              void* workspace, hipStream_t stream);
+
 // The whole mixture-of-experts layer; workspace laid out by q8v::moe_layer_workspace_layout.
 hipError_t launch_moe_layer(const DeviceInfo& dev, const float* w_router, const uint8_t* wgu, const uint8_t* wdn,
                             int64_t n_exp, int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int k,

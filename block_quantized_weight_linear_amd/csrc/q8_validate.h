@@ -256,7 +256,19 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
     return w;
 }
 
-inline size_t lora_base_bytes(int64_t m, int64_t n) { return sizeof(float) * size_t(m) * size_t(n); }
+// The packed calls run on the digit tiles (digit_tiles.h) below the prefill rows, for widths
+// whose digits fit a block's registers and fused matrices whose up rows lie within 32-bit
+// byte offsets of their gate rows; else on q8_linear's kernels and the correction behind them.
+constexpr int64_t kLoraTilesMaxK = 16384;
+inline bool lora_uses_tiles(int64_t m, int64_t n, int64_t k) {
+    return m < kPrefillRows && k <= kLoraTilesMaxK && n * row_bytes(k) < (int64_t(1) << 31);
+}
+
+// Workspace behind the adapters': the rows' exponents and digits, or the shared product.
+inline size_t lora_base_bytes(int64_t m, int64_t n, int64_t k) {
+    if (lora_uses_tiles(m, n, k)) return sizeof(int32_t) * size_t(kPrefillRows) + 4 * size_t(m) * size_t(k);
+    return sizeof(float) * size_t(m) * size_t(n);
+}
 
 inline q8_status check_workspace(size_t need, const void* ws, size_t ws_bytes, char* msg, size_t cap) {
     if (!ws) return fail(msg, cap, Q8_ERR_WORKSPACE, "workspace is NULL");
