@@ -60,31 +60,69 @@ __host__ __device__ inline SliceShare slice_share(int S) {
     return best;
 }
 
-// One item into lds .. lds + 4351: four copies of 16 bytes a lane and one of 4 from base (an
-// SGPR pair) + off[c], five vmcnt events, with the non-temporal hint (weights are read once).
+// One item into lds .. lds + 4351: four copies of 16 bytes a lane and one of 4 from base +
+// off[c] (base wave-uniform), five vmcnt events, with the non-temporal hint (weights are
+// read once).  The compiler counts these loads, so the digits loaded before them are waited
+// for without waiting for the copies; nothing it can see reads LDS until the run's end
+// (read_item, read_sums and write_sum are inline assembly), or it would drain the copies.
+typedef __attribute__((address_space(1))) const uint8_t GlobalBytes;
+typedef __attribute__((address_space(3))) uint8_t LdsBytes;
 __device__ __forceinline__ void copy_item(const uint8_t* base, const uint32_t (&off)[5], uint32_t lds) {
-    uint32_t saved;
+    constexpr int kNonTemporal = 2;
+    GlobalBytes* g = (GlobalBytes*)base;
+    LdsBytes* l = (LdsBytes*)lds;
+    __builtin_amdgcn_global_load_lds(g + off[0], l, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[1], l + 1024, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[2], l + 2048, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[3], l + 3072, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[4], l + 4096, 4, 0, kNonTemporal);
+}
+
+// A lane's share of an item: of each block pair q the dwords holding the lane's quants of its
+// first block (e, f: 12 bytes, shifted by two), of its second (o) and both scales (s: low half
+// of the first dword, high half of the second).  row: the lane's weight row, mine: row + 8 *
+// (lane >> 4).  Done when it returns.
+struct ItemWords {
+    uint64_t e[4], o[4], s[4], f[2];
+};
+__device__ __forceinline__ void read_item(uint32_t row, uint32_t mine, ItemWords& v) {
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %7\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, %6 nt\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %2, %6 nt\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %3, %6 nt\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %4, %6 nt\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dword %5, %6 nt\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "v"(off[4]), "s"(base), "s"(lds)
-        : "memory", "scc");
+        "ds_read2_b32 %0, %14 offset0:0 offset1:1\n\t"
+        "ds_read2_b32 %1, %14 offset0:17 offset1:18\n\t"
+        "ds_read2_b32 %2, %14 offset0:34 offset1:35\n\t"
+        "ds_read2_b32 %3, %14 offset0:51 offset1:52\n\t"
+        "ds_read2_b32 %4, %14 offset0:9 offset1:10\n\t"
+        "ds_read2_b32 %5, %14 offset0:26 offset1:27\n\t"
+        "ds_read2_b32 %6, %14 offset0:43 offset1:44\n\t"
+        "ds_read2_b32 %7, %14 offset0:60 offset1:61\n\t"
+        "ds_read2_b32 %8, %15 offset0:0 offset1:8\n\t"
+        "ds_read2_b32 %9, %15 offset0:17 offset1:25\n\t"
+        "ds_read2_b32 %10, %15 offset0:34 offset1:42\n\t"
+        "ds_read2_b32 %11, %15 offset0:51 offset1:59\n\t"
+        "ds_read2_b32 %12, %14 offset0:2 offset1:19\n\t"
+        "ds_read2_b32 %13, %14 offset0:36 offset1:53\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v.e[0]), "=&v"(v.e[1]), "=&v"(v.e[2]), "=&v"(v.e[3]), "=&v"(v.o[0]), "=&v"(v.o[1]), "=&v"(v.o[2]),
+          "=&v"(v.o[3]), "=&v"(v.s[0]), "=&v"(v.s[1]), "=&v"(v.s[2]), "=&v"(v.s[3]), "=&v"(v.f[0]), "=&v"(v.f[1])
+        : "v"(mine), "v"(row)
+        : "memory");
+}
+__device__ __forceinline__ void write_sum(uint32_t lds, float v) {
+    asm volatile("ds_write_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(lds), "v"(v) : "memory");
+}
+// The sum of n floats at lds, lds + stride, ... in order.
+__device__ __forceinline__ float read_sums(uint32_t lds, int n, uint32_t stride) {
+    float s = 0.0f;
+    for (int w = 0; w < n; w += 2, lds += 2 * stride) {  // n: 2, 4 or 8
+        float a, b;
+        asm volatile("ds_read_b32 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b)
+                     : "v"(lds), "v"(lds + stride)
+                     : "memory");
+        s += a;
+        s += b;
+    }
+    return s;
 }
 
 template <class F, int... I>
@@ -96,8 +134,14 @@ __device__ __forceinline__ void unroll(F&& f) {
     unroll_impl(f, std::make_integer_sequence<int, N>{});
 }
 
-// Digits of one activation row, by a block of 256 threads: dig is the row's
-// [k / 32][4 digits][32] bytes, *exp_out the exponent e - 29 of its scale.  A row that holds
+// Where digit d of element i lies in a row's digits: [block pair][digit][8 elements' place
+// in their block][block of the pair][8], so that a lane's bytes of two blocks are 16
+// consecutive ones.
+__host__ __device__ constexpr size_t digit_at(int i, int d) {
+    return (size_t)(i >> 6) * 256 + 64 * d + 16 * ((i >> 3) & 3) + 8 * ((i >> 5) & 1) + (i & 7);
+}
+
+// Digits of one activation row, by a block of 256 threads: dig is the row's 4 k bytes, *exp_out the exponent e - 29 of its scale.  A row that holds
 // a NaN or an infinity gets kNotFinite and zero digits: all its outputs are NaN.
 constexpr int kNotFinite = 1 << 20;
 __device__ __forceinline__ float row_scaled(float sum, int exp) {
@@ -107,16 +151,25 @@ __device__ __forceinline__ int row_exponent(uint32_t max_bits) { return max((int
 __device__ __forceinline__ void write_digits(const float* __restrict__ xr, int k, int8_t* __restrict__ dig,
                                              int* __restrict__ exp_out) {
     __shared__ uint32_t wave_max_bits[4];
+    constexpr int kKeep = 4;  // the first 4096 elements stay in registers, the rest is read twice
     const int tid = threadIdx.x;
+    float4 keep[kKeep];
     uint32_t mx = 0;  // magnitudes as bits: ordered like the values, NaN above infinity
-    for (int i = 4 * tid; i < k; i += 1024) {
-        const float4 v = *reinterpret_cast<const float4*>(xr + i);
+    auto larger = [&](const float4& v) __attribute__((always_inline)) {
         const uint32_t a = __builtin_bit_cast(uint32_t, v.x) & 0x7fffffffu;
         const uint32_t b = __builtin_bit_cast(uint32_t, v.y) & 0x7fffffffu;
         const uint32_t c = __builtin_bit_cast(uint32_t, v.z) & 0x7fffffffu;
         const uint32_t d = __builtin_bit_cast(uint32_t, v.w) & 0x7fffffffu;
         mx = max(max(max(mx, a), b), max(c, d));
+    };
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = 4 * tid + 1024 * j;
+        keep[j] = i < k ? *reinterpret_cast<const float4*>(xr + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) larger(keep[j]);
+    for (int i = 4 * tid + 1024 * kKeep; i < k; i += 1024) larger(*reinterpret_cast<const float4*>(xr + i));
     for (int off = 32; off >= 1; off >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
     if ((tid & 63) == 0) wave_max_bits[tid >> 6] = mx;
     __syncthreads();
@@ -124,8 +177,7 @@ __device__ __forceinline__ void write_digits(const float* __restrict__ xr, int k
     const bool finite = mx < 0x7f800000u;
     const int e = row_exponent(mx);
     if (tid == 0) *exp_out = finite ? e - 29 : kNotFinite;
-    for (int i = 4 * tid; i < k; i += 1024) {
-        const float4 v = *reinterpret_cast<const float4*>(xr + i);
+    auto write = [&](const float4& v, int i) __attribute__((always_inline)) {
         const float f[4] = {v.x, v.y, v.z, v.w};
         uint32_t out[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -140,8 +192,14 @@ __device__ __forceinline__ void write_digits(const float* __restrict__ xr, int k
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-            *reinterpret_cast<uint32_t*>(dig + (size_t)(i >> 5) * 128 + 32 * d + (i & 31)) = out[d];
+            *reinterpret_cast<uint32_t*>(dig + digit_at(i, d)) = out[d];
+    };
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = 4 * tid + 1024 * j;
+        if (i < k) write(keep[j], i);
     }
+    for (int i = 4 * tid + 1024 * kKeep; i < k; i += 1024) write(*reinterpret_cast<const float4*>(xr + i), i);
 }
 
 // What a wave knows about its place: its slices of a row of S, its tiles of a step.
@@ -172,53 +230,51 @@ struct TileWave {
     }
 };
 
-// A operands of the wave's slices for 4 * NG activation rows; digits_of(slot) gives the
-// row's digits (nullptr: no such row, zeros).
+// A operands of the wave's slices for 4 * NG activation rows, a[g][slice][block pair][block];
+// digits_of(slot) gives the digits of the row in a slot (for a slot without one: of any row,
+// its sums are not used).
+typedef long i64x2 __attribute__((ext_vector_type(2)));
 template <int SP, int NG, class DigitsOf>
-__device__ __forceinline__ void load_digits(const TileWave& W, DigitsOf&& digits_of, long (&a)[NG][SP][8]) {
+__device__ __forceinline__ void load_digits(const TileWave& W, DigitsOf&& digits_of, i64x2 (&a)[NG][SP][4]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const int8_t* d = digits_of(4 * g + (W.row >> 2));
+        const int8_t* d = digits_of(4 * g + (W.row >> 2)) + 64 * (W.row & 3) + 16 * W.grp;
 #pragma unroll
         for (int sl = 0; sl < SP; ++sl) {
-            const int s = W.wt + (sl << W.log2_wt);
+            const int s = W.wt + (min(sl, W.n_sl - 1) << W.log2_wt);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[g][sl][j] = 0;
-                if (d && sl < W.n_sl)
-                    a[g][sl][j] = *reinterpret_cast<const long*>(d + (size_t)(8 * s + j) * 128 + 32 * (W.row & 3) +
-                                                                 8 * W.grp);
-            }
+            for (int q = 0; q < 4; ++q) a[g][sl][q] = *reinterpret_cast<const i64x2*>(d + (size_t)(4 * s + q) * 256);
         }
     }
 }
 
-// A run of n_tiles tiles: tile_at(i, base, off) gives tile i's first byte of slice 0
-// (wave-uniform) and the lanes' copy offsets.  Constructing it issues the first copies; a
-// load issued afterwards waits for them too.
+// A run of n_tiles >= 1 tiles: tile_at(i) gives tile i's first byte of slice 0 (wave-uniform),
+// off the lanes' copy offsets from there.  Constructing it issues the first copies: a
+// wait for a load issued afterwards waits for them too, so the digits are loaded before.
 template <class TileAt>
 struct TileRun {
     const TileWave& W;
+    const uint32_t (&off)[5];
     TileAt tile_at;
     int n_tiles, tps, n_items, next_tile, next_sl;
-    __device__ __forceinline__ TileRun(const TileWave& W_, int n, TileAt t) : W(W_), tile_at(t) { restart(n); }
+    __device__ __forceinline__ TileRun(const TileWave& W_, const uint32_t (&off_)[5], int n, TileAt t)
+        : W(W_), off(off_), tile_at(t) {
+        restart(n);
+    }
     __device__ __forceinline__ void restart(int n) {
         n_tiles = n;
         tps = kTileWaves >> W.log2_wt;
         next_tile = W.tg;
         next_sl = 0;
         n_items = (W.tg < n_tiles ? (n_tiles - W.tg + tps - 1) / tps : 0) * W.n_sl;
-        unroll<kRing>([&](auto sc) __attribute__((always_inline)) {
-            constexpr int s = decltype(sc)::value;
-            if (s < n_items) issue(s);
-        });
+        // always kRing items (past the last one: it again), so that the compiler knows how
+        // many copies are younger than the digits
+        unroll<kRing>([&](auto sc) __attribute__((always_inline)) { issue(decltype(sc)::value); });
+        wait_vmcnt<5 * kRing>();
     }
     __device__ __forceinline__ void issue(int slot) {
-        const uint8_t* base;
-        uint32_t off[5];
-        tile_at(next_tile, base, off);
-        base += (size_t)(W.wt + (next_sl << W.log2_wt)) * kSliceBytes;
-        copy_item(base, off, W.ring_lds + slot * kLdsItemBytes);
+        const uint8_t* tile = tile_at(min(next_tile, n_tiles - 1));
+        copy_item(tile + (size_t)(W.wt + (next_sl << W.log2_wt)) * kSliceBytes, off, W.ring_lds + slot * kLdsItemBytes);
         if (++next_sl == W.n_sl) {
             next_sl = 0;
             next_tile += tps;
@@ -231,10 +287,12 @@ struct TileRun {
 // 2 * kTileWaves * NG * 64 floats.  Every wave of the block calls it; after a barrier by
 // the caller the sums are there.
 template <int SP, int NG, class Run>
-__device__ __forceinline__ void multiply_tiles(Run& R, const long (&a)[NG][SP][8], float* part, float* sums) {
+__device__ __forceinline__ void multiply_tiles(Run& R, const i64x2 (&a)[NG][SP][4], float* part, float* sums) {
     const TileWave& W = R.W;
     const int n_tiles = R.n_tiles, tps = R.tps, n_items = R.n_items;
     const int steps = (n_tiles + tps - 1) / tps;
+    const uint32_t part_lds = (uint32_t)(uintptr_t)part + 4 * W.lane;
+    const uint32_t sums_lds = (uint32_t)(uintptr_t)sums + 4 * W.lane;
     int it = 0, slot = 0;
     for (int step = 0; step < steps; ++step) {
         float acc[NG];
@@ -245,7 +303,8 @@ __device__ __forceinline__ void multiply_tiles(Run& R, const long (&a)[NG][SP][8
             unroll<SP>([&](auto slc) __attribute__((always_inline)) {
                 constexpr int sl = decltype(slc)::value;
                 if (sl < W.n_sl) {
-                    const int rem = n_items - 1 - it;
+                    // the item is the oldest of min(kRing, items issued and not read) in flight
+                    const int rem = max(n_items, kRing) - 1 - it;
                     if (rem >= kRing - 1) {
                         wait_vmcnt_mem<(kRing - 1) * 5>();
                     } else {
@@ -254,34 +313,24 @@ __device__ __forceinline__ void multiply_tiles(Run& R, const long (&a)[NG][SP][8
                             if (rem == k) wait_vmcnt_mem<k * 5>();
                         });
                     }
-                    const uint32_t* p =
-                        reinterpret_cast<const uint32_t*>(W.ring + slot * kLdsItemBytes) + 68 * W.row + 2 * W.grp;
-                    const uint32_t* ps = p - 2 * W.grp;
-                    uint32_t v[4][7];
+                    ItemWords v;
+                    const uint32_t row = W.ring_lds + slot * kLdsItemBytes + kSliceBytes * W.row;
+                    read_item(row, row + 8 * W.grp, v);
+                    if (it + kRing < n_items) R.issue(slot);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        v[q][0] = p[17 * q];
-                        v[q][1] = p[17 * q + 1];
-                        v[q][2] = p[17 * q + 2];
-                        v[q][3] = p[17 * q + 9];
-                        v[q][4] = p[17 * q + 10];
-                        v[q][5] = ps[17 * q];
-                        v[q][6] = ps[17 * q + 8];
-                    }
-                    wait_lgkmcnt_mem<0>();
-                    if (rem >= kRing) R.issue(slot);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t b00 = __builtin_amdgcn_alignbyte(v[q][1], v[q][0], 2);
-                        const uint32_t b01 = __builtin_amdgcn_alignbyte(v[q][2], v[q][1], 2);
+                        const uint32_t e1 = (uint32_t)(v.e[q] >> 32);
+                        const uint32_t e2 = (uint32_t)(q & 1 ? v.f[q / 2] >> 32 : v.f[q / 2]);
+                        const uint32_t b00 = __builtin_amdgcn_alignbyte(e1, (uint32_t)v.e[q], 2);
+                        const uint32_t b01 = __builtin_amdgcn_alignbyte(e2, e1, 2);
                         const long b0 = (long)(((uint64_t)b01 << 32) | b00);
-                        const long b1 = (long)(((uint64_t)v[q][4] << 32) | v[q][3]);
-                        const float d0 = half_lo(v[q][5]), d1 = half_hi(v[q][6]);
+                        const long b1 = (long)v.o[q];
+                        const float d0 = half_lo((uint32_t)v.s[q]), d1 = half_hi((uint32_t)(v.s[q] >> 32));
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             const i32x4 z = {0, 0, 0, 0};
-                            const i32x4 s0 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[g][sl][2 * q], b0, z, 0, 0, 0);
-                            const i32x4 s1 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[g][sl][2 * q + 1], b1, z, 0, 0, 0);
+                            const i32x4 s0 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[g][sl][q][0], b0, z, 0, 0, 0);
+                            const i32x4 s1 = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[g][sl][q][1], b1, z, 0, 0, 0);
                             const float t0 = __builtin_fmaf((float)(s0[3] * 256 + s0[2]), 65536.0f,
                                                             (float)(s0[1] * 256 + s0[0]));
                             acc[g] = __builtin_fmaf(d0, t0, acc[g]);
@@ -301,28 +350,25 @@ __device__ __forceinline__ void multiply_tiles(Run& R, const long (&a)[NG][SP][8
         if (W.log2_wt == 0) {  // one wave a tile: nothing to add
             if (tile < n_tiles) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) sums[(tile * NG + g) * 64 + W.lane] = acc[g];
+                for (int g = 0; g < NG; ++g) write_sum(sums_lds + 256 * (tile * NG + g), acc[g]);
             }
             continue;
         }
-        float* mine = part + ((step & 1) * kTileWaves + W.wv) * (NG * 64) + W.lane;
+        const uint32_t buf = part_lds + (step & 1) * (kTileWaves * NG * 256);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) mine[64 * g] = acc[g];
-        wait_lgkmcnt_mem<0>();
+        for (int g = 0; g < NG; ++g) write_sum(buf + 256 * (W.wv * NG + g), acc[g]);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         // tile step * tps + q is added up by wave (step * tps + q) mod 8
         const int q = (W.wv - step * tps) & (kTileWaves - 1);
         if (q < tps && step * tps + q < n_tiles) {
-            const float* from = part + ((step & 1) * kTileWaves + (q << W.log2_wt)) * (NG * 64) + W.lane;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float s = from[64 * g];
-                for (int w = 1; w < (1 << W.log2_wt); ++w) s += from[(w * NG + g) * 64];
-                sums[((step * tps + q) * NG + g) * 64 + W.lane] = s;
-            }
+            for (int g = 0; g < NG; ++g)
+                write_sum(sums_lds + 256 * ((step * tps + q) * NG + g),
+                          read_sums(buf + 256 * ((q << W.log2_wt) * NG + g), 1 << W.log2_wt, 256 * NG));
         }
     }
+    wait_vmcnt_mem<0>();  // copies past the last item
 }
 
 }  // namespace q8k

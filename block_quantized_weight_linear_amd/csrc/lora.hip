@@ -23,26 +23,31 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 // Element types of A and B: eight values from a 16-byte aligned address, widened exactly.
 struct LoraF32 {
     using T = float;
-    static __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    struct V {
+        float4 lo, hi;
+    };
+    static __device__ __forceinline__ V load8(const T* p) {
+        return V{*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
+    }
+    static __device__ __forceinline__ float at(const V& v, int q) {
+        const float4& h = q < 4 ? v.lo : v.hi;
+        return (q & 3) == 0 ? h.x : (q & 3) == 1 ? h.y : (q & 3) == 2 ? h.z : h.w;
     }
 };
 struct LoraF16 {
     using T = uint16_t;
-    static __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-        const u16x8 a = *reinterpret_cast<const u16x8*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)a[i]);
+    using V = u16x8;
+    static __device__ __forceinline__ V load8(const T* p) { return *reinterpret_cast<const u16x8*>(p); }
+    static __device__ __forceinline__ float at(const V& v, int q) {
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)v[q]);
     }
 };
 struct LoraBF16 {
     using T = uint16_t;
-    static __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-        const u16x8 a = *reinterpret_cast<const u16x8*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, (uint32_t)a[i] << 16);
+    using V = u16x8;
+    static __device__ __forceinline__ V load8(const T* p) { return *reinterpret_cast<const u16x8*>(p); }
+    static __device__ __forceinline__ float at(const V& v, int q) {
+        return __builtin_bit_cast(float, (uint32_t)v[q] << 16);
     }
 };
 
@@ -75,39 +80,68 @@ struct LoraArgs {
     }
 };
 
-// The inner products of blocks block, block + blocks, ... of four (one a wave).
+// Four inner products u[t][c0 .. c0+3] by a block of 256 threads, every load of up to 8192
+// elements of the row and the four rows of A issued before the first product.
+constexpr int kShrinkCols = 4;
 template <class Ty>
-__device__ __forceinline__ void lora_shrink(const LoraArgs& lo, const float* __restrict__ x, int m, int k,
-                                            int64_t ldx, float* __restrict__ u, int block, int blocks) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void lora_shrink(const LoraArgs& lo, const float* __restrict__ x, int k, int64_t ldx,
+                                            float* __restrict__ u, int64_t unit) {
+    __shared__ float wave_sums[4][kShrinkCols];
+    const int tid = threadIdx.x;
     const int cols = lo.n_sections * lo.rank;
-    for (int64_t id = (int64_t)block * 4 + (threadIdx.x >> 6); id < (int64_t)m * cols; id += (int64_t)blocks * 4) {
-    const int64_t t = id / cols;
-    const int c = (int)(id - t * cols);
+    const int groups = cols / kShrinkCols;
+    const int64_t t = unit / groups;
+    const int c0 = (int)(unit - t * groups) * kShrinkCols;
     const int a = lo.of_row(t);
-    if (a < 0 || c % lo.rank >= lo.rank_of(a)) {
-        if (lane == 0) u[id] = 0.0f;
-        continue;
+    const int left = a < 0 ? 0 : lo.rank_of(a) - c0 % lo.rank;  // products the adapter has here
+    if (left <= 0) {
+        if (tid < kShrinkCols) u[t * cols + c0 + tid] = 0.0f;
+        return;
     }
-    const typename Ty::T* ar = static_cast<const typename Ty::T*>(lo.a) + ((size_t)a * cols + c) * k;
+    const typename Ty::T* ar = static_cast<const typename Ty::T*>(lo.a) + ((size_t)a * cols + c0) * k;
     const float* xr = x + t * ldx;
-    float acc = 0.0f;
-    for (int i = 8 * lane; i < k; i += 512) {
-        float v[8], w[8];
-        Ty::load8(ar + i, v);
-        LoraF32::load8(xr + i, w);
+    float acc[kShrinkCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = 8 * tid; i0 < k; i0 += 8192) {
+        typename Ty::V v[4][kShrinkCols];
+        LoraF32::V w[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc = __builtin_fmaf(v[q], w[q], acc);
+        for (int s = 0; s < 4; ++s) {
+            const int i = i0 + 2048 * s < k ? i0 + 2048 * s : 8 * tid;  // past the end: not multiplied
+            w[s] = LoraF32::load8(xr + i);
+#pragma unroll
+            for (int c = 0; c < kShrinkCols; ++c) v[s][c] = Ty::load8(ar + (size_t)c * k + i);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (i0 + 2048 * s < k) {
+#pragma unroll
+                for (int c = 0; c < kShrinkCols; ++c)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[c] = __builtin_fmaf(Ty::at(v[s][c], q), LoraF32::at(w[s], q), acc[c]);
+            }
+        }
     }
-    for (int off = 32; off >= 1; off >>= 1) acc += __shfl_xor(acc, off, 64);
-    if (lane == 0) u[id] = acc * (lo.scale ? lo.scale[a] : 1.0f);
+#pragma unroll
+    for (int c = 0; c < kShrinkCols; ++c)
+        for (int off = 32; off >= 1; off >>= 1) acc[c] += __shfl_xor(acc[c], off, 64);
+    if ((tid & 63) == 0)
+#pragma unroll
+        for (int c = 0; c < kShrinkCols; ++c) wave_sums[tid >> 6][c] = acc[c];
+    __syncthreads();
+    if (tid < kShrinkCols) {
+        const float sum = (wave_sums[0][tid] + wave_sums[1][tid]) + (wave_sums[2][tid] + wave_sums[3][tid]);
+        u[t * cols + c0 + tid] = tid < left ? sum * (lo.scale ? lo.scale[a] : 1.0f) : 0.0f;
     }
 }
 
 template <class Ty>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs lo, const float* __restrict__ x, int m, int k,
                                                           int64_t ldx, float* __restrict__ u) {
-    lora_shrink<Ty>(lo, x, m, k, ldx, u, blockIdx.x, gridDim.x);
+    const int64_t units = (int64_t)m * (lo.n_sections * lo.rank / kShrinkCols);
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        lora_shrink<Ty>(lo, x, k, ldx, u, unit);
+        __syncthreads();  // the next unit overwrites the waves' sums
+    }
 }
 
 // First launch of the packed calls: blocks 0 .. m-1 write the rows' digits, the others the
@@ -120,30 +154,39 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(LoraArgs lo, const fl
     if (b < m)
         write_digits(x + b * ldx, k, dig + (size_t)b * k * 4, exps + b);
     else
-        lora_shrink<Ty>(lo, x, m, k, ldx, u, b - m, gridDim.x - m);
+        lora_shrink<Ty>(lo, x, k, ldx, u, b - m);
 }
 
 // sum_j B[a][i][j] u[j] of output row i, u the row's inner products
-template <class Ty>
+template <class Ty, int FLY = 4>
 __device__ __forceinline__ float lora_delta(const LoraArgs& lo, int64_t n, int a, int64_t i, const float* u) {
     const typename Ty::T* br = static_cast<const typename Ty::T*>(lo.b) + ((size_t)a * n + i) * lo.rank;
     const float* us = u + lo.section(i) * lo.rank;
     const int r = lo.rank_of(a);
     float acc = 0.0f;
-    for (int j = 0; j < r; j += 8) {
-        float v[8], w[8];
-        Ty::load8(br + j, v);
-        LoraF32::load8(us + j, w);
+    for (int j0 = 0; j0 < r; j0 += 8 * FLY) {  // 8 FLY of B's row in flight
+        typename Ty::V v[FLY];
+        LoraF32::V w[FLY];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc = j + q < r ? __builtin_fmaf(v[q], w[q], acc) : acc;
+        for (int s = 0; s < FLY; ++s) {
+            const int j = j0 + 8 * s < r ? j0 + 8 * s : j0;
+            v[s] = Ty::load8(br + j);
+            w[s] = LoraF32::load8(us + j);
+        }
+#pragma unroll
+        for (int s = 0; s < FLY; ++s)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc = j0 + 8 * s + q < r ? __builtin_fmaf(Ty::at(v[s], q), LoraF32::at(w[s], q), acc) : acc;
     }
     return acc;
 }
 
+template <int FLY>
 __device__ __forceinline__ float lora_delta_any(const LoraArgs& lo, int64_t n, int a, int64_t i, const float* u) {
-    if (lo.type == Q8_LORA_BF16) return lora_delta<LoraBF16>(lo, n, a, i, u);
-    if (lo.type == Q8_LORA_F16) return lora_delta<LoraF16>(lo, n, a, i, u);
-    return lora_delta<LoraF32>(lo, n, a, i, u);
+    if (lo.type == Q8_LORA_BF16) return lora_delta<LoraBF16, FLY>(lo, n, a, i, u);
+    if (lo.type == Q8_LORA_F16) return lora_delta<LoraF16, FLY>(lo, n, a, i, u);
+    return lora_delta<LoraF32, FLY>(lo, n, a, i, u);
 }
 
 template <class Ty, bool SILU>
@@ -168,7 +211,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs lo, const flo
 
 // Second launch of the packed calls: the shared product's tiles with the correction (and,
 // SILU, the activation) behind each.  A block owns a run of neighbouring tiles and streams
-// it once for every 4 * NG rows; a fused tile is 8 gate rows and their 8 up rows.
+// them once for every 4 * NG rows (blockIdx.y: every gridDim.y-th of those); a fused tile is 8 gate rows and their 8 up rows.
 constexpr int kLoraSumTiles = 64;  // tiles * NG whose sums wait in LDS
 
 template <int NG>
@@ -189,38 +232,29 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     const TileWave W(smem, k >> 8, log2_wt);
     constexpr int kOut = SILU ? kTileRows / 2 : kTileRows;  // outputs of a tile
     const uint32_t rb = (uint32_t)(k >> 5) * 34u;
-    const int tiles = (n_out + kOut - 1) / kOut;
-    const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
-    const int t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
-    // copy offsets of a tile with `rows` outputs: a row past them reads the last one
-    auto tile_offsets = [&](int rows, uint32_t (&off)[5]) __attribute__((always_inline)) {
-        W.offsets([&](int r) __attribute__((always_inline)) -> uint32_t {
-            const int half = SILU ? r / kOut : 0;
-            const int i = min(SILU ? r - half * kOut : r, rows - 1);
-            return (uint32_t)(i + half * n_out) * rb;
-        }, off);
-    };
-    uint32_t full[5];
-    tile_offsets(min(kOut, n_out), full);
+    const int tiles_all = (n_out + kOut - 1) / kOut;
+    const int first = (int)((int64_t)tiles_all * blockIdx.x / gridDim.x);
+    const int tiles = (int)((int64_t)tiles_all * (blockIdx.x + 1) / gridDim.x) - first;
+    // the last tile starts early enough to be whole; a matrix smaller than a tile repeats its
+    // last row
+    const int last_row0 = max(0, n_out - kOut);
+    auto row0_of = [&](int i) __attribute__((always_inline)) { return min((first + i) * kOut, last_row0); };
+    uint32_t off[5];
+    W.offsets([&](int r) __attribute__((always_inline)) -> uint32_t {
+        const int half = SILU ? r / kOut : 0;
+        return (uint32_t)(min(r - half * kOut, n_out - 1) + half * n_out) * rb;
+    }, off);
     constexpr int kChunk = kLoraSumTiles / NG;
-    for (int m0 = 0; m0 < m; m0 += 4 * NG) {
+    constexpr int kFly = SP * NG >= 6 ? 1 : SP * NG >= 4 ? 2 : 4;  // what the digits' registers leave
+    for (int m0 = 4 * NG * blockIdx.y; m0 < m; m0 += 4 * NG * gridDim.y) {
         const int mm = min(4 * NG, m - m0);
-        int c0 = t0;
-        auto tile_at = [&](int i, const uint8_t*& base, uint32_t (&off)[5]) __attribute__((always_inline)) {
-            const int row0 = (c0 + i) * kOut;
-            base = w + (size_t)row0 * rb;
-            if (row0 + kOut <= n_out) {
-#pragma unroll
-                for (int c = 0; c < 5; ++c) off[c] = full[c];
-            } else {
-                tile_offsets(n_out - row0, off);
-            }
-        };
-        TileRun run(W, min(kChunk, t1 - t0), tile_at);
-        long a[NG][SP][8];
+        int c0 = 0;
+        auto tile_at = [&](int i) __attribute__((always_inline)) { return w + (size_t)row0_of(c0 + i) * rb; };
+        i64x2 a[NG][SP][4];
         load_digits<SP, NG>(W, [&](int s) __attribute__((always_inline)) {
-            return s < mm ? dig + (size_t)(m0 + s) * k * 4 : nullptr;
+            return dig + (size_t)(m0 + min(s, mm - 1)) * k * 4;
         }, a);
+        TileRun run(W, off, min(kChunk, tiles), tile_at);
         while (true) {
             const int nt = run.n_tiles;
             multiply_tiles<SP, NG>(run, a, part, sums);
@@ -229,7 +263,7 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
             for (int o = threadIdx.x; o < mm * nt * kOut; o += kTileThreads) {
                 const int r = o % kOut, q = o / kOut;
                 const int s = q / nt, tile = q - s * nt;
-                const int i = (c0 + tile) * kOut + r;
+                const int i = row0_of(c0 + tile) + r;
                 if (i >= n_out) continue;
                 const int t = m0 + s;
                 const float* sum = sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
@@ -237,18 +271,18 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
                 const int ad = lo.of_row(t);
                 const float* ut = u + (size_t)t * lo.n_sections * lo.rank;
                 float v = row_scaled(sum[0], ex);
-                if (ad >= 0) v += lora_delta_any(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, i, ut);
+                if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, i, ut);
                 if constexpr (SILU) {
                     float up = row_scaled(sum[kOut], ex);
-                    if (ad >= 0) up += lora_delta_any(lo, 2 * (int64_t)n_out, ad, n_out + (int64_t)i, ut);
+                    if (ad >= 0) up += lora_delta_any<kFly>(lo, 2 * (int64_t)n_out, ad, n_out + (int64_t)i, ut);
                     v = silu_mul(v, up);
                 }
                 y[t * ldy + i] = v;
             }
             __syncthreads();  // the next chunk overwrites the sums
             c0 += nt;
-            if (c0 >= t1) break;
-            run.restart(min(kChunk, t1 - c0));
+            if (c0 >= tiles) break;
+            run.restart(min(kChunk, tiles - c0));
         }
     }
 }
@@ -267,8 +301,8 @@ template <class Ty>
 static hipError_t lora_add_typed(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu,
                                  const float* x, int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo,
                                  float* u, hipStream_t stream) {
-    const int64_t dots = m * lo.n_sections * lo.rank;
-    hipLaunchKernelGGL(lora_shrink_kernel<Ty>, dim3((unsigned)(dots < 262144 ? (dots + 3) / 4 : 65536)), dim3(256), 0, stream, lo, x, (int)m,
+    const int64_t units = m * (lo.n_sections * lo.rank / kShrinkCols);
+    hipLaunchKernelGGL(lora_shrink_kernel<Ty>, dim3((unsigned)(units < 65536 ? units : 65536)), dim3(256), 0, stream, lo, x, (int)m,
                        (int)k, ldx, u);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -309,10 +343,15 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const uint8_t* w, int
         if (e != hipSuccess) return e;
         attr_dev = dev.device;
     }
+    // one block per CU; a matrix with fewer tiles than half the CUs hands its row groups to
+    // blocks of their own
     const int64_t per_tile = SILU ? kTileRows / 2 : kTileRows;
     const int64_t tiles = (n_out + per_tile - 1) / per_tile;
-    const unsigned grid = (unsigned)(tiles < dev.cu_count ? tiles : dev.cu_count);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, log2_wt, dig,
+    const int64_t gx = tiles < dev.cu_count ? tiles : dev.cu_count;
+    const int64_t groups = (m + 4 * NG - 1) / (4 * NG);
+    const int64_t gy = dev.cu_count / gx < groups ? dev.cu_count / gx : groups;
+    const dim3 grid((unsigned)gx, (unsigned)(gy < 1 ? 1 : gy));
+    hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, log2_wt, dig,
                        exps, lo, u, (int)m, y, ldy);
     return hipGetLastError();
 }
@@ -360,8 +399,8 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     float* u = reinterpret_cast<float*>(ws + L.u_off);
     int* exps = reinterpret_cast<int*>(ws + L.base_off);
     int8_t* dig = reinterpret_cast<int8_t*>(exps + q8v::kPrefillRows);
-    const int64_t dots = lora.n_adapters ? m * lora.n_sections * lora.rank : 0;
-    const dim3 grid((unsigned)(m + (dots + 3) / 4));
+    const int64_t units = lora.n_adapters ? m * (lora.n_sections * lora.rank / kShrinkCols) : 0;
+    const dim3 grid((unsigned)(m + units));
     if (lora.type == Q8_LORA_F32)
         hipLaunchKernelGGL(lora_prepare_kernel<LoraF32>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
                            exps);
