@@ -51,12 +51,12 @@ struct SliceShare {
     int log2_wt, sp;
 };
 __host__ __device__ inline SliceShare slice_share(int S) {
-    SliceShare best{3, (S + 7) / 8};
-    for (int l = 2; l >= 0; --l) {
+    SliceShare best{-1, 0};
+    for (int l = 3; l >= 0; --l) {
         const int sp = (S + (1 << l) - 1) >> l;
-        if (sp <= 3 && (sp << l) < (best.sp << best.log2_wt) && (1 << l) <= S) best = SliceShare{l, sp};
+        if ((1 << l) > S || (sp > 3 && l < 3)) continue;
+        if (best.log2_wt < 0 || (sp << l) < (best.sp << best.log2_wt)) best = SliceShare{l, sp};
     }
-    while (best.log2_wt > 0 && (1 << best.log2_wt) > S) best = SliceShare{best.log2_wt - 1, 1};
     return best;
 }
 

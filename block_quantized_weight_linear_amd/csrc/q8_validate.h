@@ -306,18 +306,47 @@ inline q8_status check_lora_add(const float* y, int64_t n_in, int64_t ldy, const
 
 // ----------------------------------------------------- the whole mixture-of-experts layer
 
-// Workspace of q8_moe_layer: logits, the routing and the mixture's own.
+// q8_moe_layer runs in two launches on the digit tiles (digit_tiles.h) below the matrix-core
+// switch of the grouped call, up to kMoeLayerMaxTokens tokens (every block selects all
+// tokens' experts) and for widths of at most 24 slices of 256 (three a wave); else the
+// routing and the grouped mixture follow each other.
+constexpr int64_t kMoeLayerMaxTokens = 128;
+constexpr int64_t kMoeLayerMaxWidth = 24 * 256;
+inline bool moe_layer_uses_tiles(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {
+    return m <= kMoeLayerMaxTokens && h <= kMoeLayerMaxWidth && f <= kMoeLayerMaxWidth &&
+           !moe_uses_matrix_cores(m * int64_t(k), n_exp);
+}
+
+// Flags and counters of the two-launch form: claims of the chunks of two lists, the jobs' and
+// the down tiles' counts.  Jobs: an expert's tokens in eights, m * k < 8 * n_exp <= 2048 pairs.
+constexpr int kLayerMaxChunks = 512;
+constexpr int kLayerMaxJobs = 512;
+constexpr size_t kLayerCounterBytes = sizeof(uint32_t) * size_t(2 * kLayerMaxChunks + kLayerMaxJobs + 16 * 32);
+
+// Workspace of q8_moe_layer: the logits, then what its form needs.
 struct MoeLayerWorkspace {
-    size_t logits_off, idx_off, w_off, moe_off, total;
+    size_t logits_off, total;
+    size_t idx_off, w_off, moe_off;                                          // routing, then mixture
+    size_t dig_off, exps_off, hidden_off, max_off, out_off, count_off;       // two launches
 };
 
 inline MoeLayerWorkspace moe_layer_workspace_layout(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {
     MoeLayerWorkspace w{};
+    const size_t pairs = size_t(m) * size_t(k);
     size_t off = 0;
     w.logits_off = off; off = round_up(off + route_workspace_bytes(m, n_exp), 256);
-    w.idx_off = off;    off = round_up(off + sizeof(int32_t) * size_t(m) * size_t(k), 256);
-    w.w_off = off;      off = round_up(off + sizeof(float) * size_t(m) * size_t(k), 256);
-    w.moe_off = off;    off += moe_workspace_layout(m, k, n_exp, f, h).total;
+    if (moe_layer_uses_tiles(m, k, n_exp, f, h)) {
+        w.count_off = off;  off = round_up(off + kLayerCounterBytes, 256);
+        w.max_off = off;    off = round_up(off + sizeof(uint32_t) * pairs, 256);
+        w.exps_off = off;   off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+        w.dig_off = off;    off = round_up(off + 4 * size_t(m) * size_t(h), 256);
+        w.hidden_off = off; off = round_up(off + sizeof(float) * pairs * size_t(f), 256);
+        w.out_off = off;    off = round_up(off + sizeof(float) * pairs * size_t(h), 256);
+    } else {
+        w.idx_off = off;    off = round_up(off + sizeof(int32_t) * pairs, 256);
+        w.w_off = off;      off = round_up(off + sizeof(float) * pairs, 256);
+        w.moe_off = off;    off += moe_workspace_layout(m, k, n_exp, f, h).total;
+    }
     w.total = off;
     return w;
 }
