@@ -28,7 +28,7 @@
 #include "gemv_core.h"
 #include "q8_internal.h"
 #include "q8_validate.h"
-#include "route_select.h"
+#include "wave_dpp.h"
 
 namespace q8k {
 
@@ -153,13 +153,24 @@ static_assert(kLayerLdsBytes <= 160 * 1024, "one block per CU");
 
 constexpr uint64_t kPatience = 3000;  // of the 100 MHz clock
 
-// Results that other CUs read in the same launch go past the caches of this one.
+// What other CUs read in the same launch goes past the caches that are not shared, and is
+// counted once it is there (vmcnt 0 in every wave, then a barrier): no cache is written
+// back or invalidated.  (With release and acquire fences instead, which write back and
+// invalidate an XCD's whole L2, a call measured 10 us longer.)
 __device__ __forceinline__ void store_shared(float* p, float v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ uint32_t load_shared(const uint32_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_shared(const float* p) {  // 8-byte aligned
+    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__builtin_bit_cast(float, (uint32_t)v), __builtin_bit_cast(float, (uint32_t)(v >> 32)));
+}
 
 // Wave 0 waits until the counts at p, p + stride, ... (n of them, n <= 64) sum up to
-// target, for about 30 us at most; then the block sees what was stored before they did.
+// target, for about 30 us at most; then load_shared sees what was stored before they did.
 // False (in every thread): not yet.
 __device__ __forceinline__ bool wait_counts(const uint32_t* p, int n, int stride, uint32_t target, int* word) {
     if (threadIdx.x < 64) {
@@ -174,7 +185,6 @@ __device__ __forceinline__ bool wait_counts(const uint32_t* p, int n, int stride
             if (there || wall_clock64() - began > kPatience) break;
             __builtin_amdgcn_s_sleep(1);
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
         if (threadIdx.x == 0) *word = there;
     }
     __syncthreads();
@@ -213,7 +223,7 @@ __device__ __forceinline__ int take_over(uint32_t* claim, int chunks, int* word)
 __device__ __forceinline__ void signal_count(uint32_t* p, uint32_t n) {
     wait_vmcnt_mem<0>();
     __syncthreads();
-    if (threadIdx.x == 0) __hip_atomic_fetch_add(p, n, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) __hip_atomic_fetch_add(p, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Tiles [tile0, tile0 + nt) of an expert's gate_up matrix for the pairs list[0 .. n), n <= 4 NG.
@@ -286,15 +296,19 @@ __device__ __forceinline__ bool layer_down(const LayerArgs& A, LayerLds& L, cons
     for (int g = 0; g < NG; ++g) {
         const int slot = threadIdx.x >> 7;
         const int pair = list[min(4 * g + slot, n - 1)];
-        const uint32_t bits = A.hid_max[pair];
+        const uint32_t bits = load_shared(A.hid_max + pair);
         const bool finite = bits < 0x7f800000u;
         const int e = row_exponent(bits);
         for (int s0 = 0; s0 < S; s0 += 4) {
             const int i = 8 * (threadIdx.x & 127);  // element within the four slices
             if (s0 * 256 + i < A.f) {
-                const float4* src = reinterpret_cast<const float4*>(A.hidden + (size_t)pair * A.f + s0 * 256 + i);
-                const float4 lo = src[0], hi = src[1];
-                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                float v[8];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 t = load_shared(A.hidden + (size_t)pair * A.f + s0 * 256 + i + 2 * c);
+                    v[2 * c] = t.x;
+                    v[2 * c + 1] = t.y;
+                }
                 uint64_t d[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -332,7 +346,7 @@ __device__ __forceinline__ bool layer_down(const LayerArgs& A, LayerLds& L, cons
             const int r = o & 15, q = o >> 4;
             const int s = q / ct, tile = q - s * ct;
             const int pair = list[s];
-            const uint32_t bits = A.hid_max[pair];
+            const uint32_t bits = load_shared(A.hid_max + pair);
             const int ex = bits < 0x7f800000u ? row_exponent(bits) - 29 : kNotFinite;
             const float sum = L.sums[(tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r];
             store_shared(A.out + (size_t)pair * A.h + (tile0 + c0 + tile) * 16 + r, row_scaled(sum, ex));
@@ -344,6 +358,91 @@ __device__ __forceinline__ bool layer_down(const LayerArgs& A, LayerLds& L, cons
     }
 }
 
+// Order-preserving integers and the wave's largest of them: six DPP steps, then lane 63.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);  // -0 counts as 0
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __builtin_bit_cast(float, (k >> 31) ? k & 0x7fffffffu : ~k);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
+    v = dpp_max<0x111>(v);  // row_shr 1, 2, 4, 8: lane 15 of each row has its row's largest
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142>(v);  // row_bcast 15, 31: lane 63 has the wave's
+    v = dpp_max<0x143>(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Softmax, top-k choice (k <= 64) and top-p cut of one token on one wave, n_exp <= 64 NP: what
+// route_topk.hip's select_topk chooses, to the bit, with the choice made on integer keys
+// (about a fifth of its time: 8 of 128 in 0.8 us) and the chosen experts' probabilities
+// formed together, lane j holding slot j.  put(expert, weight) is called on lanes j < k; a
+// token whose probabilities are not finite gets NaN weights.
+template <int NP, class Put>
+__device__ __forceinline__ void choose_experts(const float* logits, int lane, int n_exp, int k, int normalize,
+                                               float top_p, Put&& put) {
+    float l[NP];
+    uint32_t key[NP];
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+        const int e = lane + 64 * c;
+        l[c] = e < n_exp ? logits[e] : -INFINITY;
+        key[c] = e < n_exp ? order_key(l[c]) : 0u;
+    }
+    float mx = l[0];
+#pragma unroll
+    for (int c = 1; c < NP; ++c) mx = fmaxf(mx, l[c]);
+    mx = wave_max(mx);
+    float part = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NP; ++c) part += lane + 64 * c < n_exp ? expf(l[c] - mx) : 0.0f;
+    const float inv_sum = 1.0f / wave_sum(part);
+
+    uint32_t my_key = 0;
+    int my_expert = -1;
+    for (int j = 0; j < k; ++j) {
+        uint32_t v = key[0];
+#pragma unroll
+        for (int c = 1; c < NP; ++c) v = max(v, key[c]);
+        const uint32_t best = wave_largest(v);
+        // its lowest holder: the lowest plane of 64 experts, then the lowest lane
+        uint64_t who = 0;
+        int plane = 0;
+#pragma unroll
+        for (int c = NP - 1; c >= 0; --c) {
+            const uint64_t w = __ballot(key[c] == best);
+            plane = w ? c : plane;
+            who = w ? w : who;
+        }
+        const int at = (int)__builtin_ctzll(who);
+#pragma unroll
+        for (int c = 0; c < NP; ++c) key[c] = lane == at && c == plane ? 0u : key[c];
+        if (lane == j) {
+            my_key = best;
+            my_expert = 64 * plane + at;
+        }
+    }
+    const float p = lane < k ? expf(key_value(my_key) - mx) * inv_sum : 0.0f;
+    // running sums in selection order
+    float psum = 0.0f, before = 0.0f, through = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        if (lane == j) before = psum;
+        psum += lane_f(p, j);
+        if (lane == j) through = psum;
+    }
+    const bool all = !(top_p < 1.0f);
+    const bool kept = lane < k && (all || lane == 0 || before < top_p * psum);
+    const float ksum = all ? psum : wave_max(kept ? through : 0.0f);
+    if (lane < k) put(kept ? my_expert : -1, kept ? (normalize ? p / ksum : p) : 0.0f);
+}
+
 // Pieces a job is cut into: the q <= min(32, tiles) for which the busiest of the blocks has
 // least to do, counting a piece's start (its first copies, its digits) as 1/16 of a job.
 // Lane q - 1 of the wave prices q.
@@ -351,14 +450,8 @@ __device__ __forceinline__ int pieces_per_job(int jobs, int tiles, int blocks, i
     const int q = (lane & 31) + 1;
     const float cost = (float)((jobs * q + blocks - 1) / blocks) * (1.0f / (float)q + 0.0625f);
     // the least cost (to 2^-18 of it), then the smallest q, as the largest key
-    uint32_t v = q <= tiles ? ~((__builtin_bit_cast(uint32_t, cost) & ~31u) | (uint32_t)(q - 1)) : 0u;
-    v = PickKeys::step<0x111>(v);
-    v = PickKeys::step<0x112>(v);
-    v = PickKeys::step<0x114>(v);
-    v = PickKeys::step<0x118>(v);
-    v = PickKeys::step<0x142>(v);
-    v = PickKeys::step<0x143>(v);
-    return (int)(~(uint32_t)__builtin_amdgcn_readlane((int)v, 63) & 31u) + 1;
+    const uint32_t v = q <= tiles ? ~((__builtin_bit_cast(uint32_t, cost) & ~31u) | (uint32_t)(q - 1)) : 0u;
+    return (int)(~wave_largest(v) & 31u) + 1;
 }
 
 template <int SP_H, int SP_F>
@@ -380,14 +473,16 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     __syncthreads();
     for (int t = wv; t < A.m; t += kTileWaves) {
         const float* lg = A.logits + (size_t)t * A.n_exp;
-        select_topk<PickKeys>([&](int e) { return lg[e]; }, lane, A.n_exp, A.k, A.normalize, A.top_p,
-                              [&](int j, int e, float p) {
-                                  // a token whose probabilities are not finite: no expert, weights NaN
-                                  const int keep = p == p ? e : -1;
-                                  L.idx[t * A.k + j] = (int16_t)keep;
-                                  L.w[t * A.k + j] = p;
-                                  if (keep >= 0) atomicAdd(&L.fill[keep], 1);
-                              });
+        auto put = [&](int e, float p) __attribute__((always_inline)) {
+            const int keep = p == p ? e : -1;  // weights NaN: no expert
+            L.idx[t * A.k + lane] = (int16_t)keep;
+            L.w[t * A.k + lane] = p;
+            if (keep >= 0) atomicAdd(&L.fill[keep], 1);
+        };
+        if (A.n_exp <= 128)
+            choose_experts<2>(lg, lane, A.n_exp, A.k, A.normalize, A.top_p, put);
+        else
+            choose_experts<4>(lg, lane, A.n_exp, A.k, A.normalize, A.top_p, put);
     }
     if (tid == 0) L.word = (int)(taken_up | taken_down << 1);
     __syncthreads();
@@ -512,34 +607,31 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
         if (up < 0) down = down_at = take_over(A.cnt->claim_down, blocks, &L.word);
     }
 
-    // the tokens' sums, in slot order, four columns a thread, the slots' rows loaded together
-    const int64_t all = (int64_t)A.m * (A.h / 4);
+    // the tokens' sums, in slot order, two columns a thread, eight slots' loads together
+    const int half_h = A.h / 2;
+    const int64_t all = (int64_t)A.m * half_h;
     const int64_t i1 = all * (me + 1) / blocks;
     for (int64_t i = all * me / blocks + tid; i < i1; i += kTileThreads) {
-        const int t = (int)(i / (A.h / 4)), col = 4 * (int)(i - (int64_t)t * (A.h / 4));
+        const int t = (int)(i / half_h), col = 2 * (int)(i - (int64_t)t * half_h);
         const float* o = A.out + (size_t)t * A.k * A.h + col;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 s = make_float2(0.f, 0.f);
         for (int j0 = 0; j0 < A.k; j0 += 8) {
-            float4 v[8];
+            float2 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const float4*>(o + (size_t)min(j0 + j, A.k - 1) * A.h);
+            for (int j = 0; j < 8; ++j) v[j] = load_shared(o + (size_t)min(j0 + j, A.k - 1) * A.h);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (j0 + j >= A.k) continue;
                 const float p = L.w[t * A.k + j0 + j];
-                if (p != p) s = make_float4(p, p, p, p);
+                if (p != p) s = make_float2(p, p);
                 if (L.idx[t * A.k + j0 + j] < 0) continue;  // a dropped slot's row was never written
                 s.x = __builtin_fmaf(p, v[j].x, s.x);
                 s.y = __builtin_fmaf(p, v[j].y, s.y);
-                s.z = __builtin_fmaf(p, v[j].z, s.z);
-                s.w = __builtin_fmaf(p, v[j].w, s.w);
             }
         }
         float* yo = A.y + (size_t)t * A.ldy + col;
         yo[0] = s.x;
         yo[1] = s.y;
-        yo[2] = s.z;
-        yo[3] = s.w;
     }
 }
 

@@ -308,12 +308,12 @@ inline q8_status check_lora_add(const float* y, int64_t n_in, int64_t ldy, const
 
 // q8_moe_layer runs in two launches on the digit tiles (digit_tiles.h) below the matrix-core
 // switch of the grouped call, up to kMoeLayerMaxTokens tokens (every block selects all
-// tokens' experts) and for widths of at most 24 slices of 256 (three a wave); else the
+// tokens' experts), at most 64 experts a token and widths of at most 24 slices of 256 (three a wave); else the
 // routing and the grouped mixture follow each other.
 constexpr int64_t kMoeLayerMaxTokens = 128;
 constexpr int64_t kMoeLayerMaxWidth = 24 * 256;
 inline bool moe_layer_uses_tiles(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {
-    return m <= kMoeLayerMaxTokens && h <= kMoeLayerMaxWidth && f <= kMoeLayerMaxWidth &&
+    return m <= kMoeLayerMaxTokens && k <= 64 && h <= kMoeLayerMaxWidth && f <= kMoeLayerMaxWidth &&
            !moe_uses_matrix_cores(m * int64_t(k), n_exp);
 }
 

@@ -27,7 +27,7 @@
 
 #include "lds_dma.h"
 #include "q8_internal.h"
-#include "route_select.h"
+#include "wave_dpp.h"
 
 namespace q8k {
 
@@ -36,11 +36,126 @@ constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteBatch = 4;  // experts a wave multiplies together
 constexpr int kMaxExperts = 256;
 
-__device__ __forceinline__ auto store_slots(int tok, int k, int32_t* __restrict__ out_idx, float* __restrict__ out_w) {
-    return [=](int j, int e, float w) __attribute__((always_inline)) {
-        out_idx[(size_t)tok * k + j] = e;
-        out_w[(size_t)tok * k + j] = w;
+__device__ __forceinline__ bool better(float v, int i, float bv, int bi) {
+    return v > bv || (v == bv && i < bi);
+}
+
+// Every lane gets the wave's best (value, index) under better().
+__device__ __forceinline__ void wave_best(float& v, int& i) {
+    auto step = [&](auto c) __attribute__((always_inline)) {
+        constexpr int C = decltype(c)::value;
+        const float ov = dpp_f<C>(v);
+        const int oi = dpp_i<C>(i);
+        if (better(ov, oi, v, i)) {
+            v = ov;
+            i = oi;
+        }
     };
+    step(std::integral_constant<int, kDppXor1>{});
+    step(std::integral_constant<int, kDppXor2>{});
+    step(std::integral_constant<int, kDppHalfMirror>{});
+    step(std::integral_constant<int, kDppMirror>{});
+    float bv = lane_f(v, 0);
+    int bi = __builtin_amdgcn_readlane(i, 0);
+#pragma unroll
+    for (int r = 1; r < 4; ++r) {
+        const float rv = lane_f(v, 16 * r);
+        const int ri = __builtin_amdgcn_readlane(i, 16 * r);
+        if (better(rv, ri, bv, bi)) {
+            bv = rv;
+            bi = ri;
+        }
+    }
+    v = bv;
+    i = bi;
+}
+
+// Softmax, top-k selection and the top-p cut for one token on one wave; logit_of(e)
+// returns expert e's float32 logit (e < n_exp).  Lane l owns experts l, l+64, l+128, l+192.
+template <class LogitOf>
+__device__ __forceinline__ void select_topk(LogitOf&& logit_of, int lane, int tok, int n_exp, int k, int normalize,
+                                            float top_p, int32_t* __restrict__ out_idx,
+                                            float* __restrict__ out_w) {
+    float l[4];
+    int taken = 0;  // bit c: expert lane + 64c already selected
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int e = lane + 64 * c;
+        l[c] = e < n_exp ? logit_of(e) : -INFINITY;
+        if (e >= n_exp) taken |= 1 << c;
+    }
+    const float mx = wave_max(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    float ex[4];
+    float part = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        ex[c] = (lane + 64 * c < n_exp) ? expf(l[c] - mx) : 0.0f;
+        part += ex[c];
+    }
+    const float inv_sum = 1.0f / wave_sum(part);
+
+    // k rounds; each picks the wave's best untaken expert (every lane learns it) and the
+    // owner lane's probability by readlane.  Lane (j % 64) keeps round j's result in its
+    // register slot j / 64; the chosen probabilities are summed in selection order,
+    // identically on all lanes.
+    int keep_i[4] = {0, 0, 0, 0};
+    float keep_p[4] = {0.f, 0.f, 0.f, 0.f};
+    float keep_cb[4] = {0.f, 0.f, 0.f, 0.f};  // running sum before the slot
+    float keep_ca[4] = {0.f, 0.f, 0.f, 0.f};  // running sum through the slot
+    float psum = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        float bv = -INFINITY;
+        int bi = 0x7fffffff;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int e = lane + 64 * c;
+            if (!(taken & (1 << c)) && better(l[c], e, bv, bi)) {
+                bv = l[c];
+                bi = e;
+            }
+        }
+        wave_best(bv, bi);
+        const int wl = bi & 63, wc = bi >> 6;
+        const float mine = wc == 0 ? ex[0] : wc == 1 ? ex[1] : wc == 2 ? ex[2] : ex[3];
+        const float bp = lane_f(mine, wl);
+        if (lane == wl) taken |= 1 << wc;
+        const float p = bp * inv_sum;
+        const float before = psum;
+        psum += p;
+        if ((j & 63) == lane) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if ((j >> 6) == c) {
+                    keep_i[c] = bi;
+                    keep_p[c] = p;
+                    keep_cb[c] = before;
+                    keep_ca[c] = psum;
+                }
+            }
+        }
+    }
+    // top-p cut: every lane holds the same running sums for its slots, so the kept sum is
+    // the largest running sum through a kept slot (the sums only grow)
+    const bool all = !(top_p < 1.0f);
+    const float thr = top_p * psum;
+    bool kept[4];
+    float ksum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int j = lane + 64 * c;
+        kept[c] = j < k && (all || j == 0 || keep_cb[c] < thr);
+        if (kept[c]) ksum = fmaxf(ksum, keep_ca[c]);
+    }
+    ksum = wave_max(ksum);
+    if (all) ksum = psum;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int j = lane + 64 * c;
+        if (j < k) {
+            out_idx[(size_t)tok * k + j] = kept[c] ? keep_i[c] : -1;
+            out_w[(size_t)tok * k + j] = kept[c] ? (normalize ? keep_p[c] / ksum : keep_p[c]) : 0.0f;
+        }
+    }
 }
 
 __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(const float* __restrict__ x, int h, int ldx,
@@ -97,7 +212,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(const float* 
     }
     __syncthreads();
     if (wave != 0) return;
-    select_topk<PickPairs>([&](int e) { return logits[e]; }, lane, n_exp, k, normalize, top_p, store_slots(tok, k, out_idx, out_w));
+    select_topk([&](int e) { return logits[e]; }, lane, tok, n_exp, k, normalize, top_p, out_idx, out_w);
 }
 
 // Two-pass router for many experts or tokens: the logits of a token are spread over
@@ -259,8 +374,7 @@ __global__ __launch_bounds__(256) void route_select_kernel(const float* __restri
     const int tok = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (tok >= m) return;
     const float* lg = logits + (size_t)tok * n_exp;
-    select_topk<PickPairs>([&](int e) { return lg[e]; }, threadIdx.x & 63, n_exp, k, normalize, top_p,
-                store_slots(tok, k, out_idx, out_w));
+    select_topk([&](int e) { return lg[e]; }, threadIdx.x & 63, tok, n_exp, k, normalize, top_p, out_idx, out_w);
 }
 
 hipError_t launch_route_topk(const DeviceInfo&, const float* x, int64_t m, int64_t h, int64_t ldx,
