@@ -267,10 +267,14 @@ struct TileRun {
         next_tile = W.tg;
         next_sl = 0;
         n_items = (W.tg < n_tiles ? (n_tiles - W.tg + tps - 1) / tps : 0) * W.n_sl;
-        // always kRing items (past the last one: it again), so that the compiler knows how
+        // kRing items (past the last one: it again) or none, so that the compiler knows how
         // many copies are younger than the digits
-        unroll<kRing>([&](auto sc) __attribute__((always_inline)) { issue(decltype(sc)::value); });
-        wait_vmcnt<5 * kRing>();
+        if (n_items > 0) {
+            unroll<kRing>([&](auto sc) __attribute__((always_inline)) { issue(decltype(sc)::value); });
+            wait_vmcnt<5 * kRing>();
+        } else {
+            wait_vmcnt<0>();
+        }
     }
     __device__ __forceinline__ void issue(int slot) {
         const uint8_t* tile = tile_at(min(next_tile, n_tiles - 1));

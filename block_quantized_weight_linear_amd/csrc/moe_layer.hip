@@ -6,10 +6,9 @@
 //   2. layer: one block per CU.  Every block selects all tokens' experts by itself (the same
 //      code as the routers: the same choice) and so knows the whole work list: the gate_up
 //      tiles of the chosen experts (8 gate rows and their 8 up rows), their down tiles, then
-//      the tokens' weighted sums.  An expert's tokens, eight at most, are one job; jobs are
-//      cut into equal pieces of neighbouring tiles and block b's chunk of each list is the
-//      pieces b, b + blocks, ...  A down piece waits until its job's hidden rows are there,
-//      the sums until all down tiles are.
+//      the tokens' weighted sums.  An expert's tokens, eight at most, are one job; the jobs'
+//      tiles are cut into one chunk of neighbouring tiles for each block.  A down chunk
+//      waits until its jobs' hidden rows are there, the sums until all down tiles are.
 //
 // No block needs another one to start: every chunk is claimed by a flag before it is worked
 // on, and a block that has waited for a while takes over chunks nobody has claimed (those
@@ -23,6 +22,8 @@
 // order.  A token's result depends on its own row alone.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "digit_tiles.h"
 #include "gemv_core.h"
@@ -143,9 +144,13 @@ struct LayerLds {
     float w[kLayerMaxPairs];                // the pairs' weights
     int16_t idx[kLayerMaxPairs];            // their experts, -1: none
     uint16_t list[kLayerMaxPairs];          // pairs by expert
+    uint8_t list_token[kLayerMaxPairs];     // and their tokens
+    int token_exp[q8v::kMoeLayerMaxTokens];
     int fill[q8v::kMaxExperts];
     uint16_t job_expert[kMaxJobs], job_first[kMaxJobs], job_rows[kMaxJobs];  // first: in list
-    uint32_t max_bits[8];
+    uint32_t max_bits[kJobRows];
+    int row_exp[kJobRows];                  // of the job in work: its rows' exponents
+    uint32_t row_pair[kJobRows];            // and pairs
     int n_jobs, word;
 };
 constexpr size_t kLayerLdsBytes = kRingBytes + sizeof(LayerLds);
@@ -220,21 +225,27 @@ __device__ __forceinline__ int take_over(uint32_t* claim, int chunks, int* word)
 }
 
 // The whole block: every wave's stores are done, then one thread counts.
-__device__ __forceinline__ void signal_count(uint32_t* p, uint32_t n) {
+__device__ __forceinline__ void raise_count(uint32_t* p, uint32_t n) {
     wait_vmcnt_mem<0>();
     __syncthreads();
-    if (threadIdx.x == 0) __hip_atomic_fetch_add(p, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0 && n) __hip_atomic_fetch_add(p, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Tiles [tile0, tile0 + nt) of an expert's gate_up matrix for the pairs list[0 .. n), n <= 4 NG.
 template <int SP, int NG>
 __device__ __forceinline__ void layer_gate_up(const LayerArgs& A, LayerLds& L, const TileWave& W,
                                               const uint32_t (&off)[5], const uint8_t* w, int tile0, int nt,
-                                              const uint16_t* list, int n) {
+                                              const uint16_t* list, const uint8_t* tokens, int n) {
     const uint32_t rb = (uint32_t)(A.h >> 5) * 34u;
+    if ((int)threadIdx.x < n) {
+        const int pair = list[threadIdx.x];
+        L.row_pair[threadIdx.x] = pair;
+        L.row_exp[threadIdx.x] = L.token_exp[tokens[threadIdx.x]];
+        L.max_bits[threadIdx.x] = 0;
+    }
     i64x2 a[NG][SP][4];
     load_digits<SP, NG>(W, [&](int s) __attribute__((always_inline)) {
-        return A.dig + (size_t)(list[min(s, n - 1)] / A.k) * A.h * 4;
+        return A.dig + (size_t)tokens[min(s, n - 1)] * A.h * 4;
     }, a);
     int c0 = 0;
     auto tile_at = [&](int i) __attribute__((always_inline)) { return w + (size_t)((tile0 + c0 + i) * 8) * rb; };
@@ -243,26 +254,30 @@ __device__ __forceinline__ void layer_gate_up(const LayerArgs& A, LayerLds& L, c
     while (true) {
         const int ct = run.n_tiles;
         multiply_tiles<SP, NG>(run, a, L.part, L.sums);
-        if (threadIdx.x < 4 * NG) L.max_bits[threadIdx.x] = 0;
         __syncthreads();
-        for (int o = threadIdx.x; o < n * ct * 8; o += kTileThreads) {
-            const int r = o & 7, q = o >> 3;
-            const int s = q / ct, tile = q - s * ct;
-            const int pair = list[s];
-            const float* sum = L.sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
-            const int ex = A.exps[pair / A.k];
-            const float v = silu_mul(row_scaled(sum[0], ex), row_scaled(sum[8], ex));
-            store_shared(A.hidden + (size_t)pair * A.f + (tile0 + c0 + tile) * 8 + r, v);
-            atomicMax(&L.max_bits[s], __builtin_bit_cast(uint32_t, v) & 0x7fffffffu);
+        // a wave takes a tile: 8 rows of up to 8 pairs
+        const int r = threadIdx.x & 7, s = (threadIdx.x >> 3) & 7;
+        if (s < n) {
+            const int ex = L.row_exp[s];
+            float* row = A.hidden + (size_t)L.row_pair[s] * A.f + (tile0 + c0) * 8 + r;
+            uint32_t mx = 0;
+            for (int tile = threadIdx.x >> 6; tile < ct; tile += kTileWaves) {
+                const float* sum = L.sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
+                const float v = silu_mul(row_scaled(sum[0], ex), row_scaled(sum[8], ex));
+                store_shared(row + 8 * tile, v);
+                mx = max(mx, __builtin_bit_cast(uint32_t, v) & 0x7fffffffu);
+            }
+            for (int o = 4; o >= 1; o >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o, 64));
+            if (r == 0 && mx) atomicMax(&L.max_bits[s], mx);
         }
         __syncthreads();
-        if (threadIdx.x < n)
-            __hip_atomic_fetch_max(A.hid_max + list[threadIdx.x], L.max_bits[threadIdx.x], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
         c0 += ct;
         if (c0 >= nt) break;
         run.restart(min(kChunk, nt - c0));
     }
+    if ((int)threadIdx.x < n)
+        __hip_atomic_fetch_max(A.hid_max + L.row_pair[threadIdx.x], L.max_bits[threadIdx.x], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // A wave's 16 bytes of the staged digits.
@@ -299,6 +314,10 @@ __device__ __forceinline__ bool layer_down(const LayerArgs& A, LayerLds& L, cons
         const uint32_t bits = load_shared(A.hid_max + pair);
         const bool finite = bits < 0x7f800000u;
         const int e = row_exponent(bits);
+        if ((threadIdx.x & 127) == 0) {
+            L.row_pair[4 * g + slot] = pair;
+            L.row_exp[4 * g + slot] = finite ? e - 29 : kNotFinite;
+        }
         for (int s0 = 0; s0 < S; s0 += 4) {
             const int i = 8 * (threadIdx.x & 127);  // element within the four slices
             if (s0 * 256 + i < A.f) {
@@ -342,14 +361,13 @@ __device__ __forceinline__ bool layer_down(const LayerArgs& A, LayerLds& L, cons
         const int ct = run.n_tiles;
         multiply_tiles<SP, NG>(run, a, L.part, L.sums);
         __syncthreads();
-        for (int o = threadIdx.x; o < n * ct * 16; o += kTileThreads) {
-            const int r = o & 15, q = o >> 4;
-            const int s = q / ct, tile = q - s * ct;
-            const int pair = list[s];
-            const uint32_t bits = load_shared(A.hid_max + pair);
-            const int ex = bits < 0x7f800000u ? row_exponent(bits) - 29 : kNotFinite;
-            const float sum = L.sums[(tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r];
-            store_shared(A.out + (size_t)pair * A.h + (tile0 + c0 + tile) * 16 + r, row_scaled(sum, ex));
+        // two waves take a tile: 16 rows of up to 8 pairs
+        const int r = threadIdx.x & 15, s = (threadIdx.x >> 4) & 7;
+        if (s < n) {
+            const int ex = L.row_exp[s];
+            float* row = A.out + (size_t)L.row_pair[s] * A.h + (tile0 + c0) * 16 + r;
+            for (int tile = threadIdx.x >> 7; tile < ct; tile += kTileWaves / 2)
+                store_shared(row + 16 * tile, row_scaled(L.sums[(tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r], ex));
         }
         __syncthreads();
         c0 += ct;
@@ -380,22 +398,31 @@ __device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+// Inclusive prefix sums over the wave: within rows of 16, then the rows before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+}
+
 // Softmax, top-k choice (k <= 64) and top-p cut of one token on one wave, n_exp <= 64 NP: what
 // route_topk.hip's select_topk chooses, to the bit, with the choice made on integer keys
-// (about a fifth of its time: 8 of 128 in 0.8 us) and the chosen experts' probabilities
+// (about a quarter of its time) and the chosen experts' probabilities
 // formed together, lane j holding slot j.  put(expert, weight) is called on lanes j < k; a
 // token whose probabilities are not finite gets NaN weights.
 template <int NP, class Put>
-__device__ __forceinline__ void choose_experts(const float* logits, int lane, int n_exp, int k, int normalize,
+__device__ __forceinline__ void choose_experts(const float (&l)[NP], int lane, int n_exp, int k, int normalize,
                                                float top_p, Put&& put) {
-    float l[NP];
     uint32_t key[NP];
 #pragma unroll
-    for (int c = 0; c < NP; ++c) {
-        const int e = lane + 64 * c;
-        l[c] = e < n_exp ? logits[e] : -INFINITY;
-        key[c] = e < n_exp ? order_key(l[c]) : 0u;
-    }
+    for (int c = 0; c < NP; ++c) key[c] = lane + 64 * c < n_exp ? order_key(l[c]) : 0u;
     float mx = l[0];
 #pragma unroll
     for (int c = 1; c < NP; ++c) mx = fmaxf(mx, l[c]);
@@ -443,16 +470,25 @@ __device__ __forceinline__ void choose_experts(const float* logits, int lane, in
     if (lane < k) put(kept ? my_expert : -1, kept ? (normalize ? p / ksum : p) : 0.0f);
 }
 
-// Pieces a job is cut into: the q <= min(32, tiles) for which the busiest of the blocks has
-// least to do, counting a piece's start (its first copies, its digits) as 1/16 of a job.
-// Lane q - 1 of the wave prices q.
-__device__ __forceinline__ int pieces_per_job(int jobs, int tiles, int blocks, int lane) {
-    const int q = (lane & 31) + 1;
-    const float cost = (float)((jobs * q + blocks - 1) / blocks) * (1.0f / (float)q + 0.0625f);
-    // the least cost (to 2^-18 of it), then the smallest q, as the largest key
-    const uint32_t v = q <= tiles ? ~((__builtin_bit_cast(uint32_t, cost) & ~31u) | (uint32_t)(q - 1)) : 0u;
-    return (int)(~wave_largest(v) & 31u) + 1;
-}
+// How a list of jobs x `per` tiles is cut into the blocks' chunks, ranges of neighbouring
+// tiles: where a job has at least one block to itself, q = blocks / jobs equal parts of every
+// job (a chunk then starts one job only), unless equal parts of the whole list leave the
+// busiest block less to do although it starts two; a start (the first copies, the digits)
+// counts as `start` tiles.
+struct Cut {
+    int q, per, all, blocks;
+    __device__ __forceinline__ Cut(int jobs, int per_, int blocks_, int start)
+        : per(per_), all(jobs * per_), blocks(blocks_) {
+        q = jobs > 0 ? min(blocks / jobs, per) : 0;
+        if (q > 0 && (per + q - 1) / q > (all + blocks - 1) / blocks + start) q = 0;
+    }
+    __device__ __forceinline__ int begin(int chunk) const {
+        if (q == 0) return (int)((int64_t)all * chunk / blocks);
+        const int job = chunk / q, part = chunk - job * q;
+        return min(job * per + per * part / q, all);
+    }
+    __device__ __forceinline__ int end(int chunk) const { return begin(chunk + 1); }
+};
 
 template <int SP_H, int SP_F>
 __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
@@ -470,20 +506,35 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
         taken_down = __hip_atomic_exchange(&A.cnt->claim_down[me], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     for (int e = tid; e < q8v::kMaxExperts; e += kTileThreads) L.fill[e] = 0;
+    for (int t = tid; t < A.m; t += kTileThreads) L.token_exp[t] = A.exps[t];
     __syncthreads();
-    for (int t = wv; t < A.m; t += kTileWaves) {
-        const float* lg = A.logits + (size_t)t * A.n_exp;
-        auto put = [&](int e, float p) __attribute__((always_inline)) {
-            const int keep = p == p ? e : -1;  // weights NaN: no expert
-            L.idx[t * A.k + lane] = (int16_t)keep;
-            L.w[t * A.k + lane] = p;
-            if (keep >= 0) atomicAdd(&L.fill[keep], 1);
+    auto choose_all = [&](auto np) __attribute__((always_inline)) {
+        constexpr int NP = decltype(np)::value;
+        float l[NP], next[NP];
+        auto load = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int c = 0; c < NP; ++c) {
+                const int e = lane + 64 * c;
+                next[c] = e < A.n_exp ? A.logits[(size_t)min(t, A.m - 1) * A.n_exp + e] : -INFINITY;
+            }
         };
-        if (A.n_exp <= 128)
-            choose_experts<2>(lg, lane, A.n_exp, A.k, A.normalize, A.top_p, put);
-        else
-            choose_experts<4>(lg, lane, A.n_exp, A.k, A.normalize, A.top_p, put);
-    }
+        load(wv);
+        for (int t = wv; t < A.m; t += kTileWaves) {
+#pragma unroll
+            for (int c = 0; c < NP; ++c) l[c] = next[c];
+            load(t + kTileWaves);
+            choose_experts<NP>(l, lane, A.n_exp, A.k, A.normalize, A.top_p, [&](int e, float p) __attribute__((always_inline)) {
+                const int keep = p == p ? e : -1;  // weights NaN: no expert
+                L.idx[t * A.k + lane] = (int16_t)keep;
+                L.w[t * A.k + lane] = p;
+                if (keep >= 0) atomicAdd(&L.fill[keep], 1);
+            });
+        }
+    };
+    if (A.n_exp <= 128)
+        choose_all(std::integral_constant<int, 2>{});
+    else
+        choose_all(std::integral_constant<int, 4>{});
     if (tid == 0) L.word = (int)(taken_up | taken_down << 1);
     __syncthreads();
     if (wv == 0) {  // lane l: experts 4l .. 4l + 3
@@ -494,14 +545,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
             sum += c[q];
             jobs += (c[q] + kJobRows - 1) / kJobRows;
         }
-        int incl = sum, jincl = jobs;
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(incl, o, 64), v = __shfl_up(jincl, o, 64);
-            if (lane >= o) {
-                incl += u;
-                jincl += v;
-            }
-        }
+        const int incl = wave_scan(sum), jincl = wave_scan(jobs);
         int at = incl - sum, jat = jincl - jobs;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -529,6 +573,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
             if (e >= 0) {
                 const int pos = L.fill[e] + __popcll(same & ((1ull << lane) - 1));
                 L.list[pos] = (uint16_t)(i0 + lane);
+                L.list_token[pos] = (uint8_t)((i0 + lane) / A.k);
                 wait_lgkmcnt_mem<0>();                        // every lane has read its position
                 if ((same >> lane) == 1ull) L.fill[e] = pos + 1;  // the highest lane of its expert
             }
@@ -539,53 +584,59 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     __syncthreads();
     const int jobs = __builtin_amdgcn_readfirstlane(L.n_jobs);
     const int up_tiles = A.f / 8, down_tiles = A.h / 16;
-    const int q_up = pieces_per_job(jobs, up_tiles, blocks, lane);
-    const int q_down = pieces_per_job(jobs, down_tiles, blocks, lane);
+    // a start takes about as long as 6 gate_up tiles and 16 down tiles of 2048 and 768 inputs
+    const Cut cut_up(jobs, up_tiles, blocks, 6), cut_down(jobs, down_tiles, blocks, 16);
     const uint32_t rb_h = (uint32_t)(A.h >> 5) * 34u, rb_f = (uint32_t)(A.f >> 5) * 34u;
-    // piece p of the list with q pieces a job of `per` tiles
+    // the tiles [t, end) as far as they belong to one job
     struct Piece {
         int job, expert, rows, tile0, tiles;
         const uint16_t* list;
+        const uint8_t* tokens;
     };
-    auto piece_of = [&](int p, int q, int per) __attribute__((always_inline)) {
+    auto piece_at = [&](int t, int end, int per) __attribute__((always_inline)) {
         Piece r;
-        r.job = p / q;
-        const int part = p - r.job * q;
+        r.job = t / per;
+        r.tile0 = t - r.job * per;
+        r.tiles = min(per - r.tile0, end - t);
         r.expert = __builtin_amdgcn_readfirstlane((int)L.job_expert[r.job]);
         r.rows = __builtin_amdgcn_readfirstlane((int)L.job_rows[r.job]);
-        r.list = L.list + __builtin_amdgcn_readfirstlane((int)L.job_first[r.job]);
-        r.tile0 = per * part / q;
-        r.tiles = per * (part + 1) / q - r.tile0;
+        const int first = __builtin_amdgcn_readfirstlane((int)L.job_first[r.job]);
+        r.list = L.list + first;
+        r.tokens = L.list_token + first;
         return r;
     };
     const TileWave Wh(smem, A.h >> 8, A.log2_wt_h), Wf(smem, A.f >> 8, A.log2_wt_f);
 
-    int up = taken & 1 ? -1 : me;                       // the gate_up chunk to work on
-    int down = taken & 2 ? -1 : me, down_at = me;       // the down chunk, its next piece
+    int up = taken & 1 ? -1 : me;    // the gate_up chunk to work on
+    int down = taken & 2 ? -1 : me;  // the down chunk, its next tile
+    int down_at = cut_down.begin(me);
     while (true) {
         if (up >= 0) {
             uint32_t off[5];
             Wh.offsets([&](int r) __attribute__((always_inline)) -> uint32_t {
                 return (uint32_t)(r < 8 ? r : A.f + r - 8) * rb_h;
             }, off);
-            for (int p = up; p < jobs * q_up; p += blocks) {
-                const Piece pc = piece_of(p, q_up, up_tiles);
+            const int end = cut_up.end(up);
+            for (int t = cut_up.begin(up); t < end;) {
+                const Piece pc = piece_at(t, end, up_tiles);
                 const uint8_t* w = A.wgu + (size_t)pc.expert * (2 * A.f) * rb_h;
                 if (pc.rows > 4)
-                    layer_gate_up<SP_H, 2>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.rows);
+                    layer_gate_up<SP_H, 2>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.tokens, pc.rows);
                 else
-                    layer_gate_up<SP_H, 1>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.rows);
-                signal_count(&A.cnt->up_done[pc.job], (uint32_t)pc.tiles);
+                    layer_gate_up<SP_H, 1>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.tokens, pc.rows);
+                raise_count(&A.cnt->up_done[pc.job], (uint32_t)pc.tiles);
+                t += pc.tiles;
             }
             up = -1;
         }
         if (down >= 0) {
             uint32_t off[5];
             Wf.offsets([&](int r) __attribute__((always_inline)) -> uint32_t { return (uint32_t)r * rb_f; }, off);
+            const int end = cut_down.end(down);
             uint32_t done = 0;
             bool ready = true;
-            for (; down_at < jobs * q_down; down_at += blocks) {
-                const Piece pc = piece_of(down_at, q_down, down_tiles);
+            while (down_at < end) {
+                const Piece pc = piece_at(down_at, end, down_tiles);
                 const uint8_t* w = A.wdn + (size_t)pc.expert * A.h * rb_f;
                 const uint32_t* count = &A.cnt->up_done[pc.job];
                 if (pc.rows > 4)
@@ -594,17 +645,21 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
                     ready = layer_down<SP_F, 1>(A, L, Wf, off, w, pc.tile0, pc.tiles, pc.list, pc.rows, count, up_tiles);
                 if (!ready) break;
                 done += pc.tiles;
+                down_at += pc.tiles;
             }
-            signal_count(&A.cnt->down_done[me % kDoneParts][0], done);
+            raise_count(&A.cnt->down_done[me % kDoneParts][0], done);
             if (!ready) {
                 up = take_over(A.cnt->claim_up, blocks, &L.word);
                 continue;
             }
             down = -1;
         }
-        if (wait_counts(&A.cnt->down_done[0][0], kDoneParts, 32, (uint32_t)(jobs * down_tiles), &L.word)) break;
+        if (wait_counts(&A.cnt->down_done[0][0], kDoneParts, 32, (uint32_t)cut_down.all, &L.word)) break;
         up = take_over(A.cnt->claim_up, blocks, &L.word);
-        if (up < 0) down = down_at = take_over(A.cnt->claim_down, blocks, &L.word);
+        if (up < 0) {
+            down = take_over(A.cnt->claim_down, blocks, &L.word);
+            if (down >= 0) down_at = cut_down.begin(down);
+        }
     }
 
     // the tokens' sums, in slot order, two columns a thread, eight slots' loads together
