@@ -9,12 +9,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "digit_tiles.h"
 #include "gemv_core.h"
 #include "q8_internal.h"
 #include "q8_validate.h"
+#include "wave_dpp.h"
 
 namespace q8k {
 
@@ -287,6 +289,312 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     }
 }
 
+// ------------------------------------------------------------------- many rows
+//
+// From kLoraTiledRows rows on the correction runs on the bf16 matrix cores at float32
+// accuracy.  A float32 value is the exact sum of three bf16 values (its leading 8 bits, the
+// next 8, the last 8, each cut off, not rounded); a bf16 element of A or B is itself, a
+// binary16 one the sum of two.  A product takes the partial products down to 2^-16 of its
+// leading one (those left out are below 2^-23 of the product): 3, 5 or 6 instructions for
+// bf16, binary16 and float32 elements, with float32 accumulation.
+//
+//   1. plan:   the rows sorted by adapter (those without one last), in tiles of 64 rows.
+//   2. inner:  block (tile half of 32 rows, part of k): u of all sections' ranks; its four
+//              waves take 64-wide steps of k in turn and add up through LDS.  The parts of k
+//              give the few tiles enough blocks; u is kept apart for each.
+//   3. outer:  block (tile, 256 outputs): the parts of u added up in order, split and staged
+//              in LDS, then 64 x 64 outputs a wave, added to the product (or activated).
+// Bound by the memory: x once, the product in and out.
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRowTile = 64;
+constexpr int kRankChunk = 64;  // of u staged at a time
+
+// Eight values as PARTS bf16 vectors that add up to them.
+template <int PARTS>
+__device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&p)[PARTS]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) r[q] = __builtin_bit_cast(uint32_t, v[q]);
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s) {
+        u32x4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = __builtin_amdgcn_perm(r[2 * q + 1], r[2 * q], 0x07060302u);
+        p[s] = __builtin_bit_cast(bf16x8, w);
+        if (s + 1 < PARTS) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                r[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, r[q]) -
+                                                        __builtin_bit_cast(float, r[q] & 0xffff0000u));
+        }
+    }
+}
+
+// Eight elements of A or B as bf16 parts; from the n-th on zero.
+template <class Ty>
+struct LoraParts;
+template <>
+struct LoraParts<LoraBF16> {
+    static constexpr int N = 1;
+    static __device__ __forceinline__ void get(LoraBF16::V v, int n, bf16x8 (&p)[N]) {
+        if (n < 8)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q >= n) v[q] = 0;
+        p[0] = __builtin_bit_cast(bf16x8, v);
+    }
+};
+template <class Ty, int PARTS>
+struct LoraFloatParts {
+    static constexpr int N = PARTS;
+    static __device__ __forceinline__ void get(const typename Ty::V& v, int n, bf16x8 (&p)[N]) {
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = q < n ? Ty::at(v, q) : 0.0f;
+        split8<PARTS>(f, p);
+    }
+};
+template <>
+struct LoraParts<LoraF16> : LoraFloatParts<LoraF16, 2> {};
+template <>
+struct LoraParts<LoraF32> : LoraFloatParts<LoraF32, 3> {};
+
+template <int N>
+__device__ __forceinline__ f32x16 mfma_parts(const bf16x8 (&a)[3], const bf16x8 (&b)[N], f32x16 c) {
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j)
+            if (i + j <= 2) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], c, 0, 0, 0);
+    return c;
+}
+
+// Rows by adapter: sorted [m], and the tiles: adapter (n_adapters: none), first place, rows.
+struct LoraPlan {
+    int32_t* sorted;
+    int4* tiles;
+    int32_t* n_tiles;
+};
+
+__global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs lo, int m, LoraPlan P) {
+    constexpr int kBins = q8v::kLoraMaxAdapters + 64;  // five a lane of one wave
+    __shared__ int count[kBins], at[kBins], tile_at[kBins];
+    const int tid = threadIdx.x;
+    auto bin = [&](int t) __attribute__((always_inline)) {
+        const int a = lo.of_row(t);
+        return a < 0 ? lo.n_adapters : a;
+    };
+    for (int b = tid; b < kBins; b += 1024) count[b] = 0;
+    __syncthreads();
+    for (int t = tid; t < m; t += 1024) atomicAdd(&count[bin(t)], 1);
+    __syncthreads();
+    if (tid < 64) {
+        int rows = 0, tiles = 0;
+        for (int q = 0; q < 5; ++q) {
+            rows += count[5 * tid + q];
+            tiles += (count[5 * tid + q] + kRowTile - 1) / kRowTile;
+        }
+        int r = wave_scan(rows) - rows;
+        const int incl = wave_scan(tiles);
+        int tl = incl - tiles;
+        for (int q = 0; q < 5; ++q) {
+            at[5 * tid + q] = r;
+            tile_at[5 * tid + q] = tl;
+            r += count[5 * tid + q];
+            tl += (count[5 * tid + q] + kRowTile - 1) / kRowTile;
+        }
+        if (tid == 63) *P.n_tiles = incl;
+    }
+    __syncthreads();
+    if (tid <= lo.n_adapters)
+        for (int i = 0; i < count[tid]; i += kRowTile)
+            P.tiles[tile_at[tid] + i / kRowTile] = make_int4(tid, at[tid] + i, min(kRowTile, count[tid] - i), 0);
+    __syncthreads();
+    // the order within an adapter is free: a row's result does not depend on its tile
+    for (int t = tid; t < m; t += 1024) P.sorted[atomicAdd(&at[bin(t)], 1)] = t;
+}
+
+template <class Ty>
+__global__ __launch_bounds__(256) void lora_inner_kernel(LoraArgs lo, LoraPlan P, const float* __restrict__ x, int m,
+                                                         int k, int64_t ldx, float* __restrict__ u) {
+    constexpr int kChunks = 4;  // of 32 columns a pass
+    __shared__ float sums[4][kChunks * 16][64];
+    if ((int)(blockIdx.x >> 1) >= *P.n_tiles) return;
+    const int4 tile = P.tiles[blockIdx.x >> 1];
+    const int a = tile.x, rows = min(32, tile.z - 32 * (int)(blockIdx.x & 1));
+    if (a >= lo.n_adapters || rows <= 0) return;
+    const int32_t* ids = P.sorted + tile.y + 32 * (blockIdx.x & 1);
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
+    const int cols = lo.n_sections * lo.rank, r = lo.rank_of(a);
+    const float sc = lo.scale ? lo.scale[a] : 1.0f;
+    // a lane's k within a step of 64: 32 consecutive ones, eight for each of four instructions
+    const float* xr = x + (int64_t)ids[min(col, rows - 1)] * ldx + 32 * half;
+    const typename Ty::T* ab = static_cast<const typename Ty::T*>(lo.a) + (size_t)a * cols * k + 32 * half;
+    const int steps = k >> 6;
+    const int s0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
+    for (int c0 = 0; c0 < cols; c0 += 32 * kChunks) {
+        const int chunks = min(kChunks, (cols - c0 + 31) >> 5);
+        f32x16 acc[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
+        for (int st = s0 + wv; st < s1; st += 4) {
+            LoraF32::V xv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xv[q] = LoraF32::load8(xr + 64 * st + 8 * q);
+            typename Ty::V av[kChunks][4];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                if (c < chunks) {
+                    // a column past the last one repeats it
+                    const typename Ty::T* p = ab + (size_t)min(c0 + 32 * c + col, cols - 1) * k + 64 * st;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) av[c][q] = Ty::load8(p + 8 * q);
+                }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = LoraF32::at(xv[q], i);
+                bf16x8 xs[3];
+                split8<3>(f, xs);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    if (c < chunks) {
+                        bf16x8 as[LoraParts<Ty>::N];
+                        LoraParts<Ty>::get(av[c][q], 8, as);
+                        acc[c] = mfma_parts(xs, as, acc[c]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+            if (c < chunks)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sums[wv][16 * c + i][lane] = acc[c][i];
+        __syncthreads();
+        for (int e = wv; e < 16 * chunks; e += 4) {
+            const int i = e & 15, c = c0 + 32 * (e >> 4) + col;
+            const int row = 8 * (i >> 2) + 4 * half + (i & 3);
+            const float v = (sums[0][e][lane] + sums[1][e][lane]) + (sums[2][e][lane] + sums[3][e][lane]);
+            // products past the adapter's own rank (whatever A holds there) are 0
+            if (c < cols && row < rows)
+                u[((int64_t)blockIdx.y * m + ids[row]) * cols + c] = c % lo.rank < r ? v * sc : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+// Outputs [j0, j1) whose rows of B belong to one section (SILU: gate rows to one, up rows to
+// one), in blocks of 256.
+struct LoraSpans {
+    int n;
+    int64_t begin[2 * Q8_LORA_MAX_SECTIONS + 1];
+    int block[2 * Q8_LORA_MAX_SECTIONS + 1];  // first block
+};
+
+template <class Ty, bool SILU>
+__global__ __launch_bounds__(256) void lora_outer_kernel(LoraArgs lo, LoraPlan P, const float* __restrict__ u, int parts,
+                                                         int m, const float* y, int64_t n, int64_t ldy, float* out,
+                                                         int64_t ldo, LoraSpans S) {
+    constexpr int kSides = SILU ? 2 : 1;
+    constexpr int kN = LoraParts<Ty>::N;
+    // u split: [side][part][k group of 8][row][8]
+    __shared__ bf16x8 us[kSides][3][kRankChunk / 8][kRowTile];
+    __shared__ int ids[kRowTile];
+    if ((int)blockIdx.x >= *P.n_tiles) return;
+    const int4 tile = P.tiles[blockIdx.x];
+    const int a = tile.x, rows = tile.z;
+    int sp = 0;
+    while (sp + 1 < S.n && (int)blockIdx.y >= S.block[sp + 1]) ++sp;
+    const int64_t n_out = SILU ? n / 2 : n;
+    const int64_t j0 = S.begin[sp] + 256 * (int64_t)((int)blockIdx.y - S.block[sp]);
+    const int64_t j1 = min(S.begin[sp + 1], j0 + 256);
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, half = lane >> 5, col = lane & 31;
+    if (tid < kRowTile) ids[tid] = P.sorted[tile.y + min(tid, rows - 1)];
+    __syncthreads();
+    f32x16 acc[kSides][2][2];  // [row half][column half]
+#pragma unroll
+    for (int s = 0; s < kSides; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[s][i >> 1][i & 1][e] = 0.0f;
+    if (a < lo.n_adapters) {
+        const int cols = lo.n_sections * lo.rank, r = lo.rank_of(a);
+        for (int k0 = 0; k0 < r; k0 += kRankChunk) {
+            const int groups = (min(kRankChunk, r - k0) + 7) >> 3, pairs = (groups + 1) >> 1;
+            if (k0) __syncthreads();
+            for (int i = tid; i < kSides * 2 * pairs * kRowTile; i += 256) {
+                const int row = i & (kRowTile - 1), q = (i / kRowTile) % (2 * pairs), s = i / (kRowTile * 2 * pairs);
+                const int sec = lo.section(s * n_out + j0);
+                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (q < groups)
+                    for (int p = 0; p < parts; ++p) {
+                        const LoraF32::V v =
+                            LoraF32::load8(u + ((int64_t)p * m + ids[row]) * cols + sec * lo.rank + k0 + 8 * q);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] += LoraF32::at(v, e);
+                    }
+                bf16x8 sv[3];
+                split8<3>(f, sv);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) us[s][p][q][row] = sv[p];
+            }
+            __syncthreads();
+            for (int g = 0; g < pairs; ++g) {
+#pragma unroll
+                for (int s = 0; s < kSides; ++s) {
+                    bf16x8 b[2][kN];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int64_t j = min(j0 + 64 * wv + 32 * c + col, j1 - 1);
+                        const int kk = k0 + 16 * g + 8 * half;  // entries past the adapter's rank count as 0
+                        const typename Ty::T* p =
+                            static_cast<const typename Ty::T*>(lo.b) + ((size_t)a * n + s * n_out + j) * lo.rank;
+                        LoraParts<Ty>::get(Ty::load8(p + min(kk, lo.rank - 8)), r - kk, b[c]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        bf16x8 av[3];
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) av[p] = us[s][p][2 * g + half][32 * h + col];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) acc[s][h][c] = mfma_parts(av, b[c], acc[s][h][c]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int64_t j = j0 + 64 * wv + 32 * c + col;
+            if (j >= j1) continue;
+            float g[16], v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
+                const float* p = y + (int64_t)ids[min(row, rows - 1)] * ldy + j;
+                g[e] = *p;
+                if constexpr (SILU) v[e] = p[n_out];
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
+                g[e] += acc[0][h][c][e];
+                if constexpr (SILU) g[e] = silu_mul(g[e], v[e] + acc[1][h][c][e]);
+                if (row < rows) out[(int64_t)ids[row] * ldo + j] = g[e];
+            }
+        }
+}
+
 static LoraArgs lora_args(const q8_lora& lo) {
     LoraArgs a{lo.a, lo.b, lo.ranks, lo.scale, lo.adapter, lo.type, lo.n_adapters, lo.rank, lo.n_sections, {}};
     int64_t end = 0;
@@ -317,16 +625,74 @@ static hipError_t lora_add_typed(const LoraArgs& lo, const float* y, int64_t n, 
     return hipGetLastError();
 }
 
+template <class Ty>
+static hipError_t lora_add_tiled(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu, const float* x,
+                                 int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, char* ws,
+                                 const q8v::LoraWorkspace& L, hipStream_t stream) {
+    float* u = reinterpret_cast<float*>(ws + L.u_off);
+    const LoraPlan P{reinterpret_cast<int32_t*>(ws + L.sorted_off), reinterpret_cast<int4*>(ws + L.tiles_off),
+                     reinterpret_cast<int32_t*>(ws + L.count_off)};
+    hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, stream, lo, (int)m, P);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const unsigned tiles = (unsigned)q8v::lora_max_tiles(m, lo.n_adapters);
+    const int64_t steps = k / 64;
+    const int parts = (int)(q8v::lora_parts(m) * 4 <= steps ? q8v::lora_parts(m) : (steps + 3) / 4);
+    hipLaunchKernelGGL(lora_inner_kernel<Ty>, dim3(2 * tiles, (unsigned)parts), dim3(256), 0, stream, lo, P, x, (int)m,
+                       (int)k, ldx, u);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // the outputs' spans: cut at every section's end, and (SILU) at those of the up rows
+    const int64_t n_out = silu ? n / 2 : n;
+    int64_t cuts[2 * Q8_LORA_MAX_SECTIONS + 2];
+    int nc = 0;
+    cuts[nc++] = 0;
+    cuts[nc++] = n_out;
+    for (int s = 0; s < lo.n_sections; ++s)
+        for (int64_t c : {lo.end[s], lo.end[s] - n_out})
+            if (c > 0 && c < n_out) cuts[nc++] = c;
+    std::sort(cuts, cuts + nc);
+    nc = (int)(std::unique(cuts, cuts + nc) - cuts);
+    LoraSpans S{};
+    S.n = nc - 1;
+    int blocks = 0;
+    for (int i = 0; i < nc; ++i) {
+        S.begin[i] = cuts[i];
+        S.block[i] = blocks;
+        if (i + 1 < nc) blocks += (int)((cuts[i + 1] - cuts[i] + 255) / 256);
+    }
+    const dim3 grid(tiles, (unsigned)blocks);
+    if (silu)
+        hipLaunchKernelGGL((lora_outer_kernel<Ty, true>), grid, dim3(256), 0, stream, lo, P, u, parts, (int)m, y, n, ldy,
+                           out, ldo, S);
+    else
+        hipLaunchKernelGGL((lora_outer_kernel<Ty, false>), grid, dim3(256), 0, stream, lo, P, u, parts, (int)m, y, n,
+                           ldy, out, ldo, S);
+    return hipGetLastError();
+}
+
+// From this many rows on the matrix-core form.
+constexpr int64_t kLoraTiledRows = 48;
+
+template <class Ty>
+static hipError_t lora_add_any(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu, const float* x,
+                               int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, char* ws,
+                               const q8v::LoraWorkspace& L, hipStream_t stream) {
+    if (m >= kLoraTiledRows && n <= q8v::kLoraTiledMaxOutputs)
+        return lora_add_tiled<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, ws, L, stream);
+    return lora_add_typed<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, reinterpret_cast<float*>(ws + L.u_off), stream);
+}
+
 hipError_t launch_lora_add(const DeviceInfo&, const float* y, int64_t n, int64_t ldy, bool silu_pairs,
                            const float* x, int64_t m, int64_t k, int64_t ldx, const q8_lora& lora, float* out,
                            int64_t ldo, void* workspace, hipStream_t stream) {
     const LoraArgs lo = lora_args(lora);
     const q8v::LoraWorkspace L = q8v::lora_workspace_layout(m, lora.n_sections, lora.rank, 0);
-    float* u = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.u_off);
+    char* ws = static_cast<char*>(workspace);
     switch (lora.type) {
-        case Q8_LORA_F32: return lora_add_typed<LoraF32>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, u, stream);
-        case Q8_LORA_F16: return lora_add_typed<LoraF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, u, stream);
-        default: return lora_add_typed<LoraBF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, u, stream);
+        case Q8_LORA_F32: return lora_add_any<LoraF32>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
+        case Q8_LORA_F16: return lora_add_any<LoraF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
+        default: return lora_add_any<LoraBF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
     }
 }
 

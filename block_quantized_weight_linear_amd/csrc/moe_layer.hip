@@ -398,20 +398,6 @@ __device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Inclusive prefix sums over the wave: within rows of 16, then the rows before.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {
-    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-    v = dpp_add<0x111, 0xF>(v);
-    v = dpp_add<0x112, 0xF>(v);
-    v = dpp_add<0x114, 0xF>(v);
-    v = dpp_add<0x118, 0xF>(v);
-    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
-    return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
-}
-
 // Softmax, top-k choice (k <= 64) and top-p cut of one token on one wave, n_exp <= 64 NP: what
 // route_topk.hip's select_topk chooses, to the bit, with the choice made on integer keys
 // (about a quarter of its time) and the chosen experts' probabilities

@@ -235,23 +235,30 @@ inline bool lora_sizes_valid(const q8_lora& lo) {
 // shared product is q8_linear's, on the bf16 matrix cores.
 constexpr int64_t kPrefillRows = 256;
 
-// Workspace of the adapter calls: the inner products u [m][n_sections * rank], the rows
-// sorted by adapter; the packed calls add what their shared product needs.
+// The matrix-core form of the correction (many rows): rows sorted by adapter in tiles of 64,
+// the inner products in parts of k (enough blocks for few tiles).  Outputs: one grid's worth.
+constexpr int64_t kLoraTiledMaxOutputs = int64_t(1) << 23;
+inline int64_t lora_max_tiles(int64_t m, int64_t n_adapters) { return m / 64 + n_adapters + 1; }
+inline int64_t lora_parts(int64_t m) {
+    const int64_t tiles = (m + 31) / 32;
+    return tiles >= 256 ? 1 : tiles > 64 ? (256 + tiles - 1) / tiles : 4;
+}
+
+// Workspace of the adapter calls: the inner products u [parts][m][n_sections * rank], the rows
+// sorted by adapter and their tiles; the packed calls add what their shared product needs.
 struct LoraWorkspace {
-    size_t u_off, offsets_off, sorted_off, inv_off, active_off, tiles_off, base_off, total;
+    size_t u_off, sorted_off, tiles_off, count_off, base_off, total;
 };
 
 inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_t rank, size_t base_bytes) {
     LoraWorkspace w{};
-    const size_t ints = sizeof(int32_t) * size_t(kLoraMaxAdapters + 1);
     size_t off = 0;
-    w.u_off = off;       off = round_up(off + sizeof(float) * size_t(m) * size_t(n_sections) * size_t(rank), 256);
-    w.offsets_off = off; off = round_up(off + ints, 256);
-    w.sorted_off = off;  off = round_up(off + sizeof(int32_t) * size_t(m), 256);
-    w.inv_off = off;     off = round_up(off + sizeof(int32_t) * size_t(m), 256);
-    w.active_off = off;  off = round_up(off + ints, 256);
-    w.tiles_off = off;   off = round_up(off + ints, 256);
-    w.base_off = off;    off = round_up(off + base_bytes, 256);
+    w.u_off = off;
+    off = round_up(off + sizeof(float) * size_t(lora_parts(m)) * size_t(m) * size_t(n_sections) * size_t(rank), 256);
+    w.sorted_off = off; off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+    w.tiles_off = off;  off = round_up(off + 16 * size_t(lora_max_tiles(m, kLoraMaxAdapters)), 256);
+    w.count_off = off;  off = round_up(off + sizeof(int32_t), 256);
+    w.base_off = off;   off = round_up(off + base_bytes, 256);
     w.total = off;
     return w;
 }

@@ -1,5 +1,6 @@
-// Cross-lane sums and maxima of a wave on the DPP network (gfx950), shared by the routers and
-// the whole mixture-of-experts layer: the softmax of a token has the same bits in both.
+// Cross-lane sums, maxima and prefix sums of a wave on the DPP network (gfx950).  The routers
+// and the whole mixture-of-experts layer share them: the softmax of a token has the same bits
+// in both.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -43,6 +44,20 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dpp_f<kDppHalfMirror>(v);
     v += dpp_f<kDppMirror>(v);
     return ((lane_f(v, 0) + lane_f(v, 16)) + lane_f(v, 32)) + lane_f(v, 48);
+}
+
+// Inclusive prefix sums over the wave: within rows of 16, then the rows before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
 }
 
 }  // namespace q8k
