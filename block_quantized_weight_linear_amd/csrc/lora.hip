@@ -301,9 +301,10 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 //   1. plan:   the rows sorted by adapter (those without one last), in tiles of 64 rows.
 //   2. inner:  block (tile half of 32 rows, part of k): u of all sections' ranks; its four
 //              waves take 64-wide steps of k in turn and add up through LDS.  The parts of k
-//              give the few tiles enough blocks; u is kept apart for each.
-//   3. outer:  block (tile, 256 outputs): the parts of u added up in order, split and staged
-//              in LDS, then 64 x 64 outputs a wave, added to the product (or activated).
+//              give the few tiles enough blocks.
+//   3. sum:    the parts added up, scaled and split, laid out as the next launch's operand.
+//   4. outer:  block (tile, 128 outputs), 64 rows x 32 outputs a wave: u and B start out,
+//              then the product's values, and no barrier lies between.
 // Bound by the memory: x once, the product in and out.
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -311,7 +312,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowTile = 64;
-constexpr int kRankChunk = 64;  // of u staged at a time
 
 // Eight values as PARTS bf16 vectors that add up to them.
 template <int PARTS>
@@ -375,6 +375,7 @@ __device__ __forceinline__ f32x16 mfma_parts(const bf16x8 (&a)[3], const bf16x8 
 
 // Rows by adapter: sorted [m], and the tiles: adapter (n_adapters: none), first place, rows.
 struct LoraPlan {
+    bf16x8* split;         // [tile][3 parts][cols / 8][64 rows]
     int32_t* sorted;
     int4* tiles;
     int32_t* n_tiles;
@@ -411,8 +412,10 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs lo, int m, Lor
     }
     __syncthreads();
     if (tid <= lo.n_adapters)
-        for (int i = 0; i < count[tid]; i += kRowTile)
-            P.tiles[tile_at[tid] + i / kRowTile] = make_int4(tid, at[tid] + i, min(kRowTile, count[tid] - i), 0);
+        for (int i = 0; i < count[tid]; i += kRowTile) {
+            const int t = tile_at[tid] + i / kRowTile;
+            P.tiles[t] = make_int4(tid, at[tid] + i, min(kRowTile, count[tid] - i), 0);
+        }
     __syncthreads();
     // the order within an adapter is free: a row's result does not depend on its tile
     for (int t = tid; t < m; t += 1024) P.sorted[atomicAdd(&at[bin(t)], 1)] = t;
@@ -426,14 +429,14 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(LoraArgs lo, LoraPlan P
     if ((int)(blockIdx.x >> 1) >= *P.n_tiles) return;
     const int4 tile = P.tiles[blockIdx.x >> 1];
     const int a = tile.x, rows = min(32, tile.z - 32 * (int)(blockIdx.x & 1));
-    if (a >= lo.n_adapters || rows <= 0) return;
+    if (a >= lo.n_adapters || rows <= 0) return;  // all parts alike
     const int32_t* ids = P.sorted + tile.y + 32 * (blockIdx.x & 1);
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
-    const int cols = lo.n_sections * lo.rank, r = lo.rank_of(a);
-    const float sc = lo.scale ? lo.scale[a] : 1.0f;
-    // a lane's k within a step of 64: 32 consecutive ones, eight for each of four instructions
-    const float* xr = x + (int64_t)ids[min(col, rows - 1)] * ldx + 32 * half;
-    const typename Ty::T* ab = static_cast<const typename Ty::T*>(lo.a) + (size_t)a * cols * k + 32 * half;
+    const int cols = lo.n_sections * lo.rank;
+    // a lane's k of instruction q within a step of 64: 16 q + 8 half, so that a load
+    // instruction takes neighbouring bytes of every row
+    const float* xr = x + (int64_t)ids[min(col, rows - 1)] * ldx + 8 * half;
+    const typename Ty::T* ab = static_cast<const typename Ty::T*>(lo.a) + (size_t)a * cols * k + 8 * half;
     const int steps = k >> 6;
     const int s0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
     for (int c0 = 0; c0 < cols; c0 += 32 * kChunks) {
@@ -445,16 +448,16 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(LoraArgs lo, LoraPlan P
             for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
         for (int st = s0 + wv; st < s1; st += 4) {
             LoraF32::V xv[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) xv[q] = LoraF32::load8(xr + 64 * st + 8 * q);
             typename Ty::V av[kChunks][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xv[q] = LoraF32::load8(xr + 64 * st + 16 * q);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 if (c < chunks) {
                     // a column past the last one repeats it
                     const typename Ty::T* p = ab + (size_t)min(c0 + 32 * c + col, cols - 1) * k + 64 * st;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) av[c][q] = Ty::load8(p + 8 * q);
+                    for (int q = 0; q < 4; ++q) av[c][q] = Ty::load8(p + 16 * q);
                 }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -482,116 +485,139 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(LoraArgs lo, LoraPlan P
             const int i = e & 15, c = c0 + 32 * (e >> 4) + col;
             const int row = 8 * (i >> 2) + 4 * half + (i & 3);
             const float v = (sums[0][e][lane] + sums[1][e][lane]) + (sums[2][e][lane] + sums[3][e][lane]);
-            // products past the adapter's own rank (whatever A holds there) are 0
-            if (c < cols && row < rows)
-                u[((int64_t)blockIdx.y * m + ids[row]) * cols + c] = c % lo.rank < r ? v * sc : 0.0f;
+            if (c < cols && row < rows) u[((int64_t)blockIdx.y * m + ids[row]) * cols + c] = v;
         }
         __syncthreads();
     }
 }
 
-// Outputs [j0, j1) whose rows of B belong to one section (SILU: gate rows to one, up rows to
-// one), in blocks of 256.
+// u of a tile, its parts of k added up in their order, scaled and split.
+__global__ __launch_bounds__(256) void lora_sum_kernel(LoraArgs lo, LoraPlan P, const float* __restrict__ u, int parts,
+                                                       int m) {
+    if ((int)blockIdx.x >= *P.n_tiles) return;
+    const int4 tile = P.tiles[blockIdx.x];
+    if (tile.x >= lo.n_adapters) return;
+    const int cols = lo.n_sections * lo.rank, groups = cols >> 3, r = lo.rank_of(tile.x);
+    const float sc = lo.scale ? lo.scale[tile.x] : 1.0f;
+    const int row = threadIdx.x & (kRowTile - 1);
+    const float* ur = u + (int64_t)P.sorted[tile.y + min(row, tile.z - 1)] * cols;
+    const int64_t part = (int64_t)m * cols;
+    for (int g = (threadIdx.x >> 6) + 4 * blockIdx.y; g < groups; g += 4 * gridDim.y) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            LoraF32::V v[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) v[p] = LoraF32::load8(ur + 8 * g + min(p0 + p, parts - 1) * part);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (p0 + p < parts)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] += LoraF32::at(v[p], e);
+        }
+        // products past the adapter's own rank (whatever A holds there) are 0
+        const int j = 8 * g % lo.rank;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = j + e < r ? f[e] * sc : 0.0f;
+        bf16x8 sv[3];
+        split8<3>(f, sv);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) P.split[(((int64_t)blockIdx.x * 3 + p) * groups + g) * kRowTile + row] = sv[p];
+    }
+}
+
+constexpr int kOuterColumns = 128;  // outputs of a block, 32 a wave
+
+// Outputs whose rows of B belong to one section (SILU: gate rows to one, up rows to one), in
+// blocks of kOuterColumns.
 struct LoraSpans {
     int n;
     int64_t begin[2 * Q8_LORA_MAX_SECTIONS + 1];
-    int block[2 * Q8_LORA_MAX_SECTIONS + 1];  // first block
+    int block[2 * Q8_LORA_MAX_SECTIONS + 1];  // first block; [n]: their number
 };
 
 template <class Ty, bool SILU>
-__global__ __launch_bounds__(256) void lora_outer_kernel(LoraArgs lo, LoraPlan P, const float* __restrict__ u, int parts,
-                                                         int m, const float* y, int64_t n, int64_t ldy, float* out,
-                                                         int64_t ldo, LoraSpans S) {
+__global__ __launch_bounds__(256) void lora_outer_kernel(LoraArgs lo, LoraPlan P, const float* y, int64_t n, int64_t ldy,
+                                                         float* out, int64_t ldo, LoraSpans S) {
     constexpr int kSides = SILU ? 2 : 1;
     constexpr int kN = LoraParts<Ty>::N;
-    // u split: [side][part][k group of 8][row][8]
-    __shared__ bf16x8 us[kSides][3][kRankChunk / 8][kRowTile];
-    __shared__ int ids[kRowTile];
-    if ((int)blockIdx.x >= *P.n_tiles) return;
-    const int4 tile = P.tiles[blockIdx.x];
+    // neighbouring blocks take neighbouring outputs of the same rows: the memory sees whole rows
+    const int row_tile = blockIdx.x / S.block[S.n], part = blockIdx.x - row_tile * S.block[S.n];
+    if (row_tile >= *P.n_tiles) return;
+    const int4 tile = P.tiles[row_tile];
     const int a = tile.x, rows = tile.z;
+    const int32_t* ids = P.sorted + tile.y;
     int sp = 0;
-    while (sp + 1 < S.n && (int)blockIdx.y >= S.block[sp + 1]) ++sp;
+    while (sp + 1 < S.n && part >= S.block[sp + 1]) ++sp;
     const int64_t n_out = SILU ? n / 2 : n;
-    const int64_t j0 = S.begin[sp] + 256 * (int64_t)((int)blockIdx.y - S.block[sp]);
-    const int64_t j1 = min(S.begin[sp + 1], j0 + 256);
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, half = lane >> 5, col = lane & 31;
-    if (tid < kRowTile) ids[tid] = P.sorted[tile.y + min(tid, rows - 1)];
-    __syncthreads();
-    f32x16 acc[kSides][2][2];  // [row half][column half]
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
+    const int64_t j1 = S.begin[sp + 1];
+    const int64_t j = S.begin[sp] + kOuterColumns * (int64_t)(part - S.block[sp]) + 32 * wv + col;
+    const int64_t jc = min(j, j1 - 1);  // a lane past the span repeats its last output, not stored
+    const bool with = a < lo.n_adapters;
+    const int r = with ? lo.rank_of(a) : 0, pairs = (r + 15) >> 4;
+
+    // operands of k pair g: u of both row halves, B's row (entries past the adapter's rank as 0)
+    const int groups = lo.n_sections * lo.rank >> 3;
+    const bf16x8* ua[kSides];
+    const typename Ty::T* bp[kSides];
+#pragma unroll
+    for (int s = 0; s < kSides; ++s) {
+        const int sec = lo.section(s * n_out + S.begin[sp]);
+        ua[s] = P.split + ((int64_t)row_tile * 3 * groups + sec * (lo.rank >> 3)) * kRowTile + col;
+        bp[s] = static_cast<const typename Ty::T*>(lo.b) + ((size_t)(with ? a : 0) * n + s * n_out + jc) * lo.rank;
+    }
+    bf16x8 av[kSides][2][3];
+    typename Ty::V bv[kSides];
+    auto load = [&](int g) __attribute__((always_inline)) {
+        const int q = min(2 * g + half, (lo.rank >> 3) - 1);
+#pragma unroll
+        for (int s = 0; s < kSides; ++s) {
+            bv[s] = Ty::load8(bp[s] + 8 * q);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < 3; ++p) av[s][h][p] = ua[s][((int64_t)p * groups + q) * kRowTile + 32 * h];
+        }
+    };
+    if (pairs) load(0);
+    // then the product's values; the lane's rows of the tile: 32 h + 8 (e / 4) + 4 half + e % 4
+    float py[kSides][2][16];
+    int id[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) id[h][e] = ids[min(32 * h + 8 * (e >> 2) + 4 * half + (e & 3), rows - 1)];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int s = 0; s < kSides; ++s) py[s][h][e] = y[(int64_t)id[h][e] * ldy + s * n_out + jc];
+    f32x16 acc[kSides][2];
 #pragma unroll
     for (int s = 0; s < kSides; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[s][i >> 1][i & 1][e] = 0.0f;
-    if (a < lo.n_adapters) {
-        const int cols = lo.n_sections * lo.rank, r = lo.rank_of(a);
-        for (int k0 = 0; k0 < r; k0 += kRankChunk) {
-            const int groups = (min(kRankChunk, r - k0) + 7) >> 3, pairs = (groups + 1) >> 1;
-            if (k0) __syncthreads();
-            for (int i = tid; i < kSides * 2 * pairs * kRowTile; i += 256) {
-                const int row = i & (kRowTile - 1), q = (i / kRowTile) % (2 * pairs), s = i / (kRowTile * 2 * pairs);
-                const int sec = lo.section(s * n_out + j0);
-                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (q < groups)
-                    for (int p = 0; p < parts; ++p) {
-                        const LoraF32::V v =
-                            LoraF32::load8(u + ((int64_t)p * m + ids[row]) * cols + sec * lo.rank + k0 + 8 * q);
+            for (int e = 0; e < 16; ++e) acc[s][h][e] = 0.0f;
+    for (int g = 0; g < pairs; ++g) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] += LoraF32::at(v, e);
-                    }
-                bf16x8 sv[3];
-                split8<3>(f, sv);
+        for (int s = 0; s < kSides; ++s) {
+            bf16x8 b[kN];
+            LoraParts<Ty>::get(bv[s], r - 16 * g - 8 * half, b);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) us[s][p][q][row] = sv[p];
-            }
-            __syncthreads();
-            for (int g = 0; g < pairs; ++g) {
-#pragma unroll
-                for (int s = 0; s < kSides; ++s) {
-                    bf16x8 b[2][kN];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int64_t j = min(j0 + 64 * wv + 32 * c + col, j1 - 1);
-                        const int kk = k0 + 16 * g + 8 * half;  // entries past the adapter's rank count as 0
-                        const typename Ty::T* p =
-                            static_cast<const typename Ty::T*>(lo.b) + ((size_t)a * n + s * n_out + j) * lo.rank;
-                        LoraParts<Ty>::get(Ty::load8(p + min(kk, lo.rank - 8)), r - kk, b[c]);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        bf16x8 av[3];
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) av[p] = us[s][p][2 * g + half][32 * h + col];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) acc[s][h][c] = mfma_parts(av, b[c], acc[s][h][c]);
-                    }
-                }
-            }
+            for (int h = 0; h < 2; ++h) acc[s][h] = mfma_parts(av[s][h], b, acc[s][h]);
         }
+        if (g + 1 < pairs) load(g + 1);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int64_t j = j0 + 64 * wv + 32 * c + col;
-            if (j >= j1) continue;
-            float g[16], v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
-                const float* p = y + (int64_t)ids[min(row, rows - 1)] * ldy + j;
-                g[e] = *p;
-                if constexpr (SILU) v[e] = p[n_out];
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
-                g[e] += acc[0][h][c][e];
-                if constexpr (SILU) g[e] = silu_mul(g[e], v[e] + acc[1][h][c][e]);
-                if (row < rows) out[(int64_t)ids[row] * ldo + j] = g[e];
-            }
+        for (int e = 0; e < 16; ++e) {
+            const int row = 32 * h + 8 * (e >> 2) + 4 * half + (e & 3);
+            float v = py[0][h][e] + acc[0][h][e];
+            if constexpr (SILU) v = silu_mul(v, py[1][h][e] + acc[1][h][e]);
+            if (row < rows && j < j1) out[(int64_t)id[h][e] * ldo + j] = v;
         }
 }
 
@@ -630,16 +656,22 @@ static hipError_t lora_add_tiled(const LoraArgs& lo, const float* y, int64_t n, 
                                  int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, char* ws,
                                  const q8v::LoraWorkspace& L, hipStream_t stream) {
     float* u = reinterpret_cast<float*>(ws + L.u_off);
-    const LoraPlan P{reinterpret_cast<int32_t*>(ws + L.sorted_off), reinterpret_cast<int4*>(ws + L.tiles_off),
+    const LoraPlan P{reinterpret_cast<bf16x8*>(ws + L.split_off),
+                     reinterpret_cast<int32_t*>(ws + L.sorted_off), reinterpret_cast<int4*>(ws + L.tiles_off),
                      reinterpret_cast<int32_t*>(ws + L.count_off)};
     hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, stream, lo, (int)m, P);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)q8v::lora_max_tiles(m, lo.n_adapters);
     const int64_t steps = k / 64;
-    const int parts = (int)(q8v::lora_parts(m) * 4 <= steps ? q8v::lora_parts(m) : (steps + 3) / 4);
+    const int parts = (int)(q8v::lora_parts(m) * 4 <= steps ? q8v::lora_parts(m) : (steps + 3) / 4);  // a step a wave at least
     hipLaunchKernelGGL(lora_inner_kernel<Ty>, dim3(2 * tiles, (unsigned)parts), dim3(256), 0, stream, lo, P, x, (int)m,
                        (int)k, ldx, u);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int groups = lo.n_sections * lo.rank / 8;
+    hipLaunchKernelGGL(lora_sum_kernel, dim3(tiles, (unsigned)((groups + 3) / 4)), dim3(256), 0, stream, lo, P, u,
+                       parts, (int)m);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     // the outputs' spans: cut at every section's end, and (SILU) at those of the up rows
@@ -659,26 +691,21 @@ static hipError_t lora_add_tiled(const LoraArgs& lo, const float* y, int64_t n, 
     for (int i = 0; i < nc; ++i) {
         S.begin[i] = cuts[i];
         S.block[i] = blocks;
-        if (i + 1 < nc) blocks += (int)((cuts[i + 1] - cuts[i] + 255) / 256);
+        if (i + 1 < nc) blocks += (int)((cuts[i + 1] - cuts[i] + kOuterColumns - 1) / kOuterColumns);
     }
-    const dim3 grid(tiles, (unsigned)blocks);
+    const dim3 grid(tiles * (unsigned)blocks);
     if (silu)
-        hipLaunchKernelGGL((lora_outer_kernel<Ty, true>), grid, dim3(256), 0, stream, lo, P, u, parts, (int)m, y, n, ldy,
-                           out, ldo, S);
+        hipLaunchKernelGGL((lora_outer_kernel<Ty, true>), grid, dim3(256), 0, stream, lo, P, y, n, ldy, out, ldo, S);
     else
-        hipLaunchKernelGGL((lora_outer_kernel<Ty, false>), grid, dim3(256), 0, stream, lo, P, u, parts, (int)m, y, n,
-                           ldy, out, ldo, S);
+        hipLaunchKernelGGL((lora_outer_kernel<Ty, false>), grid, dim3(256), 0, stream, lo, P, y, n, ldy, out, ldo, S);
     return hipGetLastError();
 }
-
-// From this many rows on the matrix-core form.
-constexpr int64_t kLoraTiledRows = 48;
 
 template <class Ty>
 static hipError_t lora_add_any(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu, const float* x,
                                int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, char* ws,
                                const q8v::LoraWorkspace& L, hipStream_t stream) {
-    if (m >= kLoraTiledRows && n <= q8v::kLoraTiledMaxOutputs)
+    if (m >= q8v::kLoraTiledRows && n <= q8v::kLoraTiledMaxOutputs)
         return lora_add_tiled<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, ws, L, stream);
     return lora_add_typed<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, reinterpret_cast<float*>(ws + L.u_off), stream);
 }

@@ -238,16 +238,18 @@ constexpr int64_t kPrefillRows = 256;
 // The matrix-core form of the correction (many rows): rows sorted by adapter in tiles of 64,
 // the inner products in parts of k (enough blocks for few tiles).  Outputs: one grid's worth.
 constexpr int64_t kLoraTiledMaxOutputs = int64_t(1) << 23;
-inline int64_t lora_max_tiles(int64_t m, int64_t n_adapters) { return m / 64 + n_adapters + 1; }
+constexpr int64_t kLoraTiledRows = 48;
+inline int64_t lora_max_tiles(int64_t m, int64_t n_adapters) { return m / 64 + (m < n_adapters + 1 ? m : n_adapters + 1); }
 inline int64_t lora_parts(int64_t m) {
+    if (m < kLoraTiledRows) return 1;
     const int64_t tiles = (m + 31) / 32;
-    return tiles >= 256 ? 1 : tiles > 64 ? (256 + tiles - 1) / tiles : 4;
+    return tiles >= 512 ? 1 : tiles > 64 ? (512 + tiles - 1) / tiles : 8;
 }
 
 // Workspace of the adapter calls: the inner products u [parts][m][n_sections * rank], the rows
 // sorted by adapter and their tiles; the packed calls add what their shared product needs.
 struct LoraWorkspace {
-    size_t u_off, sorted_off, tiles_off, count_off, base_off, total;
+    size_t u_off, split_off, sorted_off, tiles_off, count_off, base_off, total;
 };
 
 inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_t rank, size_t base_bytes) {
@@ -255,8 +257,11 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
     size_t off = 0;
     w.u_off = off;
     off = round_up(off + sizeof(float) * size_t(lora_parts(m)) * size_t(m) * size_t(n_sections) * size_t(rank), 256);
+    const size_t tiles = m < kLoraTiledRows ? 0 : size_t(lora_max_tiles(m, kLoraMaxAdapters));
+    // u split in three bf16 parts, by tiles of 64 rows
+    w.split_off = off;  off = round_up(off + 6 * 64 * tiles * size_t(n_sections) * size_t(rank), 256);
     w.sorted_off = off; off = round_up(off + sizeof(int32_t) * size_t(m), 256);
-    w.tiles_off = off;  off = round_up(off + 16 * size_t(lora_max_tiles(m, kLoraMaxAdapters)), 256);
+    w.tiles_off = off;  off = round_up(off + 16 * tiles, 256);
     w.count_off = off;  off = round_up(off + sizeof(int32_t), 256);
     w.base_off = off;   off = round_up(off + base_bytes, 256);
     w.total = off;
