@@ -168,6 +168,9 @@ def _rows_out(out, m, width, name, dtype, device):
 
 
 def _contig_out(t, shape, name, dtype, device):
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        return t
     _dev(t, dtype, name, device)
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {tuple(t.shape)}")
@@ -196,6 +199,9 @@ def _quant_bytes(rows, k, bytes_256):
 
 def _call(device, fn, *args):
     # the library launches on the current device: make it the tensors' device
+    if device.index == torch.cuda.current_device():
+        check(fn(*args))
+        return
     with torch.cuda.device(device):
         check(fn(*args))
 

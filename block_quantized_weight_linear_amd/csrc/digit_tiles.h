@@ -45,8 +45,8 @@ constexpr int kRingBytes = kTileWaves * kRing * kLdsItemBytes;
 static_assert(kTileRows * kSliceBytes == kLdsItemBytes, "an item is one slice of a tile");
 
 // How a tile's S = k / 256 slices are shared: WT waves (1, 2, 4 or 8) with at most SP
-// slices each.  The fewest idle wave slices win, ties go to more waves (fewer registers),
-// and SP stays at 3 or below while S <= 24.
+// slices each, for S <= 24 at most three.  The fewest idle wave slices win, ties go to more
+// waves (fewer registers).
 struct SliceShare {
     int log2_wt, sp;
 };
@@ -202,12 +202,13 @@ __device__ __forceinline__ void write_digits(const float* __restrict__ xr, int k
     for (int i = 4 * tid + 1024 * kKeep; i < k; i += 1024) write(*reinterpret_cast<const float4*>(xr + i), i);
 }
 
-// What a wave knows about its place: its slices of a row of S, its tiles of a step.
+// What a wave knows about its place: its slices of the S from `first` on, its tiles of a step.
 struct TileWave {
-    int lane, wv, wt, tg, log2_wt, n_sl, row, grp;  // row, grp: lane & 15, lane >> 4
+    int lane, wv, wt, tg, log2_wt, n_sl, row, grp, first;  // row, grp: lane & 15, lane >> 4
     uint32_t ring_lds;
     const uint8_t* ring;
-    __device__ __forceinline__ TileWave(uint8_t* smem_ring, int S, int log2_wt_) : log2_wt(log2_wt_) {
+    __device__ __forceinline__ TileWave(uint8_t* smem_ring, int S, int log2_wt_, int first_ = 0)
+        : log2_wt(log2_wt_), first(first_) {
         lane = threadIdx.x & 63;
         wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wt = wv & ((1 << log2_wt) - 1);
@@ -241,7 +242,8 @@ __device__ __forceinline__ void load_digits(const TileWave& W, DigitsOf&& digits
         const int8_t* d = digits_of(4 * g + (W.row >> 2)) + 64 * (W.row & 3) + 16 * W.grp;
 #pragma unroll
         for (int sl = 0; sl < SP; ++sl) {
-            const int s = W.wt + (min(sl, W.n_sl - 1) << W.log2_wt);
+            // a wave without a slice (it multiplies nothing): any
+            const int s = W.first + (W.n_sl > 0 ? W.wt + (min(sl, W.n_sl - 1) << W.log2_wt) : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) a[g][sl][q] = *reinterpret_cast<const i64x2*>(d + (size_t)(4 * s + q) * 256);
         }
@@ -278,7 +280,7 @@ struct TileRun {
     }
     __device__ __forceinline__ void issue(int slot) {
         const uint8_t* tile = tile_at(min(next_tile, n_tiles - 1));
-        copy_item(tile + (size_t)(W.wt + (next_sl << W.log2_wt)) * kSliceBytes, off, W.ring_lds + slot * kLdsItemBytes);
+        copy_item(tile + (size_t)(W.first + W.wt + (next_sl << W.log2_wt)) * kSliceBytes, off, W.ring_lds + slot * kLdsItemBytes);
         if (++next_sl == W.n_sl) {
             next_sl = 0;
             next_tile += tps;

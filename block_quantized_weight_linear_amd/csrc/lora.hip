@@ -16,6 +16,7 @@
 #include "gemv_core.h"
 #include "q8_internal.h"
 #include "q8_validate.h"
+#include "shared_mem.h"
 #include "wave_dpp.h"
 
 namespace q8k {
@@ -151,8 +152,10 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs lo, const flo
 template <class Ty>
 __global__ __launch_bounds__(256) void lora_prepare_kernel(LoraArgs lo, const float* __restrict__ x, int m, int k,
                                                            int64_t ldx, float* __restrict__ u,
-                                                           int8_t* __restrict__ dig, int* __restrict__ exps) {
+                                                           int8_t* __restrict__ dig, int* __restrict__ exps,
+                                                           uint32_t* __restrict__ arrived, int counters) {
     const int b = blockIdx.x;
+    for (int i = b * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
     if (b < m)
         write_digits(x + b * ldx, k, dig + (size_t)b * k * 4, exps + b);
     else
@@ -213,7 +216,16 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs lo, const flo
 
 // Second launch of the packed calls: the shared product's tiles with the correction (and,
 // SILU, the activation) behind each.  A block owns a run of neighbouring tiles and streams
-// them once for every 4 * NG rows (blockIdx.y: every gridDim.y-th of those); a fused tile is 8 gate rows and their 8 up rows.
+// them once for every 4 * NG rows (blockIdx.y: every gridDim.y-th of those); a fused tile is
+// 8 gate rows and their 8 up rows.  A row of more than 16 slices (k > 4096) is cut into ks
+// ranges, blocks b % ks taking range b % ks of the same tiles: the digits of a range fit
+// the registers for as many tiles as the block has.  The ranges' sums then go through
+// memory, and the last block of a tile adds them up, in their order, and finishes it.
+struct TileSplit {
+    int ks, log2_wt;    // ranges; waves a tile within a range
+    float* partial;     // [row group][range][tile][NG * 64]
+    uint32_t* arrived;  // [row group][tile]: ranges there, zero before the launch
+};
 constexpr int kLoraSumTiles = 64;  // tiles * NG whose sums wait in LDS
 
 template <int NG>
@@ -223,7 +235,8 @@ constexpr size_t lora_tiles_lds() {
 
 template <int SP, int NG, bool SILU>
 __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t* __restrict__ w, int n_out, int k,
-                                                                  int log2_wt, const int8_t* __restrict__ dig,
+                                                                  TileSplit split,
+                                                                  const int8_t* __restrict__ dig,
                                                                   const int* __restrict__ exps, LoraArgs lo,
                                                                   const float* __restrict__ u, int m,
                                                                   float* __restrict__ y, int64_t ldy) {
@@ -231,12 +244,15 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     uint8_t* smem = reinterpret_cast<uint8_t*>(smem4);
     float* part = reinterpret_cast<float*>(smem + kRingBytes);
     float* sums = part + 2 * kTileWaves * NG * 64;
-    const TileWave W(smem, k >> 8, log2_wt);
+    __shared__ uint32_t before;
+    const int kz = blockIdx.x % split.ks, runs = gridDim.x / split.ks, run_id = blockIdx.x / split.ks;
+    const int s0 = (k >> 8) * kz / split.ks, s1 = (k >> 8) * (kz + 1) / split.ks;
+    const TileWave W(smem, s1 - s0, split.log2_wt, s0);
     constexpr int kOut = SILU ? kTileRows / 2 : kTileRows;  // outputs of a tile
     const uint32_t rb = (uint32_t)(k >> 5) * 34u;
     const int tiles_all = (n_out + kOut - 1) / kOut;
-    const int first = (int)((int64_t)tiles_all * blockIdx.x / gridDim.x);
-    const int tiles = (int)((int64_t)tiles_all * (blockIdx.x + 1) / gridDim.x) - first;
+    const int first = (int)((int64_t)tiles_all * run_id / runs);
+    const int tiles = (int)((int64_t)tiles_all * (run_id + 1) / runs) - first;
     // the last tile starts early enough to be whole; a matrix smaller than a tile repeats its
     // last row
     const int last_row0 = max(0, n_out - kOut);
@@ -261,8 +277,34 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
             const int nt = run.n_tiles;
             multiply_tiles<SP, NG>(run, a, part, sums);
             __syncthreads();
+            bool finish = true;
+            if (split.ks > 1) {
+                const int64_t group = m0 / (4 * NG);
+                float* mine = split.partial + ((group * split.ks + kz) * tiles_all + first + c0) * (NG * 64);
+                const int64_t range = (int64_t)tiles_all * (NG * 64);
+                for (int i = threadIdx.x; i < nt * NG * 64; i += kTileThreads) store_shared(mine + i, sums[i]);
+                wait_vmcnt_mem<0>();
+                __syncthreads();
+                if (threadIdx.x == 0)
+                    before = __hip_atomic_fetch_add(split.arrived + group * tiles_all + first + c0, 1u, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+                __syncthreads();
+                finish = (int)before == split.ks - 1;
+                if (finish)
+                    for (int i = 2 * threadIdx.x; i < nt * NG * 64; i += 2 * kTileThreads) {
+                        float2 v = load_shared(mine + i - kz * range);
+                        for (int z = 1; z < split.ks; ++z) {
+                            const float2 t = load_shared(mine + i + (z - kz) * range);
+                            v.x += t.x;
+                            v.y += t.y;
+                        }
+                        sums[i] = v.x;
+                        sums[i + 1] = v.y;
+                    }
+                __syncthreads();
+            }
             // outputs of the chunk: (row of the call, tile, output of the tile), outputs fastest
-            for (int o = threadIdx.x; o < mm * nt * kOut; o += kTileThreads) {
+            for (int o = threadIdx.x; finish && o < mm * nt * kOut; o += kTileThreads) {
                 const int r = o % kOut, q = o / kOut;
                 const int s = q / nt, tile = q - s * nt;
                 const int i = row0_of(c0 + tile) + r;
@@ -723,10 +765,36 @@ hipError_t launch_lora_add(const DeviceInfo&, const float* y, int64_t n, int64_t
     }
 }
 
+// How the packed calls cut a matrix: ranges of k (a function of the sizes and the device
+// alone, never of m), waves a tile and slices a wave within a range, runs of tiles.
+struct TileCut {
+    int ks, log2_wt, sp, runs;
+};
+static TileCut tile_cut(const DeviceInfo& dev, int64_t tiles, int64_t k) {
+    const int S = (int)(k >> 8);
+    const int least = (S + 15) / 16;
+    TileCut best{};
+    int64_t cost = 0;
+    // beyond 16 slices, of the fewest ranges and the next two the one whose busiest block has
+    // the fewest items a wave
+    for (int ks = least; ks <= (least == 1 ? 1 : least + 2); ++ks) {
+        const SliceShare sh = slice_share((S + ks - 1) / ks);
+        const int64_t runs = std::min<int64_t>(tiles, std::max(1, dev.cu_count / ks));
+        const int64_t most = (tiles + runs - 1) / runs, at_once = kTileWaves >> sh.log2_wt;
+        const int64_t items = (most + at_once - 1) / at_once * sh.sp;
+        if (!best.ks || items < cost) {
+            cost = items;
+            best = TileCut{ks, sh.log2_wt, sh.sp, (int)runs};
+        }
+    }
+    return best;
+}
+
 template <int SP, int NG, bool SILU>
-static hipError_t launch_lora_tiles(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, int log2_wt,
-                                    const int8_t* dig, const int* exps, const LoraArgs& lo, const float* u,
-                                    int64_t m, float* y, int64_t ldy, hipStream_t stream) {
+static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, int64_t m, const uint8_t* w,
+                                    int64_t n_out, int64_t k, const TileSplit& split, const int8_t* dig,
+                                    const int* exps, const LoraArgs& lo, const float* u, float* y, int64_t ldy,
+                                    hipStream_t stream) {
     auto kernel = lora_tiles_kernel<SP, NG, SILU>;
     constexpr size_t lds = lora_tiles_lds<NG>();
     static thread_local int attr_dev = -1;
@@ -738,38 +806,31 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const uint8_t* w, int
     }
     // one block per CU; a matrix with fewer tiles than half the CUs hands its row groups to
     // blocks of their own
-    const int64_t per_tile = SILU ? kTileRows / 2 : kTileRows;
-    const int64_t tiles = (n_out + per_tile - 1) / per_tile;
-    const int64_t gx = tiles < dev.cu_count ? tiles : dev.cu_count;
     const int64_t groups = (m + 4 * NG - 1) / (4 * NG);
+    const int64_t gx = (int64_t)cut.runs * cut.ks;
     const int64_t gy = dev.cu_count / gx < groups ? dev.cu_count / gx : groups;
     const dim3 grid((unsigned)gx, (unsigned)(gy < 1 ? 1 : gy));
-    hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, log2_wt, dig,
-                       exps, lo, u, (int)m, y, ldy);
+    hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, split, dig, exps, lo, u,
+                       (int)m, y, ldy);
     return hipGetLastError();
 }
 
 // Activation rows a pass takes, in fours: as many as there are, up to 128 registers a lane
 // of digits (16 a slice and four rows).
-template <int SP, bool SILU, class... Args>
-static hipError_t launch_lora_tiles_sp(const DeviceInfo& dev, int64_t m, Args... args) {
-    if constexpr (SP <= 2) {
-        if (m > 8) return launch_lora_tiles<SP, 4, SILU>(dev, args...);
-    }
-    if constexpr (SP <= 4) {
-        if (m > 4) return launch_lora_tiles<SP, 2, SILU>(dev, args...);
-    }
-    return launch_lora_tiles<SP, 1, SILU>(dev, args...);
-}
-
 template <bool SILU, class... Args>
-static hipError_t launch_lora_tiles_m(int sp, const DeviceInfo& dev, int64_t m, Args... args) {
-    if (sp <= 1) return launch_lora_tiles_sp<1, SILU>(dev, m, args...);
-    if (sp <= 2) return launch_lora_tiles_sp<2, SILU>(dev, m, args...);
-    if (sp <= 3) return launch_lora_tiles_sp<3, SILU>(dev, m, args...);
-    if (sp <= 4) return launch_lora_tiles_sp<4, SILU>(dev, m, args...);
-    if (sp <= 6) return launch_lora_tiles_sp<6, SILU>(dev, m, args...);
-    return launch_lora_tiles_sp<8, SILU>(dev, m, args...);
+static hipError_t launch_lora_tiles_m(const DeviceInfo& dev, const TileCut& cut, int64_t m, Args... args) {
+    if (cut.sp == 1) {
+        if (m > 8) return launch_lora_tiles<1, 4, SILU>(dev, cut, m, args...);
+        if (m > 4) return launch_lora_tiles<1, 2, SILU>(dev, cut, m, args...);
+        return launch_lora_tiles<1, 1, SILU>(dev, cut, m, args...);
+    }
+    if (cut.sp == 2) {
+        if (m > 8) return launch_lora_tiles<2, 4, SILU>(dev, cut, m, args...);
+        if (m > 4) return launch_lora_tiles<2, 2, SILU>(dev, cut, m, args...);
+        return launch_lora_tiles<2, 1, SILU>(dev, cut, m, args...);
+    }
+    if (m > 4) return launch_lora_tiles<3, 2, SILU>(dev, cut, m, args...);
+    return launch_lora_tiles<3, 1, SILU>(dev, cut, m, args...);
 }
 
 hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu,
@@ -790,25 +851,30 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     }
     const LoraArgs lo = lora_args(lora);
     float* u = reinterpret_cast<float*>(ws + L.u_off);
-    int* exps = reinterpret_cast<int*>(ws + L.base_off);
-    int8_t* dig = reinterpret_cast<int8_t*>(exps + q8v::kPrefillRows);
-    const int64_t units = lora.n_adapters ? m * (lora.n_sections * lora.rank / kShrinkCols) : 0;
-    const dim3 grid((unsigned)(m + units));
+    const int64_t per_tile = silu ? kTileRows / 2 : kTileRows;
+    const int64_t tiles = (n_out + per_tile - 1) / per_tile;
+    const TileCut cut = tile_cut(dev, tiles, k);
+    const q8v::LoraTilesWorkspace T = q8v::lora_tiles_workspace_layout(m, n, k);
+    int* exps = reinterpret_cast<int*>(ws + L.base_off + T.exps_off);
+    int8_t* dig = reinterpret_cast<int8_t*>(ws + L.base_off + T.dig_off);
+    TileSplit split{cut.ks, cut.log2_wt, reinterpret_cast<float*>(ws + L.base_off + T.partial_off),
+                    reinterpret_cast<uint32_t*>(ws + L.base_off + T.arrived_off)};
+    const int counters = cut.ks > 1 ? (int)(q8v::lora_row_groups(m) * tiles) : 0;
+    const int units = lora.n_adapters ? (int)m * (lora.n_sections * lora.rank / kShrinkCols) : 0;
+    const dim3 grid((unsigned)((int)m + units));
     if (lora.type == Q8_LORA_F32)
         hipLaunchKernelGGL(lora_prepare_kernel<LoraF32>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
-                           exps);
+                           exps, split.arrived, counters);
     else if (lora.type == Q8_LORA_F16)
         hipLaunchKernelGGL(lora_prepare_kernel<LoraF16>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
-                           exps);
+                           exps, split.arrived, counters);
     else
-        hipLaunchKernelGGL(lora_prepare_kernel<LoraBF16>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u,
-                           dig, exps);
+        hipLaunchKernelGGL(lora_prepare_kernel<LoraBF16>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
+                           exps, split.arrived, counters);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const SliceShare sh = slice_share((int)(k >> 8));
-    return silu ? launch_lora_tiles_m<true>(sh.sp, dev, m, w, n_out, k, sh.log2_wt, dig, exps, lo, u, m, y, ldy, stream)
-                : launch_lora_tiles_m<false>(sh.sp, dev, m, w, n_out, k, sh.log2_wt, dig, exps, lo, u, m, y, ldy,
-                                             stream);
+    return silu ? launch_lora_tiles_m<true>(dev, cut, m, w, n_out, k, split, dig, exps, lo, u, y, ldy, stream)
+                : launch_lora_tiles_m<false>(dev, cut, m, w, n_out, k, split, dig, exps, lo, u, y, ldy, stream);
 }
 
 }  // namespace q8k

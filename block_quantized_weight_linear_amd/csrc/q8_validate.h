@@ -268,17 +268,42 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
     return w;
 }
 
-// The packed calls run on the digit tiles (digit_tiles.h) below the prefill rows, for widths
-// whose digits fit a block's registers and fused matrices whose up rows lie within 32-bit
-// byte offsets of their gate rows; else on q8_linear's kernels and the correction behind them.
+// The packed calls run on the digit tiles (digit_tiles.h) below the prefill rows, up to 64
+// rows where k is cut into ranges (their sums go through the workspace), for widths up to 64
+// slices and fused matrices whose up rows lie within 32-bit byte offsets of their gate
+// rows; else on q8_linear's kernels and the correction behind them.
 constexpr int64_t kLoraTilesMaxK = 16384;
+constexpr int64_t kLoraTilesMaxRange = 16 * 256;  // of k without a cut
+constexpr int64_t kLoraMaxRanges = 6;             // at most two more than the fewest, 4
 inline bool lora_uses_tiles(int64_t m, int64_t n, int64_t k) {
-    return m < kPrefillRows && k <= kLoraTilesMaxK && n * row_bytes(k) < (int64_t(1) << 31);
+    return m < kPrefillRows && (k <= kLoraTilesMaxRange || m <= 64) && k <= kLoraTilesMaxK &&
+           n * row_bytes(k) < (int64_t(1) << 31);
+}
+// Row groups of four, as many as any form has.
+inline int64_t lora_row_groups(int64_t m) { return (m + 3) / 4; }
+
+// Workspace behind the adapters', from its start: the rows' exponents and digits, and for a
+// cut k the ranges' sums and their counts (a tile: 16 rows of the matrix).
+struct LoraTilesWorkspace {
+    size_t exps_off, dig_off, partial_off, arrived_off, total;
+};
+inline LoraTilesWorkspace lora_tiles_workspace_layout(int64_t m, int64_t n, int64_t k) {
+    LoraTilesWorkspace w{};
+    const bool cut = k > kLoraTilesMaxRange;
+    const size_t tiles = size_t((n + 15) / 16 + 1);  // + 1: gate and up rows round up apart
+    const size_t rows = size_t((m + 15) / 16 * 16);
+    size_t off = 0;
+    w.exps_off = off;    off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+    w.dig_off = off;     off = round_up(off + 4 * size_t(m) * size_t(k), 256);
+    w.partial_off = off; off = round_up(off + (cut ? sizeof(float) * size_t(kLoraMaxRanges) * tiles * 16 * rows : 0), 256);
+    w.arrived_off = off; off = round_up(off + (cut ? sizeof(uint32_t) * size_t(lora_row_groups(m)) * tiles : 0), 256);
+    w.total = off;
+    return w;
 }
 
-// Workspace behind the adapters': the rows' exponents and digits, or the shared product.
+// Workspace behind the adapters': that, or the shared product.
 inline size_t lora_base_bytes(int64_t m, int64_t n, int64_t k) {
-    if (lora_uses_tiles(m, n, k)) return sizeof(int32_t) * size_t(kPrefillRows) + 4 * size_t(m) * size_t(k);
+    if (lora_uses_tiles(m, n, k)) return lora_tiles_workspace_layout(m, n, k).total;
     return sizeof(float) * size_t(m) * size_t(n);
 }
 

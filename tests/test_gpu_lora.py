@@ -120,7 +120,11 @@ LINEARS = [(1, 64, 256, 1, 8, None), (1, 2001, 1024, 3, 16, [1500, 501]), (2, 16
            (9, 48, 3840, 3, 16, [16, 16, 16]), (16, 6144, 4096, 8, 16, [4096, 1024, 1024]),
            (17, 130, 768, 17, 40, None), (33, 77, 4352, 2, 256, None), (64, 200, 1536, 6, 8, [50, 50, 50, 50]),
            (255, 129, 512, 30, 16, None), (3, 40, 12288, 2, 8, None), (6, 24, 16384, 2, 16, [8, 16]),
-           (2, 18, 20480, 1, 8, None)]
+           (2, 18, 20480, 1, 8, None),
+           # rows of 17 to 64 slices cut into ranges: uneven ones, more rows than one pass takes,
+           # more tiles than blocks, and past the rows that are cut
+           (1, 4096, 5888, 1, 8, None), (13, 700, 8192, 3, 8, [350, 350]), (64, 33, 8448, 4, 8, None),
+           (65, 20, 4352, 4, 8, None), (7, 9000, 4352, 2, 8, None)]
 
 
 @pytest.mark.parametrize("m,n,k,count,rank,sections", LINEARS)
@@ -137,7 +141,8 @@ def test_linear(q8, m, n, k, count, rank, sections):
 @pytest.mark.parametrize("m,f,k,count,rank,split", [(1, 128, 256, 1, 16, True), (3, 33, 1024, 2, 8, True),
                                                     (8, 1000, 2048, 4, 32, True), (21, 40, 4096, 3, 8, False),
                                                     (70, 24, 768, 5, 16, True), (5, 7, 12288, 2, 8, False),
-                                                    (255, 17, 512, 9, 24, True), (4, 19, 16640, 2, 8, True)])
+                                                    (255, 17, 512, 9, 24, True), (4, 19, 16640, 2, 8, True),
+                                                    (18, 300, 5888, 3, 8, True)])
 def test_gate_up(q8, m, f, k, count, rank, split):
     lib, torch, dev = q8
     kind = TYPES[(m + f) % 3]
