@@ -273,6 +273,39 @@ def test_rows_of_any_magnitude(q8, scale):
     assert np.all(np.abs(y - want) <= bound + 2.0 ** -126), scale
 
 
+@pytest.mark.parametrize("n,k,most", [(200, 1024, 255), (96, 4096, 255), (300, 768, 100), (70, 5888, 64),
+                                      (33, 16384, 64)])
+def test_a_row_depends_on_itself_alone(q8, n, k, most):
+    """Any subset of the rows gives the same bits, rows alone included."""
+    lib, torch, dev = q8
+    c = Case(q8, 75 + n, most, n, k, 5, 16, "bfloat16", [n // 2, n - n // 2])
+    w = to_dev(wl.q8_weight(76, n, k)[0], dev)
+    a, b, ids = c.args
+    whole = lib.q8_linear_lora(w, n, k, c.xd, a, b, ids, **c.more)
+    rng = np.random.default_rng(77)
+    for m in (1, 2, 4, 5, 8, 9, 13, 17, 40):
+        rows = torch.from_numpy(np.sort(rng.choice(most, m, replace=False))).to(dev)
+        part = lib.q8_linear_lora(w, n, k, c.xd[rows].contiguous(), a, b, ids[rows].contiguous(), **c.more)
+        assert torch.equal(part, whole[rows]), m
+    for _ in range(5):
+        assert torch.equal(lib.q8_linear_lora(w, n, k, c.xd, a, b, ids, **c.more), whole)
+
+
+@pytest.mark.parametrize("m", [20, 300])
+def test_adding_does_not_depend_on_the_other_rows(q8, m):
+    """Within a form (few rows, many rows) a row's bits are its own."""
+    lib, torch, dev = q8
+    n, k = 150, 512
+    c = Case(q8, 78 + m, m, n, k, 6, 24, "float16", [70, 80], none=0.3)
+    a, b, ids = c.args
+    y = torch.randn(m, n, device=dev)
+    whole = lib.lora_add(y, c.xd, a, b, ids, **c.more)
+    turned = torch.randperm(m, device=dev)
+    part = lib.lora_add(y[turned], c.xd[turned], a, b, ids[turned], **c.more)
+    assert torch.equal(part, whole[turned])
+    assert torch.equal(whole[ids < 0], y[ids < 0])
+
+
 def test_strided_rows_and_rows_behind_the_last(q8):
     """Padded leading dimensions; what lies outside the outputs stays as it was."""
     lib, torch, dev = q8

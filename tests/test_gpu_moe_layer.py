@@ -147,6 +147,31 @@ def test_tokens_that_are_not_finite_stay_apart(q8, m):
     assert torch.isnan(y).all()
 
 
+@pytest.mark.parametrize("e,k,f,h,most", [(16, 2, 256, 512, 63), (64, 8, 512, 1280, 60), (4, 3, 768, 256, 10)])
+def test_a_token_depends_on_itself_alone(q8, e, k, f, h, most):
+    """Any subset of the tokens gives the same bits, tokens alone included."""
+    lib, torch, dev = q8
+    gu, dn, wr = (to_dev(v, dev) for v in layer(3250, e, f, h))
+    x = to_dev(wl.activations(3251, most, h), dev)
+    whole = lib.q8_moe_layer(wr, gu, dn, e, f, h, x, k)
+    rng = np.random.default_rng(3252)
+    for m in (1, 2, 3, 5, 8, 10):
+        rows = torch.from_numpy(np.sort(rng.choice(most, m, replace=False))).to(dev)
+        assert torch.equal(lib.q8_moe_layer(wr, gu, dn, e, f, h, x[rows].contiguous(), k), whole[rows]), m
+
+
+def test_many_calls_in_a_row_on_one_workspace(q8):
+    """Calls of changing sizes back to back on one workspace, none waited for."""
+    lib, torch, dev = q8
+    e, k, f, h = 32, 4, 256, 768
+    gu, dn, wr = (to_dev(v, dev) for v in layer(3260, e, f, h))
+    xs = [to_dev(wl.activations(3261 + m, m, h), dev) for m in (1, 33, 2, 60, 7)]
+    ws = torch.empty(lib.q8_moe_layer_workspace_bytes(60, k, e, f, h), dtype=torch.uint8, device=dev)
+    want = [lib.q8_moe_layer(wr, gu, dn, e, f, h, x, k) for x in xs]
+    got = [lib.q8_moe_layer(wr, gu, dn, e, f, h, xs[i % 5], k, workspace=ws) for i in range(40)]
+    assert all(torch.equal(got[i], want[i % 5]) for i in range(40))
+
+
 def test_zero_tokens_ties_and_zero_rows(q8):
     """No token; rows of zeros (every logit ties: the lowest experts; outputs 0)."""
     lib, torch, dev = q8
