@@ -21,6 +21,7 @@
 // digits with its own scale when the down tiles take it), y[t] = sum_j w_j out_j in slot
 // order.  A token's result depends on its own row alone.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -48,11 +49,17 @@ __global__ __launch_bounds__(256) void moe_poison_kernel(const float* __restrict
 // Flags and counters of the second launch, cleared by the first.
 constexpr int kMaxChunks = q8v::kLayerMaxChunks;
 constexpr int kMaxJobs = q8v::kLayerMaxJobs;  // an expert's tokens in eights
-constexpr int kDoneParts = 16;                // the down tiles' count, in cache lines of its own
+constexpr int kDoneParts = 16;                // the down tiles' count
+// Each in a cache line of its own: a line that several blocks raise and poll is taken in
+// turns (256 blocks on counters of the same line measured 6 us from the last raise to the
+// last block that saw it).
+struct alignas(128) LayerWord {
+    uint32_t v;
+};
 struct LayerCounters {
-    uint32_t claim_up[kMaxChunks], claim_down[kMaxChunks];
-    uint32_t up_done[kMaxJobs];  // gate_up tiles
-    uint32_t down_done[kDoneParts][32];
+    LayerWord down_done[kDoneParts];
+    LayerWord claim_up[kMaxChunks], claim_down[kMaxChunks];
+    LayerWord up_done[kMaxJobs];  // gate_up tiles
 };
 static_assert(sizeof(LayerCounters) == q8v::kLayerCounterBytes, "workspace layout");
 
@@ -80,11 +87,10 @@ __global__ __launch_bounds__(256) void moe_layer_prepare_kernel(const float* __r
                                                                 float* __restrict__ logits, int8_t* __restrict__ dig,
                                                                 int* __restrict__ exps,
                                                                 uint32_t* __restrict__ hid_max,
-                                                                uint32_t* __restrict__ counters) {
+                                                                LayerWord* __restrict__ counters, int n_counters) {
     const int b = blockIdx.x;
+    for (int i = b * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i].v = 0;
     if (b < m) {
-        if (b == 0)
-            for (int i = threadIdx.x; i < (int)(sizeof(LayerCounters) / 4); i += 256) counters[i] = 0;
         for (int i = threadIdx.x; i < k; i += 256) hid_max[b * k + i] = 0;
         write_digits(x + (size_t)b * ldx, h, dig + (size_t)b * h * 4, exps + b);
         return;
@@ -184,20 +190,20 @@ __device__ __forceinline__ bool wait_counts(const uint32_t* p, int n, int stride
 }
 
 // Wave 0 claims the first chunk nobody has; -1 (in every thread): all are claimed.
-__device__ __forceinline__ int take_over(uint32_t* claim, int chunks, int* word) {
+__device__ __forceinline__ int take_over(LayerWord* claim, int chunks, int* word) {
     if (threadIdx.x < 64) {
         int got = -1;
         for (int c0 = 0; c0 < chunks && got < 0; c0 += 64) {
             const int c = c0 + (int)threadIdx.x;
             const bool open =
-                c < chunks && __hip_atomic_load(claim + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
+                c < chunks && __hip_atomic_load(&claim[c].v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
             uint64_t who = __ballot(open);
             while (who && got < 0) {
                 const int l = (int)__builtin_ctzll(who);
                 who &= who - 1;
                 uint32_t old = 1;
                 if ((int)threadIdx.x == l)
-                    old = __hip_atomic_exchange(claim + c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    old = __hip_atomic_exchange(&claim[c].v, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 if (__builtin_amdgcn_readlane((int)old, l) == 0) got = c0 + l;
             }
         }
@@ -473,8 +479,8 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     // selection and the jobs
     uint32_t taken_up = 0, taken_down = 0;
     if (tid == 0) {
-        taken_up = __hip_atomic_exchange(&A.cnt->claim_up[me], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        taken_down = __hip_atomic_exchange(&A.cnt->claim_down[me], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        taken_up = __hip_atomic_exchange(&A.cnt->claim_up[me].v, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        taken_down = __hip_atomic_exchange(&A.cnt->claim_down[me].v, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     for (int e = tid; e < q8v::kMaxExperts; e += kTileThreads) L.fill[e] = 0;
     for (int t = tid; t < A.m; t += kTileThreads) L.token_exp[t] = A.exps[t];
@@ -595,7 +601,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
                     layer_gate_up<SP_H, 2>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.tokens, pc.rows);
                 else
                     layer_gate_up<SP_H, 1>(A, L, Wh, off, w, pc.tile0, pc.tiles, pc.list, pc.tokens, pc.rows);
-                raise_count(&A.cnt->up_done[pc.job], (uint32_t)pc.tiles);
+                raise_count(&A.cnt->up_done[pc.job].v, (uint32_t)pc.tiles);
                 t += pc.tiles;
             }
             up = -1;
@@ -609,7 +615,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
             while (down_at < end) {
                 const Piece pc = piece_at(down_at, end, down_tiles);
                 const uint8_t* w = A.wdn + (size_t)pc.expert * A.h * rb_f;
-                const uint32_t* count = &A.cnt->up_done[pc.job];
+                const uint32_t* count = &A.cnt->up_done[pc.job].v;
                 if (pc.rows > 4)
                     ready = layer_down<SP_F, 2>(A, L, Wf, off, w, pc.tile0, pc.tiles, pc.list, pc.rows, count, up_tiles);
                 else
@@ -618,14 +624,14 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
                 done += pc.tiles;
                 down_at += pc.tiles;
             }
-            raise_count(&A.cnt->down_done[me % kDoneParts][0], done);
+            raise_count(&A.cnt->down_done[me % kDoneParts].v, done);
             if (!ready) {
                 up = take_over(A.cnt->claim_up, blocks, &L.word);
                 continue;
             }
             down = -1;
         }
-        if (wait_counts(&A.cnt->down_done[0][0], kDoneParts, 32, (uint32_t)cut_down.all, &L.word)) break;
+        if (wait_counts(&A.cnt->down_done[0].v, kDoneParts, sizeof(LayerWord) / 4, (uint32_t)cut_down.all, &L.word)) break;
         up = take_over(A.cnt->claim_up, blocks, &L.word);
         if (up < 0) {
             down = take_over(A.cnt->claim_down, blocks, &L.word);
@@ -712,10 +718,14 @@ hipError_t launch_moe_layer(const DeviceInfo& dev, const float* w_router, const 
         A.log2_wt_h = sh.log2_wt;
         A.log2_wt_f = sf.log2_wt;
         const int64_t blocks = m + (n_exp + 3) / 4 * ((m + kPrepareTokens - 1) / kPrepareTokens);
+        // the counters in use: of the jobs (one for an expert's first eight tokens, and for every
+        // eight more), the last ones
+        const int jobs = (int)(m * k < n_exp ? m * k : n_exp) + (int)(m * k / kJobRows);
+        const int counters = (int)(offsetof(LayerCounters, up_done) / sizeof(LayerWord)) + (jobs < kMaxJobs ? jobs : kMaxJobs);
         hipLaunchKernelGGL(moe_layer_prepare_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, (int)m, (int)h,
                            (int)ldx, w_router, (int)n_exp, k, const_cast<float*>(A.logits),
                            const_cast<int8_t*>(A.dig), const_cast<int*>(A.exps), A.hid_max,
-                           reinterpret_cast<uint32_t*>(A.cnt));
+                           reinterpret_cast<LayerWord*>(A.cnt), counters);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (sh.sp <= 1) return launch_layer_f<1>(dev, sf.sp, A, stream);

@@ -358,7 +358,7 @@ inline bool moe_layer_uses_tiles(int64_t m, int32_t k, int64_t n_exp, int64_t f,
 // the down tiles' counts.  Jobs: an expert's tokens in eights, m * k < 8 * n_exp <= 2048 pairs.
 constexpr int kLayerMaxChunks = 512;
 constexpr int kLayerMaxJobs = 512;
-constexpr size_t kLayerCounterBytes = sizeof(uint32_t) * size_t(2 * kLayerMaxChunks + kLayerMaxJobs + 16 * 32);
+constexpr size_t kLayerCounterBytes = 128 * size_t(16 + 2 * kLayerMaxChunks + kLayerMaxJobs);
 
 // Workspace of q8_moe_layer: the logits, then what its form needs.
 struct MoeLayerWorkspace {
