@@ -153,7 +153,7 @@ struct LayerLds {
     uint16_t list[kLayerMaxPairs];          // pairs by expert
     uint8_t list_token[kLayerMaxPairs];     // and their tokens
     int token_exp[q8v::kMoeLayerMaxTokens];
-    int fill[q8v::kMaxExperts];
+    alignas(16) int fill[q8v::kMaxExperts];
     uint16_t job_expert[kMaxJobs], job_first[kMaxJobs], job_rows[kMaxJobs];  // first: in list
     uint32_t max_bits[kJobRows];
     int row_exp[kJobRows];                  // of the job in work: its rows' exponents
@@ -377,7 +377,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
     v = dpp_max<0x111>(v);  // row_shr 1, 2, 4, 8: lane 15 of each row has its row's largest
@@ -456,13 +456,14 @@ struct Cut {
     int q, per, all, blocks;
     __device__ __forceinline__ Cut(int jobs, int per_, int blocks_, int start)
         : per(per_), all(jobs * per_), blocks(blocks_) {
-        q = jobs > 0 ? min(blocks / jobs, per) : 0;
-        if (q > 0 && (per + q - 1) / q > (all + blocks - 1) / blocks + start) q = 0;
+        q = jobs > 0 ? min((int)((uint32_t)blocks / (uint32_t)jobs), per) : 0;
+        if (q > 0 && (int)((uint32_t)(per + q - 1) / (uint32_t)q) > (int)((uint32_t)(all + blocks - 1) / (uint32_t)blocks) + start) q = 0;
     }
     __device__ __forceinline__ int begin(int chunk) const {
-        if (q == 0) return (int)((int64_t)all * chunk / blocks);
-        const int job = chunk / q, part = chunk - job * q;
-        return min(job * per + per * part / q, all);
+        // all <= 512 jobs x 768 tiles and chunk <= 512: 32 bits hold the products
+        if (q == 0) return (int)((uint32_t)(all * chunk) / (uint32_t)blocks);
+        const int job = (int)((uint32_t)chunk / (uint32_t)q), part = chunk - job * q;
+        return min(job * per + (int)((uint32_t)(per * part) / (uint32_t)q), all);
     }
     __device__ __forceinline__ int end(int chunk) const { return begin(chunk + 1); }
 };
@@ -515,10 +516,11 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     if (tid == 0) L.word = (int)(taken_up | taken_down << 1);
     __syncthreads();
     if (wv == 0) {  // lane l: experts 4l .. 4l + 3
-        int c[4], sum = 0, jobs = 0;
+        const int4 counts = *reinterpret_cast<const int4*>(&L.fill[4 * lane]);
+        const int c[4] = {counts.x, counts.y, counts.z, counts.w};
+        int sum = 0, jobs = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            c[q] = L.fill[4 * lane + q];
             sum += c[q];
             jobs += (c[q] + kJobRows - 1) / kJobRows;
         }
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
             if (e >= 0) {
                 const int pos = L.fill[e] + __popcll(same & ((1ull << lane) - 1));
                 L.list[pos] = (uint16_t)(i0 + lane);
-                L.list_token[pos] = (uint8_t)((i0 + lane) / A.k);
+                L.list_token[pos] = (uint8_t)((uint32_t)(i0 + lane) / (uint32_t)A.k);
                 wait_lgkmcnt_mem<0>();                        // every lane has read its position
                 if ((same >> lane) == 1ull) L.fill[e] = pos + 1;  // the highest lane of its expert
             }
@@ -572,7 +574,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     };
     auto piece_at = [&](int t, int end, int per) __attribute__((always_inline)) {
         Piece r;
-        r.job = t / per;
+        r.job = (int)((uint32_t)t / (uint32_t)per);
         r.tile0 = t - r.job * per;
         r.tiles = min(per - r.tile0, end - t);
         r.expert = __builtin_amdgcn_readfirstlane((int)L.job_expert[r.job]);
