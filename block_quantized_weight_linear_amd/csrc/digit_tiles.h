@@ -10,7 +10,8 @@
 // largest element being 2^-24 of it).  The 16 rows of the instruction's A operand are 4
 // activation rows x 4 digits; a block's four digit sums come back exact (|sum| <= 2^19) in
 // the four registers of one lane:
-//     t = (256 s3 + s2) 2^16 + (256 s1 + s0)   (the halves exact integers, one fma)
+//     t = (256 s3 + s2) 2^16 + (256 s1 + s0)   (one fma of the halves, exact integers below
+//                                               2^27 that float32 takes with one rounding)
 //     acc = fma(d, t, acc)                      (d: the block's scale)
 // so a weight costs a lane 6 VALU operations per 512 weights and 4 activation rows instead
 // of a conversion and 4 fmas each.  Per output: the chain over the blocks of a 256-wide
@@ -141,8 +142,9 @@ __host__ __device__ constexpr size_t digit_at(int i, int d) {
     return (size_t)(i >> 6) * 256 + 64 * d + 16 * ((i >> 3) & 3) + 8 * ((i >> 5) & 1) + (i & 7);
 }
 
-// Digits of one activation row, by a block of 256 threads: dig is the row's 4 k bytes, *exp_out the exponent e - 29 of its scale.  A row that holds
-// a NaN or an infinity gets kNotFinite and zero digits: all its outputs are NaN.
+// Digits of one activation row, by a block of 256 threads: dig is the row's 4 k bytes,
+// *exp_out the exponent e - 29 of its scale.  A row that holds a NaN or an infinity gets
+// kNotFinite and zero digits: all its outputs are NaN.
 constexpr int kNotFinite = 1 << 20;
 __device__ __forceinline__ float row_scaled(float sum, int exp) {
     return exp == kNotFinite ? __builtin_nanf("") : __builtin_ldexpf(sum, exp);

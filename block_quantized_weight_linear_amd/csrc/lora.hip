@@ -5,7 +5,10 @@
 // sections' ranks; float32, one wave a product), then each output's dot of u with its row
 // of B, added to the shared product (or, for a fused gate_up, the activation behind it).
 // In the packed calls the first launch also writes the rows' digits and the second
-// computes the shared product (digit_tiles.h).
+// computes the shared product (digit_tiles.h); bound by the weights' bytes and, in small
+// matrices, by the two launches' starts: 6144 x 4096 takes 15 us at 2 rows (27 MB, of which
+// the first launch 4), the fused 24576 x 4096 28 us (107 MB at 3.8 TB/s, the second launch
+// alone 4.7), 16 rows 22 and 40 us.  With many rows the correction has a form of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -333,8 +336,8 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 
 // ------------------------------------------------------------------- many rows
 //
-// From kLoraTiledRows rows on the correction runs on the bf16 matrix cores at float32
-// accuracy.  A float32 value is the exact sum of three bf16 values (its leading 8 bits, the
+// For many rows (q8v::lora_uses_matrix_cores) the correction runs on the bf16 matrix cores at
+// float32 accuracy.  A float32 value is the exact sum of three bf16 values (its leading 8 bits, the
 // next 8, the last 8, each cut off, not rounded); a bf16 element of A or B is itself, a
 // binary16 one the sum of two.  A product takes the partial products down to 2^-16 of its
 // leading one (those left out are below 2^-23 of the product): 3, 5 or 6 instructions for
@@ -347,7 +350,11 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 //   3. sum:    the parts added up, scaled and split, laid out as the next launch's operand.
 //   4. outer:  block (tile, 128 outputs), 64 rows x 32 outputs a wave: u and B start out,
 //              then the product's values, and no barrier lies between.
-// Bound by the memory: x once, the product in and out.
+// Bound by the memory: x once, the product in and out.  6144 x 4096, three sections of rank
+// 16 and 2048 rows: 59 us (plan 4.6, inner 19, sum 5.8, outer 30: 100 MB of product in and out
+// at 3.4 TB/s).  Measured and not kept: u staged through LDS in the outer launch (37 us), the
+// parts added by the last block of the inner one (33 us against 19 + 6), its next step's
+// loads ahead (25 us).
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -567,7 +574,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(LoraArgs lo, LoraPlan P, 
     }
 }
 
-constexpr int kOuterColumns = 128;  // outputs of a block, 32 a wave
+constexpr int kOuterColumns = q8v::kLoraOuterColumns;  // outputs of a block, 32 a wave
 
 // Outputs whose rows of B belong to one section (SILU: gate rows to one, up rows to one), in
 // blocks of kOuterColumns.
@@ -745,9 +752,9 @@ static hipError_t lora_add_tiled(const LoraArgs& lo, const float* y, int64_t n, 
 
 template <class Ty>
 static hipError_t lora_add_any(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu, const float* x,
-                               int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, char* ws,
-                               const q8v::LoraWorkspace& L, hipStream_t stream) {
-    if (m >= q8v::kLoraTiledRows && n <= q8v::kLoraTiledMaxOutputs)
+                               int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo, bool with_matrix_cores,
+                               char* ws, const q8v::LoraWorkspace& L, hipStream_t stream) {
+    if (with_matrix_cores)
         return lora_add_tiled<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, ws, L, stream);
     return lora_add_typed<Ty>(lo, y, n, ldy, silu, x, m, k, ldx, out, ldo, reinterpret_cast<float*>(ws + L.u_off), stream);
 }
@@ -758,10 +765,11 @@ hipError_t launch_lora_add(const DeviceInfo&, const float* y, int64_t n, int64_t
     const LoraArgs lo = lora_args(lora);
     const q8v::LoraWorkspace L = q8v::lora_workspace_layout(m, lora.n_sections, lora.rank, 0);
     char* ws = static_cast<char*>(workspace);
+    const bool mc = q8v::lora_uses_matrix_cores(lora, m, n, k);
     switch (lora.type) {
-        case Q8_LORA_F32: return lora_add_any<LoraF32>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
-        case Q8_LORA_F16: return lora_add_any<LoraF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
-        default: return lora_add_any<LoraBF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, ws, L, stream);
+        case Q8_LORA_F32: return lora_add_any<LoraF32>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, mc, ws, L, stream);
+        case Q8_LORA_F16: return lora_add_any<LoraF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, mc, ws, L, stream);
+        default: return lora_add_any<LoraBF16>(lo, y, n, ldy, silu_pairs, x, m, k, ldx, out, ldo, mc, ws, L, stream);
     }
 }
 

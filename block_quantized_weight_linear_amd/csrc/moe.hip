@@ -430,17 +430,6 @@ static hipError_t launch_expert_pass(const DeviceInfo& dev, const uint8_t* w, si
     return hipGetLastError();
 }
 
-hipError_t launch_route_plan(const int32_t* idx, int n_pairs, int n_exp, int32_t* offsets, int32_t* sorted,
-                             int32_t* inv, int32_t* active, int32_t* tile_start, hipStream_t stream) {
-    if (n_pairs <= kPlanSmallPairs)
-        hipLaunchKernelGGL(moe_plan_kernel<4>, dim3(1), dim3(256), 0, stream, idx, n_pairs, n_exp, offsets, sorted,
-                           inv, active, tile_start);
-    else
-        hipLaunchKernelGGL(moe_plan_kernel<16>, dim3(1), dim3(1024), 0, stream, idx, n_pairs, n_exp, offsets, sorted,
-                           inv, active, tile_start);
-    return hipGetLastError();
-}
-
 hipError_t launch_moe_grouped(const DeviceInfo& dev, const uint8_t* wgu, const uint8_t* wdn, int64_t n_exp, int64_t f,
                               int64_t h, const float* x, int64_t m, int64_t ldx, const int32_t* idx, const float* wts,
                               int k, float* y, int64_t ldy, void* workspace, hipStream_t stream) {
@@ -455,7 +444,13 @@ hipError_t launch_moe_grouped(const DeviceInfo& dev, const uint8_t* wgu, const u
     const int n_pairs = (int)(m * k);
 
     int32_t* tile_start = reinterpret_cast<int32_t*>(ws + L.tiles_off);
-    hipError_t e = launch_route_plan(idx, n_pairs, (int)n_exp, offsets, sorted, inv, active, tile_start, stream);
+    if (n_pairs <= kPlanSmallPairs)
+        hipLaunchKernelGGL(moe_plan_kernel<4>, dim3(1), dim3(256), 0, stream, idx, n_pairs, (int)n_exp, offsets,
+                           sorted, inv, active, tile_start);
+    else
+        hipLaunchKernelGGL(moe_plan_kernel<16>, dim3(1), dim3(1024), 0, stream, idx, n_pairs, (int)n_exp, offsets,
+                           sorted, inv, active, tile_start);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 
     if (q8v::moe_uses_matrix_cores(n_pairs, n_exp)) {

@@ -71,12 +71,6 @@ hipError_t launch_moe_grouped(const DeviceInfo& dev, const uint8_t* wgu, const u
                               int64_t h, const float* x, int64_t m, int64_t ldx, const int32_t* idx, const float* wts,
                               int k, float* y, int64_t ldy, void* workspace, hipStream_t stream);
 
-// Counting sort of n_pairs expert (or adapter) ids idx < n_exp <= 256: offsets [n_exp + 1],
-// sorted positions -> pair, inv pair -> position (-1: id out of range), the ids with pairs
-// and their number (active[n_exp]), and each id's first 128-pair tile.
-hipError_t launch_route_plan(const int32_t* idx, int n_pairs, int n_exp, int32_t* offsets, int32_t* sorted,
-                             int32_t* inv, int32_t* active, int32_t* tile_start, hipStream_t stream);
-
 // Low-rank adapters beside a product y [m][n] that is there (n = 2f with silu_pairs: out is
 // then SiLU(gate) * up [m][f]); workspace laid out by q8v::lora_workspace_layout.
 hipError_t launch_lora_add(const DeviceInfo& dev, const float* y, int64_t n, int64_t ldy, bool silu_pairs,

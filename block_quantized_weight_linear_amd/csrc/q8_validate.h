@@ -197,7 +197,7 @@ inline q8_status check_moe(const void* wgu, const void* wdn, int64_t n_exp, int6
 
 // ------------------------------------------------------------- low-rank adapters
 
-constexpr int32_t kLoraMaxAdapters = 256;  // the row sort's bins are the route plan's
+constexpr int32_t kLoraMaxAdapters = 256;  // bins of the row sort
 constexpr int32_t kLoraMaxRank = 256;
 
 // The adapter stack beside a matrix of n rows and width k, for m rows of x.
@@ -236,10 +236,24 @@ inline bool lora_sizes_valid(const q8_lora& lo) {
 constexpr int64_t kPrefillRows = 256;
 
 // The matrix-core form of the correction (many rows): rows sorted by adapter in tiles of 64,
-// the inner products in parts of k (enough blocks for few tiles).  Outputs: one grid's worth.
-constexpr int64_t kLoraTiledMaxOutputs = int64_t(1) << 23;
+// the inner products in parts of k (enough blocks for few tiles).
 constexpr int64_t kLoraTiledRows = 48;
 inline int64_t lora_max_tiles(int64_t m, int64_t n_adapters) { return m / 64 + (m < n_adapters + 1 ? m : n_adapters + 1); }
+// It takes two launches more, the form for few rows reads its adapter for every row: the
+// latter is left once those reads would be 160 MB.  Measured, in us, few rows | matrix
+// cores, 1 and 32 adapters in use: 6144 x 4096, three sections of rank 16 (0.6 MB a row), 192
+// rows 21.5 | 23.1 and 23.6 | 30.3, 384 rows 36.4 | 25.9 and 38.5 | 32.9; of rank 64 (2.4 MB a
+// row), 64 rows 24.6 | 32.7 and 29.7 | 51.0, 128 rows 44.7 | 35.3 and 50.5 | 53.1; 1024 x 1024,
+// rank 8 in float32, 512 rows 11.7 | 17.5, 2048 rows 34.4 | 24.6.  The last launch's grid has
+// to fit 32 bits of threads.
+constexpr int64_t kLoraTiledBytes = int64_t(160) << 20;
+constexpr int64_t kLoraOuterColumns = 128;  // outputs of a block of the last launch
+inline bool lora_uses_matrix_cores(const q8_lora& lo, int64_t m, int64_t n, int64_t k) {
+    if (m < kLoraTiledRows) return false;
+    const int64_t row = (int64_t(lo.n_sections) * k + n) * lo.rank * (lo.type == Q8_LORA_F32 ? 4 : 2);
+    const int64_t blocks = n / kLoraOuterColumns + 2 * Q8_LORA_MAX_SECTIONS + 1;
+    return m * row >= kLoraTiledBytes && lora_max_tiles(m, lo.n_adapters) * blocks * 256 < (int64_t(1) << 32);
+}
 inline int64_t lora_parts(int64_t m) {
     if (m < kLoraTiledRows) return 1;
     const int64_t tiles = (m + 31) / 32;
@@ -268,16 +282,17 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
     return w;
 }
 
-// The packed calls run on the digit tiles (digit_tiles.h) below the prefill rows, up to 64
-// rows where k is cut into ranges (their sums go through the workspace), for widths up to 64
-// slices and fused matrices whose up rows lie within 32-bit byte offsets of their gate
-// rows; else on q8_linear's kernels and the correction behind them.
+// The packed calls run on the digit tiles (digit_tiles.h) from two rows to the prefill rows,
+// for widths up to 64 slices and fused matrices whose up rows lie within 32-bit byte offsets
+// of their gate rows; else on q8_linear's kernels and the correction behind them.  Measured,
+// in us, at 1 | 2 | 16 | 255 rows, rank 16: 6144 x 4096 tiles 15.0 | 15.1 | 22.1 | 251,
+// q8_linear and correction 12.9 | 15.6 | 27.5 | 346; fused 24576 x 4096 28.0 | 28.3 | 39.7 |
+// 514 and 25.3 | 31.7 | 59.9 | 850; 4096 x 12288 24.3 | 24.3 | 43.7 | 510 and 18.8 | 26.3 | 48.5 | 633.
 constexpr int64_t kLoraTilesMaxK = 16384;
 constexpr int64_t kLoraTilesMaxRange = 16 * 256;  // of k without a cut
 constexpr int64_t kLoraMaxRanges = 6;             // at most two more than the fewest, 4
 inline bool lora_uses_tiles(int64_t m, int64_t n, int64_t k) {
-    return m < kPrefillRows && (k <= kLoraTilesMaxRange || m <= 64) && k <= kLoraTilesMaxK &&
-           n * row_bytes(k) < (int64_t(1) << 31);
+    return m > 1 && m < kPrefillRows && k <= kLoraTilesMaxK && n * row_bytes(k) < (int64_t(1) << 31);
 }
 // Row groups of four, as many as any form has.
 inline int64_t lora_row_groups(int64_t m) { return (m + 3) / 4; }
@@ -344,9 +359,12 @@ inline q8_status check_lora_add(const float* y, int64_t n_in, int64_t ldy, const
 // ----------------------------------------------------- the whole mixture-of-experts layer
 
 // q8_moe_layer runs in two launches on the digit tiles (digit_tiles.h) below the matrix-core
-// switch of the grouped call, up to kMoeLayerMaxTokens tokens (every block selects all
-// tokens' experts), at most 64 experts a token and widths of at most 24 slices of 256 (three a wave); else the
-// routing and the grouped mixture follow each other.
+// switch of the grouped call, up to kMoeLayerMaxTokens tokens (every block selects all tokens'
+// experts and holds their lists), at most 64 experts a token (a lane each) and widths of at
+// most 24 slices of 256 (three a wave); else the routing and the grouped mixture follow each
+// other.  Measured, in us, two launches | the calls one after the other: 8 of 128 experts
+// of 768 x 2048 at 1 token 29.1 | 41.4, 16 87.5 | 124, 64 152 | 288, 127 239 | 488; 2 of 64 at 128
+// tokens 96 | 163; 2 of 8 experts of 2048 x 2048 at 31 tokens 64 | 146.
 constexpr int64_t kMoeLayerMaxTokens = 128;
 constexpr int64_t kMoeLayerMaxWidth = 24 * 256;
 inline bool moe_layer_uses_tiles(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {

@@ -124,7 +124,8 @@ LINEARS = [(1, 64, 256, 1, 8, None), (1, 2001, 1024, 3, 16, [1500, 501]), (2, 16
            # rows of 17 to 64 slices cut into ranges: uneven ones, more rows than one pass takes,
            # more tiles than blocks, and past the rows that are cut
            (1, 4096, 5888, 1, 8, None), (13, 700, 8192, 3, 8, [350, 350]), (64, 33, 8448, 4, 8, None),
-           (65, 20, 4352, 4, 8, None), (7, 9000, 4352, 2, 8, None)]
+           (65, 20, 4352, 4, 8, None), (7, 9000, 4352, 2, 8, None), (130, 90, 8192, 9, 16, [30, 60]),
+           (255, 333, 5120, 3, 8, None)]
 
 
 @pytest.mark.parametrize("m,n,k,count,rank,sections", LINEARS)
@@ -276,7 +277,7 @@ def test_rows_of_any_magnitude(q8, scale):
 @pytest.mark.parametrize("n,k,most", [(200, 1024, 255), (96, 4096, 255), (300, 768, 100), (70, 5888, 64),
                                       (33, 16384, 64)])
 def test_a_row_depends_on_itself_alone(q8, n, k, most):
-    """Any subset of the rows gives the same bits, rows alone included."""
+    """Any subset of two rows and more gives the same bits, one row twice included."""
     lib, torch, dev = q8
     c = Case(q8, 75 + n, most, n, k, 5, 16, "bfloat16", [n // 2, n - n // 2])
     w = to_dev(wl.q8_weight(76, n, k)[0], dev)
@@ -285,6 +286,8 @@ def test_a_row_depends_on_itself_alone(q8, n, k, most):
     rng = np.random.default_rng(77)
     for m in (1, 2, 4, 5, 8, 9, 13, 17, 40):
         rows = torch.from_numpy(np.sort(rng.choice(most, m, replace=False))).to(dev)
+        if m == 1:
+            rows = rows.repeat(2)
         part = lib.q8_linear_lora(w, n, k, c.xd[rows].contiguous(), a, b, ids[rows].contiguous(), **c.more)
         assert torch.equal(part, whole[rows]), m
     for _ in range(5):
@@ -304,6 +307,96 @@ def test_adding_does_not_depend_on_the_other_rows(q8, m):
     part = lib.lora_add(y[turned], c.xd[turned], a, b, ids[turned], **c.more)
     assert torch.equal(part, whole[turned])
     assert torch.equal(whole[ids < 0], y[ids < 0])
+
+
+# The matrix-core form: calls whose rows would read 160 MB of their adapters.  Few rows of wide
+# and many of narrow adapters, odd outputs, sections that end inside a block of 128 outputs,
+# adapters with fewer rows than a tile, one adapter for all, one part of k and several
+MANY = [(48, 129, 8192, 2, 256, None), (64, 33, 16384, 3, 256, [33]), (420, 77, 1280, 7, 96, [30, 47]),
+        (700, 515, 512, 40, 64, [256, 3, 256]), (1300, 57, 256, 256, 256, None), (5200, 1301, 768, 1, 8, [1, 1300]),
+        (2111, 640, 1024, 5, 24, [160, 160, 160, 160])]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m,n,k,count,rank,sections", MANY)
+def test_add_many_rows(q8, m, n, k, count, rank, sections, kind):
+    lib, torch, dev = q8
+    say(f"lora_add m={m} n={n} k={k} adapters={count} rank={rank} {kind}")
+    c = Case(q8, 11 * m + n, m, n, k, count, rank, kind, sections)
+    y = wl.activations(5 + m, m, n)
+    yd = to_dev(y, dev)
+    check(lib.lora_add(yd, c.xd, *c.args, **c.more), *added(y.astype(np.float64), 0, *c.delta()), "lora_add")
+
+
+@pytest.mark.parametrize("m,f,k,count,rank,split", [(420, 77, 1280, 7, 96, True), (1100, 301, 512, 30, 64, True),
+                                                    (900, 150, 2048, 3, 40, False), (48, 65, 8192, 2, 256, True)])
+def test_act_many_rows(q8, m, f, k, count, rank, split):
+    lib, torch, dev = q8
+    kind = TYPES[m % 3]
+    say(f"lora_gate_up_silu m={m} f={f} k={k} adapters={count} rank={rank} {kind}")
+    c = Case(q8, 11 * m + f, m, 2 * f, k, count, rank, kind, [f, f] if split else [f + 5, f - 5])
+    gu = wl.activations(6 + m, m, 2 * f)
+    h = lib.lora_gate_up_silu(to_dev(gu, dev), c.xd, *c.args, **c.more)
+    check(h, *activated(*added(gu.astype(np.float64), 0, *c.delta()), f), "lora_gate_up_silu")
+
+
+def test_many_rows_use_what_is_theirs(q8):
+    """In the matrix-core form: entries past a rank and adapters nobody names may hold
+    anything, rows that are not finite stay apart, a row's bits are its own, in place or
+    not, in a graph or not."""
+    lib, torch, dev = q8
+    m, n, k, rank = 800, 300, 1024, 64
+    c = Case(q8, 63, m, n, k, 4, rank, "bfloat16", [140, 160])
+    c.adapter[c.adapter == 3] = 0
+    c.ranks[:] = [5, 0, rank, rank]
+    a, b = c.a.clone(), c.b.clone()
+    a.view(4, 2, rank, k)[0, :, 5:] = float("nan")
+    b[0, :, 5:] = float("inf")
+    a[1], b[1] = float("nan"), float("nan")
+    a[3], b[3] = float("inf"), float("nan")
+    ids = to_dev(c.adapter, dev)
+    more = dict(scale=c.more["scale"], ranks=torch.tensor([5, -3, 1000, 8], dtype=torch.int32, device=dev),
+                sections=c.sections)
+    y = wl.activations(64, m, n)
+    yd = to_dev(y, dev)
+    got = lib.lora_add(yd, c.xd, a, b, ids, **more)
+    check(got, *added(y.astype(np.float64), 0, *c.delta()), "lora_add")
+    assert torch.equal(got[ids < 0], yd[ids < 0])
+    turned = torch.randperm(m, device=dev)
+    assert torch.equal(lib.lora_add(yd[turned], c.xd[turned], a, b, ids[turned], **more), got[turned])
+    x = c.xd.clone()
+    bad = torch.nonzero(ids == 2).flatten()[:3]
+    x[bad[0], 5], x[bad[1], 700], x[bad[2], 0] = float("nan"), float("inf"), float("-inf")
+    out = lib.lora_add(yd, x, a, b, ids, **more)
+    rest = torch.ones(m, dtype=torch.bool, device=dev)
+    rest[bad] = False
+    assert not torch.isfinite(out[bad]).any() and torch.equal(out[rest], got[rest])
+    ws = torch.empty(lib.lora_workspace_bytes(m, rank, 2), dtype=torch.uint8, device=dev)
+    z = yd.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.lora_add(z, c.xd, a, b, ids, **more, out=z, workspace=ws)
+    for _ in range(3):
+        z.copy_(yd)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, got)
+
+
+def test_more_outputs_and_adapters_than_a_grid_holds(q8):
+    """Row tiles of 256 adapters times 2^23 outputs pass 2^32 threads: the other form."""
+    lib, torch, dev = q8
+    m, n, k, rank, count = 300, 1 << 23, 256, 8, 256
+    a = torch.ones((count, rank, k), dtype=torch.bfloat16, device=dev)
+    b = torch.zeros((count, n, rank), dtype=torch.bfloat16, device=dev)
+    b[3, -5:] = 0.25
+    x = torch.ones((m, k), device=dev)
+    ids = (torch.arange(m, device=dev) % count).int()
+    y = torch.zeros((m, n), device=dev)
+    assert lib.lora_add(y, x, a, b, ids, out=y) is y
+    want = torch.where(ids == 3, rank * k * 0.25, 0.0)
+    assert torch.equal(y[:, -5:], want[:, None].expand(m, 5)) and not y[:, :-5].any()
 
 
 def test_strided_rows_and_rows_behind_the_last(q8):
