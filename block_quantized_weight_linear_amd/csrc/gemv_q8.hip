@@ -19,6 +19,7 @@
 
 #include "gemv_core.h"
 #include "lds_dma.h"
+#include "lora_core.h"
 #include "q8_internal.h"
 
 namespace q8k {
@@ -472,10 +473,18 @@ __device__ __forceinline__ void FmtQ8_0::mac_row(const uint32_t (&w)[R][kDwords]
 // butterfly over the S slots).
 constexpr int kXRow = 256;
 
-template <class Fmt, int R, int NR, int D, int NW, bool NT>
+// What a call adds to the sums before they are stored: nothing (LoraOneRow: an adapter's
+// correction; its loads follow the wave's last copies, but for the adapter's id and rank).
+struct AddNothing {
+    static constexpr bool kAdds = false;
+    struct State {};
+    __device__ __forceinline__ State begin() const { return {}; }
+};
+
+template <class Fmt, int R, int NR, int D, int NW, bool NT, class Add>
 __global__ __launch_bounds__(64 * NW) void gemv_one_row_kernel(const uint8_t* __restrict__ w, int n_out, int P,
                                                               int log2S, const float* __restrict__ x,
-                                                              float* __restrict__ y, int ipw) {
+                                                              float* __restrict__ y, int ipw, Add add) {
     static_assert((D - 1) * 5 * R < 64 && D * 5 * R < 64, "copies in flight must fit the vmcnt counter");
     extern __shared__ float4 smem4[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(smem4);
@@ -523,6 +532,7 @@ __global__ __launch_bounds__(64 * NW) void gemv_one_row_kernel(const uint8_t* __
 
     const bool active = wid < total / NR;
     const int n_pro = active ? (ipw < D ? ipw : D) : 0;
+    [[maybe_unused]] const typename Add::State added = add.begin();
     for (int q = wv; q < (P >> 2); q += NW) {  // 1 KB = the activations of 4 pairs per copy
         const int p = 4 * q + (lane >> 4), pos = lane & 15;
         const int c = (pos - p) & 15;  // chunk c of pair p lands in position (c + p) mod 16
@@ -578,13 +588,20 @@ __global__ __launch_bounds__(64 * NW) void gemv_one_row_kernel(const uint8_t* __
     // groups.  A store between the weight copies would also be counted by the vmcnt waits
     // above and make them wait for the newest copies.
     float keep = 0.0f;
+    [[maybe_unused]] float keep_up = 0.0f;  // where the correction comes before the activation
     int kept_base = 0;  // local row group of lane j == 0's kept value
     auto flush = [&](int count) __attribute__((always_inline)) {
         if (j < count) {
             int rg, ii;
             item_of((kept_base + j) * NR, rg, ii);
             const int n = rg * G + g;
-            y[n < n_out ? n : n_out - 1] = keep;  // a clamped duplicate stores the same bits
+            const int nc = n < n_out ? n : n_out - 1;  // a clamped duplicate stores the same bits
+            if constexpr (Add::kAdds) {
+                const float v = keep + add.at(added, nc);
+                y[nc] = R == 2 ? silu_mul(v, keep_up + add.at(added, (int64_t)n_out + nc)) : v;
+            } else {
+                y[nc] = keep;
+            }
         }
     };
 
@@ -620,9 +637,12 @@ __global__ __launch_bounds__(64 * NW) void gemv_one_row_kernel(const uint8_t* __
                     for (int r = 0; r < R; ++r) acc[r][0] += __shfl_xor(acc[r][0], off, 64);
                 }
                 // every lane of the row holds the same bits
-                const float v = R == 2 ? silu_mul(acc[0][0], acc[R - 1][0]) : acc[0][0];
+                const float v = R == 2 && !Add::kAdds ? silu_mul(acc[0][0], acc[R - 1][0]) : acc[0][0];
                 const int t = rgl - kept_base;
-                if (j == t) keep = v;
+                if (j == t) {
+                    keep = v;
+                    if constexpr (R == 2 && Add::kAdds) keep_up = acc[R - 1][0];
+                }
                 if (t == S - 1) {
                     flush(S);
                     kept_base = rgl + 1;
@@ -1392,10 +1412,10 @@ void gemv_rows_stream_kernel(const uint8_t* __restrict__ w, int n_out, int P, co
 
 namespace {
 
-template <class Fmt, int R, int NR, int D, int NW, bool NT = false>
+template <class Fmt, int R, int NR, int D, int NW, bool NT = false, class Add = AddNothing>
 hipError_t launch_one_row(const DeviceInfo& dev, const uint8_t* w, int n_out, int P, int log2S, const float* x,
-                          float* y, hipStream_t stream) {
-    auto kernel = gemv_one_row_kernel<Fmt, R, NR, D, NW, NT>;
+                          float* y, hipStream_t stream, const Add& add = {}) {
+    auto kernel = gemv_one_row_kernel<Fmt, R, NR, D, NW, NT, Add>;
     const size_t lds = (size_t)P * kXRow + (size_t)NW * D * R * kLdsItemBytes;
     // Once per device: allow the largest dynamic LDS this instance uses (rows of up to
     // 64*NR pairs), above the default limit.  Resident blocks per CU depend on the LDS
@@ -1434,7 +1454,7 @@ hipError_t launch_one_row(const DeviceInfo& dev, const uint8_t* w, int n_out, in
     ipw = ((ipw + NR - 1) / NR) * NR;
     const int waves = (total + ipw - 1) / ipw;
     const int blocks = (waves + NW - 1) / NW;
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * NW), lds, stream, w, n_out, P, log2S, x, y, ipw);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * NW), lds, stream, w, n_out, P, log2S, x, y, ipw, add);
     return hipGetLastError();
 }
 
@@ -1445,27 +1465,27 @@ hipError_t launch_one_row(const DeviceInfo& dev, const uint8_t* w, int n_out, in
 // (2-6% faster there).  Smaller matrices (or 4 rounds, where the activations need more
 // registers): 4-wave blocks, spread over more CUs, two slots each, plain copies (the hint
 // measured slower on the Qwen3-0.6B shapes).  Measured on the Qwen3 shapes.
-template <class Fmt, int R>
+template <class Fmt, int R, class Add = AddNothing>
 bool try_one_row(const DeviceInfo& dev, const uint8_t* w, int n_out, int P, int log2S, const float* x, float* y,
-                 hipStream_t stream, hipError_t* err) {
+                 hipStream_t stream, hipError_t* err, const Add& add = {}) {
     const int S = 1 << log2S;
     const int NR = (P + S - 1) / S;
     const int64_t items = (int64_t)((n_out + (64 >> log2S) - 1) / (64 >> log2S)) * NR;
     const bool wide = items >= (int64_t)16 * dev.cu_count;
     switch (NR) {
         case 1:
-            *err = wide ? launch_one_row<Fmt, R, 1, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream)
-                        : launch_one_row<Fmt, R, 1, 2, 4>(dev, w, n_out, P, log2S, x, y, stream);
+            *err = wide ? launch_one_row<Fmt, R, 1, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream, add)
+                        : launch_one_row<Fmt, R, 1, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
             return true;
         case 2:
-            *err = wide ? launch_one_row<Fmt, R, 2, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream)
-                        : launch_one_row<Fmt, R, 2, 2, 4>(dev, w, n_out, P, log2S, x, y, stream);
+            *err = wide ? launch_one_row<Fmt, R, 2, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream, add)
+                        : launch_one_row<Fmt, R, 2, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
             return true;
         case 3:
-            *err = wide && R == 1 ? launch_one_row<Fmt, R, 3, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream)
-                                  : launch_one_row<Fmt, R, 3, 2, 4>(dev, w, n_out, P, log2S, x, y, stream);
+            *err = wide && R == 1 ? launch_one_row<Fmt, R, 3, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream, add)
+                                  : launch_one_row<Fmt, R, 3, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
             return true;
-        case 4: *err = launch_one_row<Fmt, R, 4, 2, 4>(dev, w, n_out, P, log2S, x, y, stream); return true;
+        case 4: *err = launch_one_row<Fmt, R, 4, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add); return true;
         default: return false;
     }
 }
@@ -1753,6 +1773,17 @@ hipError_t launch_gemv_q6_k(const DeviceInfo& dev, const uint8_t* w, int64_t n_o
 hipError_t launch_gemv_q5_k(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu_pairs,
                             const float* x, int64_t m, int64_t ldx, float* y, int64_t ldy, hipStream_t stream) {
     return launch_gemv_kq<FmtQ5_K>(dev, w, n_out, k, silu_pairs, x, m, ldx, y, ldy, stream);
+}
+
+hipError_t launch_gemv_q8_lora_row(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu_pairs,
+                                   const float* x, const LoraOneRow& lora, float* y, hipStream_t stream) {
+    const int P = (int)(k / 64);
+    hipError_t e = hipErrorInvalidValue;  // k past the one-row kernel
+    if (silu_pairs)
+        try_one_row<FmtQ8_0, 2>(dev, w, (int)n_out, P, slots_log2(P), x, y, stream, &e, lora);
+    else
+        try_one_row<FmtQ8_0, 1>(dev, w, (int)n_out, P, slots_log2(P), x, y, stream, &e, lora);
+    return e;
 }
 
 hipError_t launch_gemv_q8(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu_pairs,

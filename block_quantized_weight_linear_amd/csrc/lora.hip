@@ -4,11 +4,12 @@
 // the inner products u[t][c] = scale[a] * A[a][c] . x[t] of every row (c over the
 // sections' ranks; float32, one wave a product), then each output's dot of u with its row
 // of B, added to the shared product (or, for a fused gate_up, the activation behind it).
-// In the packed calls the first launch also writes the rows' digits and the second
-// computes the shared product (digit_tiles.h); bound by the weights' bytes and, in small
-// matrices, by the two launches' starts: 6144 x 4096 takes 15 us at 2 rows (27 MB, of which
-// the first launch 4), the fused 24576 x 4096 28 us (107 MB at 3.8 TB/s, the second launch
-// alone 4.7), 16 rows 22 and 40 us.  With many rows the correction has a form of its own.
+// In the packed calls the second launch computes the shared product too: one row on the
+// one-row kernel of gemv_q8.hip, more on the digit tiles (digit_tiles.h), whose digits the
+// first launch writes.  Bound by the weights' bytes and, in small matrices, by the two
+// launches' starts: 6144 x 4096 (27 MB) takes 11.5 us at 1 row, 15 at 2 (4 of them the first
+// launch) and 22 at 16, the fused 24576 x 4096 (107 MB) 24.4, 28 (3.8 TB/s) and 39 us.  With
+// many rows the correction has a form of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -17,6 +18,7 @@
 
 #include "digit_tiles.h"
 #include "gemv_core.h"
+#include "lora_core.h"
 #include "q8_internal.h"
 #include "q8_validate.h"
 #include "shared_mem.h"
@@ -24,67 +26,9 @@
 
 namespace q8k {
 
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-
-// Element types of A and B: eight values from a 16-byte aligned address, widened exactly.
-struct LoraF32 {
-    using T = float;
-    struct V {
-        float4 lo, hi;
-    };
-    static __device__ __forceinline__ V load8(const T* p) {
-        return V{*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
-    }
-    static __device__ __forceinline__ float at(const V& v, int q) {
-        const float4& h = q < 4 ? v.lo : v.hi;
-        return (q & 3) == 0 ? h.x : (q & 3) == 1 ? h.y : (q & 3) == 2 ? h.z : h.w;
-    }
-};
-struct LoraF16 {
-    using T = uint16_t;
-    using V = u16x8;
-    static __device__ __forceinline__ V load8(const T* p) { return *reinterpret_cast<const u16x8*>(p); }
-    static __device__ __forceinline__ float at(const V& v, int q) {
-        return (float)__builtin_bit_cast(_Float16, (uint16_t)v[q]);
-    }
-};
-struct LoraBF16 {
-    using T = uint16_t;
-    using V = u16x8;
-    static __device__ __forceinline__ V load8(const T* p) { return *reinterpret_cast<const u16x8*>(p); }
-    static __device__ __forceinline__ float at(const V& v, int q) {
-        return __builtin_bit_cast(float, (uint32_t)v[q] << 16);
-    }
-};
-
-// What the kernels need of a q8_lora, by value.
-struct LoraArgs {
-    const void* a;
-    const void* b;
-    const int32_t* ranks;
-    const float* scale;
-    const int32_t* adapter;
-    int type, n_adapters, rank, n_sections;
-    int64_t end[Q8_LORA_MAX_SECTIONS];  // first row past each section
-
-    // the row's adapter, -1 for none
-    __device__ __forceinline__ int of_row(int64_t t) const {
-        if (n_adapters == 0) return -1;
-        const int a = adapter[t];
-        return a >= 0 && a < n_adapters ? a : -1;
-    }
-    __device__ __forceinline__ int rank_of(int a) const {
-        if (!ranks) return rank;
-        const int r = ranks[a];
-        return r < 0 ? 0 : r < rank ? r : rank;
-    }
-    __device__ __forceinline__ int section(int64_t i) const {
-        int s = 0;
-#pragma unroll
-        for (int q = 0; q < Q8_LORA_MAX_SECTIONS - 1; ++q) s += (q < n_sections - 1 && i >= end[q]) ? 1 : 0;
-        return s;
-    }
-};
+// gemv_q8.hip: q8_linear of one row (k <= 16384) with a correction behind its sums
+hipError_t launch_gemv_q8_lora_row(const DeviceInfo& dev, const uint8_t* w, int64_t n_out, int64_t k, bool silu_pairs,
+                                   const float* x, const LoraOneRow& lora, float* y, hipStream_t stream);
 
 // Four inner products u[t][c0 .. c0+3] by a block of 256 threads, every load of up to 8192
 // elements of the row and the four rows of A issued before the first product.
@@ -165,38 +109,6 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(LoraArgs lo, const fl
         lora_shrink<Ty>(lo, x, k, ldx, u, b - m);
 }
 
-// sum_j B[a][i][j] u[j] of output row i, u the row's inner products
-template <class Ty, int FLY = 4>
-__device__ __forceinline__ float lora_delta(const LoraArgs& lo, int64_t n, int a, int64_t i, const float* u) {
-    const typename Ty::T* br = static_cast<const typename Ty::T*>(lo.b) + ((size_t)a * n + i) * lo.rank;
-    const float* us = u + lo.section(i) * lo.rank;
-    const int r = lo.rank_of(a);
-    float acc = 0.0f;
-    for (int j0 = 0; j0 < r; j0 += 8 * FLY) {  // 8 FLY of B's row in flight
-        typename Ty::V v[FLY];
-        LoraF32::V w[FLY];
-#pragma unroll
-        for (int s = 0; s < FLY; ++s) {
-            const int j = j0 + 8 * s < r ? j0 + 8 * s : j0;
-            v[s] = Ty::load8(br + j);
-            w[s] = LoraF32::load8(us + j);
-        }
-#pragma unroll
-        for (int s = 0; s < FLY; ++s)
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc = j0 + 8 * s + q < r ? __builtin_fmaf(Ty::at(v[s], q), LoraF32::at(w[s], q), acc) : acc;
-    }
-    return acc;
-}
-
-template <int FLY>
-__device__ __forceinline__ float lora_delta_any(const LoraArgs& lo, int64_t n, int a, int64_t i, const float* u) {
-    if (lo.type == Q8_LORA_BF16) return lora_delta<LoraBF16, FLY>(lo, n, a, i, u);
-    if (lo.type == Q8_LORA_F16) return lora_delta<LoraF16, FLY>(lo, n, a, i, u);
-    return lora_delta<LoraF32, FLY>(lo, n, a, i, u);
-}
-
 template <class Ty, bool SILU>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs lo, const float* __restrict__ u, const float* y,
                                                           int64_t n, int64_t ldy, float* out, int64_t ldo, int m) {
@@ -204,13 +116,13 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs lo, const flo
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n_out) return;
     for (int64_t t = blockIdx.y; t < m; t += gridDim.y) {
-        const int a = lo.of_row(t);
+        const int a = lo.of_row(t), r = a < 0 ? 0 : lo.rank_of(a);
         const float* ut = u + t * lo.n_sections * lo.rank;
         float g = y[t * ldy + i];
-        if (a >= 0) g += lora_delta<Ty>(lo, n, a, i, ut);
+        if (a >= 0) g += lora_delta<Ty>(lo, n, a, r, i, ut);
         if constexpr (SILU) {
             float v = y[t * ldy + n_out + i];
-            if (a >= 0) v += lora_delta<Ty>(lo, n, a, n_out + i, ut);
+            if (a >= 0) v += lora_delta<Ty>(lo, n, a, r, n_out + i, ut);
             g = silu_mul(g, v);
         }
         out[t * ldo + i] = g;
@@ -315,13 +227,13 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
                 const int t = m0 + s;
                 const float* sum = sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
                 const int ex = exps[t];
-                const int ad = lo.of_row(t);
+                const int ad = lo.of_row(t), rank = ad < 0 ? 0 : lo.rank_of(ad);
                 const float* ut = u + (size_t)t * lo.n_sections * lo.rank;
                 float v = row_scaled(sum[0], ex);
-                if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, i, ut);
+                if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, rank, i, ut);
                 if constexpr (SILU) {
                     float up = row_scaled(sum[kOut], ex);
-                    if (ad >= 0) up += lora_delta_any<kFly>(lo, 2 * (int64_t)n_out, ad, n_out + (int64_t)i, ut);
+                    if (ad >= 0) up += lora_delta_any<kFly>(lo, 2 * (int64_t)n_out, ad, rank, n_out + (int64_t)i, ut);
                     v = silu_mul(v, up);
                 }
                 y[t * ldy + i] = v;
@@ -670,24 +582,22 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraArgs lo, LoraPlan P
         }
 }
 
-static LoraArgs lora_args(const q8_lora& lo) {
-    LoraArgs a{lo.a, lo.b, lo.ranks, lo.scale, lo.adapter, lo.type, lo.n_adapters, lo.rank, lo.n_sections, {}};
-    int64_t end = 0;
-    for (int s = 0; s < Q8_LORA_MAX_SECTIONS; ++s) {
-        if (s < lo.n_sections) end += lo.section_rows[s];
-        a.end[s] = end;
-    }
-    return a;
+static hipError_t launch_lora_shrink(const LoraArgs& lo, const float* x, int64_t m, int64_t k, int64_t ldx, float* u,
+                                     hipStream_t stream) {
+    const int64_t units = m * (lo.n_sections * lo.rank / kShrinkCols);
+    auto kernel = lo.type == Q8_LORA_F32   ? lora_shrink_kernel<LoraF32>
+                  : lo.type == Q8_LORA_F16 ? lora_shrink_kernel<LoraF16>
+                                           : lora_shrink_kernel<LoraBF16>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(units < 65536 ? units : 65536)), dim3(256), 0, stream, lo, x, (int)m, (int)k,
+                       ldx, u);
+    return hipGetLastError();
 }
 
 template <class Ty>
 static hipError_t lora_add_typed(const LoraArgs& lo, const float* y, int64_t n, int64_t ldy, bool silu,
                                  const float* x, int64_t m, int64_t k, int64_t ldx, float* out, int64_t ldo,
                                  float* u, hipStream_t stream) {
-    const int64_t units = m * (lo.n_sections * lo.rank / kShrinkCols);
-    hipLaunchKernelGGL(lora_shrink_kernel<Ty>, dim3((unsigned)(units < 65536 ? units : 65536)), dim3(256), 0, stream, lo, x, (int)m,
-                       (int)k, ldx, u);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_lora_shrink(lo, x, m, k, ldx, u, stream);
     if (e != hipSuccess) return e;
     const int64_t n_out = silu ? n / 2 : n;
     const dim3 grid((unsigned)((n_out + 255) / 256), (unsigned)(m < 65535 ? m : 65535));
@@ -848,6 +758,14 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     const q8v::LoraWorkspace L =
         q8v::lora_workspace_layout(m, lora.n_sections, lora.rank, q8v::lora_base_bytes(m, n, k));
     char* ws = static_cast<char*>(workspace);
+    if (m == 1 && k <= q8v::kLoraTilesMaxK) {
+        // the inner products, then the one-row kernel with the correction behind its sums
+        const LoraArgs lo = lora_args(lora);
+        float* u = reinterpret_cast<float*>(ws + L.u_off);
+        hipError_t e = lora.n_adapters ? launch_lora_shrink(lo, x, m, k, ldx, u, stream) : hipSuccess;
+        if (e != hipSuccess) return e;
+        return launch_gemv_q8_lora_row(dev, w, n_out, k, silu, x, LoraOneRow{lo, u, n}, y, stream);
+    }
     if (!q8v::lora_uses_tiles(m, n, k)) {
         // the shared product, then the correction in place (behind a fused one: its own)
         float* base = silu ? reinterpret_cast<float*>(ws + L.base_off) : y;

@@ -373,9 +373,11 @@ size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_
  *               overlap (other streams, or captured graphs replayed side by side) need
  *               workspaces of their own.
  * A row of x that holds a NaN or an infinity gives outputs that are not finite; other rows
- * are not touched by it.  Below 256 rows the arithmetic is of float32 accuracy; from 256
- * rows on the shared product takes the bf16 matrix-core tiles of q8_linear, the
- * correction stays in float32.
+ * are not touched by it.  Below 256 rows the arithmetic is of float32 accuracy: products
+ * accumulate in float32, and from two rows on (k <= 16384) an element of x is taken to within
+ * 2^-30 of its row's largest magnitude, and a row's outputs have the same bits whatever other
+ * rows share the call.  From 256 rows on the shared product takes the bf16 matrix-core
+ * tiles of q8_linear, the correction stays in float32.
  */
 q8_status q8_linear_lora(const void* w_q8, int64_t n, int64_t k, const float* x, int64_t m, int64_t ldx,
                          const q8_lora* lora, float* y, int64_t ldy, void* workspace, size_t workspace_bytes,
@@ -420,7 +422,10 @@ size_t q8_moe_layer_workspace_bytes(int64_t m, int32_t k, int64_t n_exp, int64_t
  * A token whose router probabilities are not finite (a NaN or an infinity in its row)
  * gets NaN in every output; other tokens are not touched by it.  Below 8 routed pairs per
  * expert on average (m * k < 8 * n_exp) the results are of float32 accuracy; from there on
- * the expert products run on the bf16 tiles of q8_moe_grouped_linear.
+ * the expert products run on the bf16 tiles of q8_moe_grouped_linear.  Up to 128 tokens, 64
+ * experts a token and f, h <= 6144 the former is two launches, which take an element of x (and
+ * of an expert's hidden row) to within 2^-30 of its row's largest magnitude; a token's
+ * outputs then have the same bits whatever other tokens share the call.
  */
 q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const void* w_down_exps, int64_t n_exp,
                        int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, int32_t normalize,
