@@ -266,6 +266,14 @@ struct TileRun {
         restart(n);
     }
     __device__ __forceinline__ void restart(int n) {
+        start(n);
+        if (n_items > 0)
+            wait_vmcnt<5 * kRing>();
+        else
+            wait_vmcnt<0>();
+    }
+    // The first copies alone: the caller waits, with wait_vmcnt, for digits loaded before.
+    __device__ __forceinline__ void start(int n) {
         n_tiles = n;
         tps = kTileWaves >> W.log2_wt;
         next_tile = W.tg;
@@ -273,12 +281,7 @@ struct TileRun {
         n_items = (W.tg < n_tiles ? (n_tiles - W.tg + tps - 1) / tps : 0) * W.n_sl;
         // kRing items (past the last one: it again) or none, so that the compiler knows how
         // many copies are younger than the digits
-        if (n_items > 0) {
-            unroll<kRing>([&](auto sc) __attribute__((always_inline)) { issue(decltype(sc)::value); });
-            wait_vmcnt<5 * kRing>();
-        } else {
-            wait_vmcnt<0>();
-        }
+        if (n_items > 0) unroll<kRing>([&](auto sc) __attribute__((always_inline)) { issue(decltype(sc)::value); });
     }
     __device__ __forceinline__ void issue(int slot) {
         const uint8_t* tile = tile_at(min(next_tile, n_tiles - 1));

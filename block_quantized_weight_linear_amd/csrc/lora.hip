@@ -179,70 +179,80 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     }, off);
     constexpr int kChunk = kLoraSumTiles / NG;
     constexpr int kFly = SP * NG >= 6 ? 1 : SP * NG >= 4 ? 2 : 4;  // what the digits' registers leave
-    for (int m0 = 4 * NG * blockIdx.y; m0 < m; m0 += 4 * NG * gridDim.y) {
-        const int mm = min(4 * NG, m - m0);
-        int c0 = 0;
-        auto tile_at = [&](int i) __attribute__((always_inline)) { return w + (size_t)row0_of(c0 + i) * rb; };
-        i64x2 a[NG][SP][4];
+    int m0 = 4 * NG * blockIdx.y, c0 = 0;  // the rows and the block's tile the run starts at
+    auto tile_at = [&](int i) __attribute__((always_inline)) { return w + (size_t)row0_of(c0 + i) * rb; };
+    i64x2 a[NG][SP][4];
+    auto load = [&] __attribute__((always_inline)) {
+        const int last = min(4 * NG, m - m0) - 1;
         load_digits<SP, NG>(W, [&](int s) __attribute__((always_inline)) {
-            return dig + (size_t)(m0 + min(s, mm - 1)) * k * 4;
+            return dig + (size_t)(m0 + min(s, last)) * k * 4;
         }, a);
-        TileRun run(W, off, min(kChunk, tiles), tile_at);
-        while (true) {
-            const int nt = run.n_tiles;
-            multiply_tiles<SP, NG>(run, a, part, sums);
-            __syncthreads();
-            bool finish = true;
-            if (split.ks > 1) {
-                const int64_t group = m0 / (4 * NG);
-                float* mine = split.partial + ((group * split.ks + kz) * tiles_all + first + c0) * (NG * 64);
-                const int64_t range = (int64_t)tiles_all * (NG * 64);
-                for (int i = threadIdx.x; i < nt * NG * 64; i += kTileThreads) store_shared(mine + i, sums[i]);
-                wait_vmcnt_mem<0>();
-                __syncthreads();
-                if (threadIdx.x == 0)
-                    before = __hip_atomic_fetch_add(split.arrived + group * tiles_all + first + c0, 1u, __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-                __syncthreads();
-                finish = (int)before == split.ks - 1;
-                if (finish)
-                    for (int i = 2 * threadIdx.x; i < nt * NG * 64; i += 2 * kTileThreads) {
-                        float2 v = load_shared(mine + i - kz * range);
-                        for (int z = 1; z < split.ks; ++z) {
-                            const float2 t = load_shared(mine + i + (z - kz) * range);
-                            v.x += t.x;
-                            v.y += t.y;
-                        }
-                        sums[i] = v.x;
-                        sums[i + 1] = v.y;
-                    }
-                __syncthreads();
-            }
-            // outputs of the chunk: (row of the call, tile, output of the tile), outputs fastest
-            for (int o = threadIdx.x; finish && o < mm * nt * kOut; o += kTileThreads) {
-                const int r = o % kOut, q = o / kOut;
-                const int s = q / nt, tile = q - s * nt;
-                const int i = row0_of(c0 + tile) + r;
-                if (i >= n_out) continue;
-                const int t = m0 + s;
-                const float* sum = sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
-                const int ex = exps[t];
-                const int ad = lo.of_row(t), rank = ad < 0 ? 0 : lo.rank_of(ad);
-                const float* ut = u + (size_t)t * lo.n_sections * lo.rank;
-                float v = row_scaled(sum[0], ex);
-                if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, rank, i, ut);
-                if constexpr (SILU) {
-                    float up = row_scaled(sum[kOut], ex);
-                    if (ad >= 0) up += lora_delta_any<kFly>(lo, 2 * (int64_t)n_out, ad, rank, n_out + (int64_t)i, ut);
-                    v = silu_mul(v, up);
-                }
-                y[t * ldy + i] = v;
-            }
-            __syncthreads();  // the next chunk overwrites the sums
-            c0 += nt;
-            if (c0 >= tiles) break;
-            run.restart(min(kChunk, tiles - c0));
+    };
+    load();
+    TileRun run(W, off, min(kChunk, tiles), tile_at);
+    while (true) {
+        const int nt = run.n_tiles, t0 = m0, tile0 = c0, mm = min(4 * NG, m - m0);
+        multiply_tiles<SP, NG>(run, a, part, sums);
+        __syncthreads();
+        // the next run's digits and first weights come while this one's outputs are finished
+        // (83 rows of 2001 x 1024, three runs a block: MEASURED)
+        c0 += nt;
+        if (c0 >= tiles) {
+            c0 = 0;
+            m0 += 4 * NG * gridDim.y;
+            if (m0 < m) load();
         }
+        const bool more = m0 < m;
+        if (more) run.start(min(kChunk, tiles - c0));
+        bool finish = true;
+        if (split.ks > 1) {
+            const int64_t group = t0 / (4 * NG);
+            float* mine = split.partial + ((group * split.ks + kz) * tiles_all + first + tile0) * (NG * 64);
+            const int64_t range = (int64_t)tiles_all * (NG * 64);
+            for (int i = threadIdx.x; i < nt * NG * 64; i += kTileThreads) store_shared(mine + i, sums[i]);
+            wait_vmcnt_mem<0>();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                before = __hip_atomic_fetch_add(split.arrived + group * tiles_all + first + tile0, 1u, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            finish = (int)before == split.ks - 1;
+            if (finish)
+                for (int i = 2 * threadIdx.x; i < nt * NG * 64; i += 2 * kTileThreads) {
+                    float2 v = load_shared(mine + i - kz * range);
+                    for (int z = 1; z < split.ks; ++z) {
+                        const float2 t = load_shared(mine + i + (z - kz) * range);
+                        v.x += t.x;
+                        v.y += t.y;
+                    }
+                    sums[i] = v.x;
+                    sums[i + 1] = v.y;
+                }
+            __syncthreads();
+        }
+        // outputs of the chunk: (row of the call, tile, output of the tile), outputs fastest
+        for (int o = threadIdx.x; finish && o < mm * nt * kOut; o += kTileThreads) {
+            const int r = o % kOut, q = o / kOut;
+            const int s = q / nt, tile = q - s * nt;
+            const int i = row0_of(tile0 + tile) + r;
+            if (i >= n_out) continue;
+            const int t = t0 + s;
+            const float* sum = sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
+            const int ex = exps[t];
+            const int ad = lo.of_row(t), rank = ad < 0 ? 0 : lo.rank_of(ad);
+            const float* ut = u + (size_t)t * lo.n_sections * lo.rank;
+            float v = row_scaled(sum[0], ex);
+            if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, rank, i, ut);
+            if constexpr (SILU) {
+                float up = row_scaled(sum[kOut], ex);
+                if (ad >= 0) up += lora_delta_any<kFly>(lo, 2 * (int64_t)n_out, ad, rank, n_out + (int64_t)i, ut);
+                v = silu_mul(v, up);
+            }
+            y[t * ldy + i] = v;
+        }
+        __syncthreads();  // the next run overwrites the sums
+        if (!more) break;
+        wait_vmcnt<0>();
     }
 }
 
@@ -263,7 +273,7 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 //   4. outer:  block (tile, 128 outputs), 64 rows x 32 outputs a wave: u and B start out,
 //              then the product's values, and no barrier lies between.
 // Bound by the memory: x once, the product in and out.  6144 x 4096, three sections of rank
-// 16 and 2048 rows: 59 us (plan 4.6, inner 19, sum 5.8, outer 30: 100 MB of product in and out
+// 32 and 2048 rows: 59 us (plan 4.6, inner 19, sum 5.8, outer 30: 100 MB of product in and out
 // at 3.4 TB/s).  Measured and not kept: u staged through LDS in the outer launch (37 us), the
 // parts added by the last block of the inner one (33 us against 19 + 6), its next step's
 // loads ahead (25 us).

@@ -374,7 +374,7 @@ size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_
  *               workspaces of their own.
  * A row of x that holds a NaN or an infinity gives outputs that are not finite; other rows
  * are not touched by it.  Below 256 rows the arithmetic is of float32 accuracy: products
- * accumulate in float32, and from two rows on (k <= 16384) an element of x is taken to within
+ * accumulate in float32, and from two rows on (k <= 16384, W below 2 GiB) an element of x is taken to within
  * 2^-30 of its row's largest magnitude, and a row's outputs have the same bits whatever other
  * rows share the call.  From 256 rows on the shared product takes the bf16 matrix-core
  * tiles of q8_linear, the correction stays in float32.
