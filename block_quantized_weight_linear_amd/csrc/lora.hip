@@ -94,19 +94,31 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs lo, const flo
     }
 }
 
+// What the second launch needs of a row beside its digits, in one load: an output's loads of
+// its exponent, adapter and rank one after the other were a good part of a tile's end.
+struct alignas(16) TileRow {
+    int exp, adapter, rank, unused;
+};
+
 // First launch of the packed calls: blocks 0 .. m-1 write the rows' digits, the others the
 // inner products.
 template <class Ty>
 __global__ __launch_bounds__(256) void lora_prepare_kernel(LoraArgs lo, const float* __restrict__ x, int m, int k,
                                                            int64_t ldx, float* __restrict__ u,
-                                                           int8_t* __restrict__ dig, int* __restrict__ exps,
+                                                           int8_t* __restrict__ dig, TileRow* __restrict__ rows,
                                                            uint32_t* __restrict__ arrived, int counters) {
     const int b = blockIdx.x;
     for (int i = b * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
-    if (b < m)
-        write_digits(x + b * ldx, k, dig + (size_t)b * k * 4, exps + b);
-    else
+    if (b < m) {
+        write_digits(x + b * ldx, k, dig + (size_t)b * k * 4, &rows[b].exp);
+        if (threadIdx.x == 0) {
+            const int a = lo.of_row(b);
+            rows[b].adapter = a;
+            rows[b].rank = a < 0 ? 0 : lo.rank_of(a);
+        }
+    } else {
         lora_shrink<Ty>(lo, x, k, ldx, u, b - m);
+    }
 }
 
 template <class Ty, bool SILU>
@@ -152,7 +164,7 @@ template <int SP, int NG, bool SILU>
 __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t* __restrict__ w, int n_out, int k,
                                                                   TileSplit split,
                                                                   const int8_t* __restrict__ dig,
-                                                                  const int* __restrict__ exps, LoraArgs lo,
+                                                                  const TileRow* __restrict__ rows, LoraArgs lo,
                                                                   const float* __restrict__ u, int m,
                                                                   float* __restrict__ y, int64_t ldy) {
     extern __shared__ float4 smem4[];
@@ -238,8 +250,8 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
             if (i >= n_out) continue;
             const int t = t0 + s;
             const float* sum = sums + (tile * NG + (s >> 2)) * 64 + 16 * (s & 3) + r;
-            const int ex = exps[t];
-            const int ad = lo.of_row(t), rank = ad < 0 ? 0 : lo.rank_of(ad);
+            const int4 row = *reinterpret_cast<const int4*>(rows + t);
+            const int ex = row.x, ad = row.y, rank = row.z;
             const float* ut = u + (size_t)t * lo.n_sections * lo.rank;
             float v = row_scaled(sum[0], ex);
             if (ad >= 0) v += lora_delta_any<kFly>(lo, SILU ? 2 * (int64_t)n_out : n_out, ad, rank, i, ut);
@@ -721,7 +733,7 @@ static TileCut tile_cut(const DeviceInfo& dev, int64_t tiles, int64_t k) {
 template <int SP, int NG, bool SILU>
 static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, int64_t m, const uint8_t* w,
                                     int64_t n_out, int64_t k, const TileSplit& split, const int8_t* dig,
-                                    const int* exps, const LoraArgs& lo, const float* u, float* y, int64_t ldy,
+                                    const TileRow* rows, const LoraArgs& lo, const float* u, float* y, int64_t ldy,
                                     hipStream_t stream) {
     auto kernel = lora_tiles_kernel<SP, NG, SILU>;
     constexpr size_t lds = lora_tiles_lds<NG>();
@@ -738,7 +750,7 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, i
     const int64_t gx = (int64_t)cut.runs * cut.ks;
     const int64_t gy = dev.cu_count / gx < groups ? dev.cu_count / gx : groups;
     const dim3 grid((unsigned)gx, (unsigned)(gy < 1 ? 1 : gy));
-    hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, split, dig, exps, lo, u,
+    hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, split, dig, rows, lo, u,
                        (int)m, y, ldy);
     return hipGetLastError();
 }
@@ -791,7 +803,7 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     const int64_t tiles = (n_out + per_tile - 1) / per_tile;
     const TileCut cut = tile_cut(dev, tiles, k);
     const q8v::LoraTilesWorkspace T = q8v::lora_tiles_workspace_layout(m, n, k);
-    int* exps = reinterpret_cast<int*>(ws + L.base_off + T.exps_off);
+    TileRow* rows = reinterpret_cast<TileRow*>(ws + L.base_off + T.rows_off);
     int8_t* dig = reinterpret_cast<int8_t*>(ws + L.base_off + T.dig_off);
     TileSplit split{cut.ks, cut.log2_wt, reinterpret_cast<float*>(ws + L.base_off + T.partial_off),
                     reinterpret_cast<uint32_t*>(ws + L.base_off + T.arrived_off)};
@@ -800,17 +812,17 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     const dim3 grid((unsigned)((int)m + units));
     if (lora.type == Q8_LORA_F32)
         hipLaunchKernelGGL(lora_prepare_kernel<LoraF32>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
-                           exps, split.arrived, counters);
+                           rows, split.arrived, counters);
     else if (lora.type == Q8_LORA_F16)
         hipLaunchKernelGGL(lora_prepare_kernel<LoraF16>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
-                           exps, split.arrived, counters);
+                           rows, split.arrived, counters);
     else
         hipLaunchKernelGGL(lora_prepare_kernel<LoraBF16>, grid, dim3(256), 0, stream, lo, x, (int)m, (int)k, ldx, u, dig,
-                           exps, split.arrived, counters);
+                           rows, split.arrived, counters);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return silu ? launch_lora_tiles_m<true>(dev, cut, m, w, n_out, k, split, dig, exps, lo, u, y, ldy, stream)
-                : launch_lora_tiles_m<false>(dev, cut, m, w, n_out, k, split, dig, exps, lo, u, y, ldy, stream);
+    return silu ? launch_lora_tiles_m<true>(dev, cut, m, w, n_out, k, split, dig, rows, lo, u, y, ldy, stream)
+                : launch_lora_tiles_m<false>(dev, cut, m, w, n_out, k, split, dig, rows, lo, u, y, ldy, stream);
 }
 
 }  // namespace q8k

@@ -298,10 +298,10 @@ inline bool lora_uses_tiles(int64_t m, int64_t n, int64_t k) {
 // Row groups of four, as many as any form has.
 inline int64_t lora_row_groups(int64_t m) { return (m + 3) / 4; }
 
-// Workspace behind the adapters', from its start: the rows' exponents and digits, and for a
+// Workspace behind the adapters', from its start: four words a row, the digits, and for a
 // cut k the ranges' sums and their counts (a tile: 16 rows of the matrix).
 struct LoraTilesWorkspace {
-    size_t exps_off, dig_off, partial_off, arrived_off, total;
+    size_t rows_off, dig_off, partial_off, arrived_off, total;
 };
 inline LoraTilesWorkspace lora_tiles_workspace_layout(int64_t m, int64_t n, int64_t k) {
     LoraTilesWorkspace w{};
@@ -309,7 +309,7 @@ inline LoraTilesWorkspace lora_tiles_workspace_layout(int64_t m, int64_t n, int6
     const size_t tiles = size_t((n + 15) / 16 + 1);  // + 1: gate and up rows round up apart
     const size_t rows = size_t((m + 15) / 16 * 16);
     size_t off = 0;
-    w.exps_off = off;    off = round_up(off + sizeof(int32_t) * size_t(m), 256);
+    w.rows_off = off;    off = round_up(off + 16 * size_t(m), 256);
     w.dig_off = off;     off = round_up(off + 4 * size_t(m) * size_t(k), 256);
     w.partial_off = off; off = round_up(off + (cut ? sizeof(float) * size_t(kLoraMaxRanges) * tiles * 16 * rows : 0), 256);
     w.arrived_off = off; off = round_up(off + (cut ? sizeof(uint32_t) * size_t(lora_row_groups(m)) * tiles : 0), 256);
