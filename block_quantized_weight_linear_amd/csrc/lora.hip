@@ -744,12 +744,23 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, i
         if (e != hipSuccess) return e;
         attr_dev = dev.device;
     }
-    // one block per CU; a matrix with fewer tiles than half the CUs hands its row groups to
-    // blocks of their own
-    const int64_t groups = (m + 4 * NG - 1) / (4 * NG);
-    const int64_t gx = (int64_t)cut.runs * cut.ks;
-    const int64_t gy = dev.cu_count / gx < groups ? dev.cu_count / gx : groups;
-    const dim3 grid((unsigned)gx, (unsigned)(gy < 1 ? 1 : gy));
+    // one block per CU, shared between runs of tiles and groups of rows: gy groups at a time,
+    // the gy with the cheapest block.  Costs in items (a wave's 16 x 256 weights): a pass over
+    // the rows about 6, finishing the tiles whose sums fit LDS about 10.
+    const int64_t groups = (m + 4 * NG - 1) / (4 * NG), tiles = (n_out + (SILU ? 8 : 16) - 1) / (SILU ? 8 : 16);
+    const int64_t at_once = kTileWaves >> cut.log2_wt, chunk = kLoraSumTiles / NG;
+    int64_t gy = 1, runs = cut.runs, cost = 0;
+    for (int64_t g = 1; g <= groups && g * cut.ks <= dev.cu_count; ++g) {
+        const int64_t r = std::min<int64_t>(tiles, dev.cu_count / (cut.ks * g)), most = (tiles + r - 1) / r;
+        const int64_t c = (groups + g - 1) / g *
+                          (6 + 10 * ((most + chunk - 1) / chunk) + (most + at_once - 1) / at_once * cut.sp);
+        if (cost == 0 || c < cost) {
+            cost = c;
+            gy = g;
+            runs = r;
+        }
+    }
+    const dim3 grid((unsigned)(runs * cut.ks), (unsigned)gy);
     hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, split, dig, rows, lo, u,
                        (int)m, y, ldy);
     return hipGetLastError();
