@@ -7,8 +7,10 @@
 // In the packed calls the second launch computes the shared product too: one row on the
 // one-row kernel of gemv_q8.hip, more on the digit tiles (digit_tiles.h), whose digits the
 // first launch writes.  Bound by the weights' bytes and, in small matrices, by the two
-// launches' starts: 6144 x 4096 (27 MB) takes 11.5 us at 1 row, 15 at 2 (4 of them the first
-// launch) and 22 at 16, the fused 24576 x 4096 (107 MB) 24.4, 28 (3.8 TB/s) and 39 us.  With
+// launches' starts: 6144 x 4096 (27 MB) takes 11.3 us at 1 row, 15 at 2 (4 of them the first
+// launch) and 21 at 16, the fused 24576 x 4096 (107 MB) 23.4, 28 (3.8 TB/s) and 37 us; from 16
+// rows on by the tiles' arithmetic (digits, scales and sums: 37, 63 and 116 us at 64, 128 and 255
+// rows of 6144 x 4096).  With
 // many rows the correction has a form of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -143,13 +145,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs lo, const flo
 
 // Second launch of the packed calls: the shared product's tiles with the correction (and,
 // SILU, the activation) behind each.  A block owns a run of neighbouring tiles and streams
-// them once for every 4 * NG rows (blockIdx.y: every gridDim.y-th of those); a fused tile is
+// them once for every 4 * NG rows (every gy-th group of those); a fused tile is
 // 8 gate rows and their 8 up rows.  A row of more than 16 slices (k > 4096) is cut into ks
-// ranges, blocks b % ks taking range b % ks of the same tiles: the digits of a range fit
+// ranges, each with blocks of its own for the same tiles: the digits of a range fit
 // the registers for as many tiles as the block has.  The ranges' sums then go through
 // memory, and the last block of a tile adds them up, in their order, and finishes it.
 struct TileSplit {
     int ks, log2_wt;    // ranges; waves a tile within a range
+    int runs, gy;       // runs of tiles; groups of rows at a time
     float* partial;     // [row group][range][tile][NG * 64]
     uint32_t* arrived;  // [row group][tile]: ranges there, zero before the launch
 };
@@ -172,7 +175,11 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     float* part = reinterpret_cast<float*>(smem + kRingBytes);
     float* sums = part + 2 * kTileWaves * NG * 64;
     __shared__ uint32_t before;
-    const int kz = blockIdx.x % split.ks, runs = gridDim.x / split.ks, run_id = blockIdx.x / split.ks;
+    // blocks that stream the same weights for other rows lie on the same XCD (workgroups go to
+    // the 8 XCDs in turn), whose L2 reads them once
+    const int place = blockIdx.x / 8, unit = blockIdx.x % 8 + 8 * (place / split.gy), gy = split.gy, runs = split.runs;
+    if (unit >= runs * split.ks) return;
+    const int kz = unit % split.ks, run_id = unit / split.ks;
     const int s0 = (k >> 8) * kz / split.ks, s1 = (k >> 8) * (kz + 1) / split.ks;
     const TileWave W(smem, s1 - s0, split.log2_wt, s0);
     constexpr int kOut = SILU ? kTileRows / 2 : kTileRows;  // outputs of a tile
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
     }, off);
     constexpr int kChunk = kLoraSumTiles / NG;
     constexpr int kFly = SP * NG >= 6 ? 1 : SP * NG >= 4 ? 2 : 4;  // what the digits' registers leave
-    int m0 = 4 * NG * blockIdx.y, c0 = 0;  // the rows and the block's tile the run starts at
+    int m0 = 4 * NG * (place % gy), c0 = 0;  // the rows and the block's tile the run starts at
     auto tile_at = [&](int i) __attribute__((always_inline)) { return w + (size_t)row0_of(c0 + i) * rb; };
     i64x2 a[NG][SP][4];
     auto load = [&] __attribute__((always_inline)) {
@@ -207,11 +214,11 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
         multiply_tiles<SP, NG>(run, a, part, sums);
         __syncthreads();
         // the next run's digits and first weights come while this one's outputs are finished
-        // (83 rows of 2001 x 1024, three runs a block: MEASURED)
+        // (24576 x 4096 fused, 64 rows: 134 us without, 128 with)
         c0 += nt;
         if (c0 >= tiles) {
             c0 = 0;
-            m0 += 4 * NG * gridDim.y;
+            m0 += 4 * NG * gy;
             if (m0 < m) load();
         }
         const bool more = m0 < m;
@@ -732,7 +739,7 @@ static TileCut tile_cut(const DeviceInfo& dev, int64_t tiles, int64_t k) {
 
 template <int SP, int NG, bool SILU>
 static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, int64_t m, const uint8_t* w,
-                                    int64_t n_out, int64_t k, const TileSplit& split, const int8_t* dig,
+                                    int64_t n_out, int64_t k, TileSplit split, const int8_t* dig,
                                     const TileRow* rows, const LoraArgs& lo, const float* u, float* y, int64_t ldy,
                                     hipStream_t stream) {
     auto kernel = lora_tiles_kernel<SP, NG, SILU>;
@@ -746,12 +753,17 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, i
     }
     // one block per CU, shared between runs of tiles and groups of rows: gy groups at a time,
     // the gy with the cheapest block.  Costs in items (a wave's 16 x 256 weights): a pass over
-    // the rows about 6, finishing the tiles whose sums fit LDS about 10.
+    // the rows about 6, finishing the tiles whose sums fit LDS about 10.  One group at a time,
+    // which streams the weights anew for each, against this: 6144 x 4096 at 64 rows 68 | 37 us, 255
+    // rows 252 | 116 us; 83 rows of 2001 x 1024 24.5 | 16.7 us.
     const int64_t groups = (m + 4 * NG - 1) / (4 * NG), tiles = (n_out + (SILU ? 8 : 16) - 1) / (SILU ? 8 : 16);
     const int64_t at_once = kTileWaves >> cut.log2_wt, chunk = kLoraSumTiles / NG;
     int64_t gy = 1, runs = cut.runs, cost = 0;
-    for (int64_t g = 1; g <= groups && g * cut.ks <= dev.cu_count; ++g) {
-        const int64_t r = std::min<int64_t>(tiles, dev.cu_count / (cut.ks * g)), most = (tiles + r - 1) / r;
+    for (int64_t g = 1; g <= groups; ++g) {
+        // (g > 1: every XCD's blocks have CUs of their own)
+        const int64_t r = std::min<int64_t>(tiles, g == 1 ? cut.runs : dev.cu_count / (8 * g) * 8 / cut.ks);
+        if (r < 1) break;
+        const int64_t most = (tiles + r - 1) / r;
         const int64_t c = (groups + g - 1) / g *
                           (6 + 10 * ((most + chunk - 1) / chunk) + (most + at_once - 1) / at_once * cut.sp);
         if (cost == 0 || c < cost) {
@@ -760,7 +772,9 @@ static hipError_t launch_lora_tiles(const DeviceInfo& dev, const TileCut& cut, i
             runs = r;
         }
     }
-    const dim3 grid((unsigned)(runs * cut.ks), (unsigned)gy);
+    split.runs = (int)runs;
+    split.gy = (int)gy;
+    const dim3 grid((unsigned)(8 * gy * ((runs * cut.ks + 7) / 8)));
     hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), lds, stream, w, (int)n_out, (int)k, split, dig, rows, lo, u,
                        (int)m, y, ldy);
     return hipGetLastError();
@@ -816,7 +830,7 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     const q8v::LoraTilesWorkspace T = q8v::lora_tiles_workspace_layout(m, n, k);
     TileRow* rows = reinterpret_cast<TileRow*>(ws + L.base_off + T.rows_off);
     int8_t* dig = reinterpret_cast<int8_t*>(ws + L.base_off + T.dig_off);
-    TileSplit split{cut.ks, cut.log2_wt, reinterpret_cast<float*>(ws + L.base_off + T.partial_off),
+    TileSplit split{cut.ks, cut.log2_wt, 0, 0, reinterpret_cast<float*>(ws + L.base_off + T.partial_off),
                     reinterpret_cast<uint32_t*>(ws + L.base_off + T.arrived_off)};
     const int counters = cut.ks > 1 ? (int)(q8v::lora_row_groups(m) * tiles) : 0;
     const int units = lora.n_adapters ? (int)m * (lora.n_sections * lora.rank / kShrinkCols) : 0;

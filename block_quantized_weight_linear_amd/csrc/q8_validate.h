@@ -286,9 +286,9 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
 // for widths up to 64 slices and fused matrices whose up rows lie within 32-bit byte offsets
 // of their gate rows; one row on q8_linear's one-row kernel with the correction behind its
 // sums; the rest on q8_linear's kernels and the correction in launches of its own.  Measured,
-// in us, at 1 | 2 | 16 | 255 rows, rank 16: 6144 x 4096 on tiles 15.0 | 15.1 | 21.7 | 249, otherwise
-// 11.5 | 15.6 | 27.5 | 346; fused 24576 x 4096 28.0 | 28.3 | 38.7 | 509 and 24.4 | 31.7 | 59.9 |
-// 850; 4096 x 12288 24.3 | 24.2 | 43.3 | 510 and 17.0 | 26.3 | 48.5 | 633.
+// in us, at 1 | 2 | 16 | 255 rows, rank 16: 6144 x 4096 on tiles 15.0 | 15.1 | 21 | 116, otherwise
+// 11.3 | 15.6 | 27.5 | 346; fused 24576 x 4096 28.0 | 28.3 | 37 | 377 and 23.4 | 31.7 | 59.9 |
+// 850; 4096 x 12288 24.3 | 24.2 | 33 | 262 and 16.6 | 26.3 | 48.5 | 633.
 constexpr int64_t kLoraTilesMaxK = 16384;
 constexpr int64_t kLoraTilesMaxRange = 16 * 256;  // of k without a cut
 constexpr int64_t kLoraMaxRanges = 6;             // at most two more than the fewest, 4
