@@ -10,8 +10,7 @@
 // launches' starts: 6144 x 4096 (27 MB) takes 11.3 us at 1 row, 15 at 2 (4 of them the first
 // launch) and 21 at 16, the fused 24576 x 4096 (107 MB) 23.4, 28 (3.8 TB/s) and 37 us; from 16
 // rows on by the tiles' arithmetic (digits, scales and sums: 37, 63 and 116 us at 64, 128 and 255
-// rows of 6144 x 4096).  With
-// many rows the correction has a form of its own.
+// rows of 6144 x 4096).  With many rows the correction has a form of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
