@@ -73,10 +73,10 @@ __device__ __forceinline__ void copy_item(const uint8_t* base, const uint32_t (&
     GlobalBytes* g = (GlobalBytes*)base;
     LdsBytes* l = (LdsBytes*)lds;
     __builtin_amdgcn_global_load_lds(g + off[0], l, 16, 0, kNonTemporal);
-    __builtin_amdgcn_global_load_lds(g + off[1], l + 1024, 16, 0, kNonTemporal);
-    __builtin_amdgcn_global_load_lds(g + off[2], l + 2048, 16, 0, kNonTemporal);
-    __builtin_amdgcn_global_load_lds(g + off[3], l + 3072, 16, 0, kNonTemporal);
-    __builtin_amdgcn_global_load_lds(g + off[4], l + 4096, 4, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[1], l + 1 * 1024, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[2], l + 2 * 1024, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[3], l + 3 * 1024, 16, 0, kNonTemporal);
+    __builtin_amdgcn_global_load_lds(g + off[4], l + 4 * 1024, 4, 0, kNonTemporal);
 }
 
 // A lane's share of an item: of each block pair q the dwords holding the lane's quants of its

@@ -309,6 +309,35 @@ def test_adding_does_not_depend_on_the_other_rows(q8, m):
     assert torch.equal(whole[ids < 0], y[ids < 0])
 
 
+@pytest.mark.parametrize("n,k,rank,sections", [(6144, 4096, 16, [4096, 1024, 1024]), (517, 8192, 40, None),
+                                               (4099, 8192, 8, [4000, 99]), (3000, 12288, 64, None),
+                                               (901, 16384, 24, [900, 1]), (24, 20480, 8, None)])
+def test_one_row(q8, n, k, rank, sections):
+    """The correction behind the one-row kernel, in all its forms; beyond it; and without a
+    correction the same values as the linears alone."""
+    lib, torch, dev = q8
+    f = n // 2
+    c = Case(q8, 65 + n, 1, n, k, 3, rank, TYPES[n % 3], sections, none=0.0)
+    w, w64 = packed(66, n, k)
+    wd = to_dev(w, dev)
+    y, bound = added(*product(w64, c.x), *c.delta())
+    got = lib.q8_linear_lora(wd, n, k, c.xd, *c.args, **c.more)
+    check(got, y, bound, "q8_linear_lora")
+    if n % 2 == 0:
+        h = lib.q8_linear_fused_gate_up_silu_lora(wd, f, k, c.xd, *c.args, **c.more)
+        check(h, *activated(y, bound, f), "q8_linear_fused_gate_up_silu_lora")
+    for a, b, i in ((c.a[:0], c.b[:0], 0), (c.a, c.b, -1), (c.a, c.b, 3)):
+        ids = torch.tensor([i], dtype=torch.int32, device=dev)
+        more = dict(sections=sections)
+        assert torch.equal(lib.q8_linear_lora(wd, n, k, c.xd, a, b, ids, **more), lib.q8_linear(wd, n, k, c.xd))
+        if n % 2 == 0:
+            assert torch.equal(lib.q8_linear_fused_gate_up_silu_lora(wd, f, k, c.xd, a, b, ids, **more),
+                               lib.q8_linear_fused_gate_up_silu(wd, f, k, c.xd))
+    x = c.xd.clone()
+    x[0, k - 1] = float("inf")
+    assert not torch.isfinite(lib.q8_linear_lora(wd, n, k, x, *c.args, **c.more)).any()
+
+
 # The matrix-core form: calls whose rows would read 160 MB of their adapters.  Few rows of wide
 # and many of narrow adapters, odd outputs, sections that end inside a block of 128 outputs,
 # adapters with fewer rows than a tile, one adapter for all, one part of k and several
