@@ -122,7 +122,7 @@ LINEARS = [(1, 64, 256, 1, 8, None), (1, 2001, 1024, 3, 16, [1500, 501]), (2, 16
            (255, 129, 512, 30, 16, None), (3, 40, 12288, 2, 8, None), (6, 24, 16384, 2, 16, [8, 16]),
            (2, 18, 20480, 1, 8, None),
            # rows of 17 to 64 slices cut into ranges: uneven ones, more rows than one pass takes,
-           # more tiles than blocks, and past the rows that are cut
+           # more tiles than blocks, many rows
            (1, 4096, 5888, 1, 8, None), (13, 700, 8192, 3, 8, [350, 350]), (64, 33, 8448, 4, 8, None),
            (65, 20, 4352, 4, 8, None), (7, 9000, 4352, 2, 8, None), (130, 90, 8192, 9, 16, [30, 60]),
            (255, 333, 5120, 3, 8, None)]
