@@ -3,8 +3,8 @@
 //
 //   1. prepare: the router's logits (summed in the order of the routers of route_topk.hip),
 //      every token's digits (digit_tiles.h), the counters of the second launch cleared.
-//   2. layer: one block per CU.  Every block selects all tokens' experts by itself (the same
-//      code as the routers: the same choice) and so knows the whole work list: the gate_up
+//   2. layer: one block per CU.  Every block selects all tokens' experts by itself (the
+//      routers' choice, to the bit) and so knows the whole work list: the gate_up
 //      tiles of the chosen experts (8 gate rows and their 8 up rows), their down tiles, then
 //      the tokens' weighted sums.  An expert's tokens, eight at most, are one job; the jobs'
 //      tiles are cut into one chunk of neighbouring tiles for each block.  A down chunk
@@ -433,12 +433,15 @@ __device__ __forceinline__ void choose_experts(const float (&l)[NP], int lane, i
             my_expert = 64 * plane + at;
         }
     }
-    const float p = lane < k ? expf(key_value(my_key) - mx) * inv_sum : 0.0f;
-    // running sums in selection order
+    const float ex = lane < k ? expf(key_value(my_key) - mx) : 0.0f;
+    const float p = ex * inv_sum;
+    // running sums in selection order, each step one fma of the unscaled exponential, as the
+    // routers form them: adding the rounded p instead gives other last bits in a quarter of
+    // the normalized weights, and another cut next to the top-p share
     float psum = 0.0f, before = 0.0f, through = 0.0f;
     for (int j = 0; j < k; ++j) {
         if (lane == j) before = psum;
-        psum += lane_f(p, j);
+        psum = __builtin_fmaf(lane_f(ex, j), inv_sum, psum);
         if (lane == j) through = psum;
     }
     const bool all = !(top_p < 1.0f);

@@ -121,7 +121,7 @@ __device__ __forceinline__ void select_topk(LogitOf&& logit_of, int lane, int to
         if (lane == wl) taken |= 1 << wc;
         const float p = bp * inv_sum;
         const float before = psum;
-        psum += p;
+        psum = __builtin_fmaf(bp, inv_sum, psum);  // moe_layer.hip's choose_experts forms it alike
         if ((j & 63) == lane) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
