@@ -252,7 +252,8 @@ inline bool lora_uses_matrix_cores(const q8_lora& lo, int64_t m, int64_t n, int6
     if (m < kLoraTiledRows) return false;
     const int64_t row = (int64_t(lo.n_sections) * k + n) * lo.rank * (lo.type == Q8_LORA_F32 ? 4 : 2);
     const int64_t blocks = n / kLoraOuterColumns + 2 * Q8_LORA_MAX_SECTIONS + 1;
-    return m * row >= kLoraTiledBytes && lora_max_tiles(m, lo.n_adapters) * blocks * 256 < (int64_t(1) << 32);
+    // m * row >= kLoraTiledBytes; the product itself can pass 63 bits
+    return row >= (kLoraTiledBytes + m - 1) / m && lora_max_tiles(m, lo.n_adapters) * blocks * 256 < (int64_t(1) << 32);
 }
 inline int64_t lora_parts(int64_t m) {
     if (m < kLoraTiledRows) return 1;
