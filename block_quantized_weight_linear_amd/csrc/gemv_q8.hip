@@ -1482,8 +1482,13 @@ bool try_one_row(const DeviceInfo& dev, const uint8_t* w, int n_out, int P, int 
                         : launch_one_row<Fmt, R, 2, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
             return true;
         case 3:
-            *err = wide && R == 1 ? launch_one_row<Fmt, R, 3, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream, add)
-                                  : launch_one_row<Fmt, R, 3, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
+            if constexpr (R == 1) {  // two rows an output of three rounds: always the narrow form
+                if (wide) {
+                    *err = launch_one_row<Fmt, R, 3, 1, 8, true>(dev, w, n_out, P, log2S, x, y, stream, add);
+                    return true;
+                }
+            }
+            *err = launch_one_row<Fmt, R, 3, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add);
             return true;
         case 4: *err = launch_one_row<Fmt, R, 4, 2, 4>(dev, w, n_out, P, log2S, x, y, stream, add); return true;
         default: return false;
