@@ -454,7 +454,12 @@ __device__ __forceinline__ void choose_experts(const float (&l)[NP], int lane, i
 // tiles: where a job has at least one block to itself, q = blocks / jobs equal parts of every
 // job (a chunk then starts one job only), unless equal parts of the whole list leave the
 // busiest block less to do although it starts two; a start (the first copies, the digits)
-// counts as `start` tiles.
+// counts as `start` tiles.  It takes about as long as kStartSlices slices of a tile (16 x 256
+// weights), whatever the width.  Measured, in us, against a count fixed in tiles (6 gate_up and
+// 16 down tiles, right for 2048 and 768 inputs alone), m tokens, k of E experts of f x h: h = f
+// = 6144, 16, 2 of 32 438.0 | 435.7; 4096 x 4096, 16, 2 of 64 248.2 | 246.7; f = 1536, h = 4096, 40, 2 of 64
+// 185.5 | 183.8; f = 6144, h = 256, 30, 2 of 64 62.0 | 62.2; 256 x 256, 60, 8 of 160 50.1 | 50.0.
+constexpr int kStartSlices = 48;
 struct Cut {
     int q, per, all, blocks;
     __device__ __forceinline__ Cut(int jobs, int per_, int blocks_, int start)
@@ -566,8 +571,8 @@ __global__ __launch_bounds__(kTileThreads) void moe_layer_kernel(LayerArgs A) {
     __syncthreads();
     const int jobs = __builtin_amdgcn_readfirstlane(L.n_jobs);
     const int up_tiles = A.f / 8, down_tiles = A.h / 16;
-    // a start takes about as long as 6 gate_up tiles and 16 down tiles of 2048 and 768 inputs
-    const Cut cut_up(jobs, up_tiles, blocks, 6), cut_down(jobs, down_tiles, blocks, 16);
+    const Cut cut_up(jobs, up_tiles, blocks, kStartSlices / (A.h >> 8)),
+        cut_down(jobs, down_tiles, blocks, kStartSlices / (A.f >> 8));
     const uint32_t rb_h = (uint32_t)(A.h >> 5) * 34u, rb_f = (uint32_t)(A.f >> 5) * 34u;
     // the tiles [t, end) as far as they belong to one job
     struct Piece {
