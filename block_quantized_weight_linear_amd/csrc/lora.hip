@@ -804,7 +804,7 @@ hipError_t launch_linear_lora(const DeviceInfo& dev, const uint8_t* w, int64_t n
     const q8v::LoraWorkspace L =
         q8v::lora_workspace_layout(m, lora.n_sections, lora.rank, q8v::lora_base_bytes(m, n, k));
     char* ws = static_cast<char*>(workspace);
-    if (m == 1 && k <= q8v::kLoraTilesMaxK) {
+    if (q8v::lora_uses_one_row(m, k)) {
         // the inner products, then the one-row kernel with the correction behind its sums
         const LoraArgs lo = lora_args(lora);
         float* u = reinterpret_cast<float*>(ws + L.u_off);

@@ -296,6 +296,7 @@ constexpr int64_t kLoraMaxRanges = 6;             // at most two more than the f
 inline bool lora_uses_tiles(int64_t m, int64_t n, int64_t k) {
     return m > 1 && m < kPrefillRows && k <= kLoraTilesMaxK && n * row_bytes(k) < (int64_t(1) << 31);
 }
+inline bool lora_uses_one_row(int64_t m, int64_t k) { return m == 1 && k <= kLoraTilesMaxK; }
 // Row groups of four, as many as any form has.
 inline int64_t lora_row_groups(int64_t m) { return (m + 3) / 4; }
 
@@ -318,8 +319,10 @@ inline LoraTilesWorkspace lora_tiles_workspace_layout(int64_t m, int64_t n, int6
     return w;
 }
 
-// Workspace behind the adapters': that, or the shared product.
+// Workspace behind the adapters': that, or the shared product (one size for both packed
+// calls; only the fused one keeps its product there).
 inline size_t lora_base_bytes(int64_t m, int64_t n, int64_t k) {
+    if (lora_uses_one_row(m, k)) return 0;
     if (lora_uses_tiles(m, n, k)) return lora_tiles_workspace_layout(m, n, k).total;
     return sizeof(float) * size_t(m) * size_t(n);
 }
