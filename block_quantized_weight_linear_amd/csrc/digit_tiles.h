@@ -15,8 +15,9 @@
 //     acc = fma(d, t, acc)                      (d: the block's scale)
 // so a weight costs a lane 6 VALU operations per 512 weights and 4 activation rows instead
 // of a conversion and 4 fmas each.  Per output: the chain over the blocks of a 256-wide
-// slice, over the wave's slices, then the waves' sums in order: it depends on k alone,
-// never on the other rows of the call.
+// slice, over the wave's slices, then the waves' sums in order: it depends on k (and, for the
+// packed calls' k > 4096, on the ranges that k is cut into, which the matrix's rows and the
+// device choose), never on the other rows of the call.
 //
 // Streaming.  A tile is 16 weight rows; its 256-wide slices (16 x 272 bytes) are copied by
 // the wave that owns the slice straight into the wave's own LDS ring (coalesced

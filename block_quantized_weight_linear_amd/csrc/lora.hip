@@ -2,15 +2,18 @@
 //
 // Row t with adapter a adds scale[a] * B[a] (A[a] x[t]) to the shared product.  Two launches:
 // the inner products u[t][c] = scale[a] * A[a][c] . x[t] of every row (c over the
-// sections' ranks; float32, one wave a product), then each output's dot of u with its row
-// of B, added to the shared product (or, for a fused gate_up, the activation behind it).
+// sections' ranks; float32, a block of four waves four products), then each output's dot of u
+// with its row of B, added to the shared product (or, for a fused gate_up, the activation behind it).
 // In the packed calls the second launch computes the shared product too: one row on the
 // one-row kernel of gemv_q8.hip, more on the digit tiles (digit_tiles.h), whose digits the
 // first launch writes.  Bound by the weights' bytes and, in small matrices, by the two
-// launches' starts: 6144 x 4096 (27 MB) takes 11.3 us at 1 row, 15 at 2 (4 of them the first
-// launch) and 21 at 16, the fused 24576 x 4096 (107 MB) 23.4, 28 (3.8 TB/s) and 37 us; from 16
-// rows on by the tiles' arithmetic (digits, scales and sums: 37, 63 and 116 us at 64, 128 and 255
-// rows of 6144 x 4096).  With many rows the correction has a form of its own.
+// launches' starts: 6144 x 4096 (27 MB, rank 16, weights from memory) takes 12.8 us at 1 row (4
+// to 5 of them the first launch) and 22.3 at 16, the fused 24576 x 4096 (107 MB) 33.9 at 8 and
+// 41.3 at 16.  More rows (38, 63 and 116 us at 64, 128 and 255 rows of 6144 x 4096; 105, 195 and
+// 379 fused) add passes over the tiles: of the tile launch's cycles the lanes issue 26 % and the
+// matrix cores work 9 % at 16 rows, 48 % and 21 % at 255 (counters); the rest is the chain of
+// copies, LDS reads, products and sums that two waves a SIMD leave open.  With many rows the
+// correction has a form of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
         multiply_tiles<SP, NG>(run, a, part, sums);
         __syncthreads();
         // the next run's digits and first weights come while this one's outputs are finished
-        // (24576 x 4096 fused, 64 rows: 134 us without, 128 with)
+        // (24576 x 4096 fused, 64 rows, one group of rows at a time: 134 us without, 128 with)
         c0 += nt;
         if (c0 >= tiles) {
             c0 = 0;
@@ -279,9 +282,13 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 // For many rows (q8v::lora_uses_matrix_cores) the correction runs on the bf16 matrix cores at
 // float32 accuracy.  A float32 value is the exact sum of three bf16 values (its leading 8 bits, the
 // next 8, the last 8, each cut off, not rounded); a bf16 element of A or B is itself, a
-// binary16 one the sum of two.  A product takes the partial products down to 2^-16 of its
-// leading one (those left out are below 2^-23 of the product): 3, 5 or 6 instructions for
-// bf16, binary16 and float32 elements, with float32 accumulation.
+// binary16 one the sum of two.  A product takes the partial products of parts i + j <= 2: 3, 5
+// or 6 instructions for bf16, binary16 and float32 elements, with float32 accumulation.  The
+// products with a bf16 element are exact.  For the others the pairs of parts 1 and 2 are left
+// out, each below 2^-22 of the product (a part 1 is below 2^-7 of its value, a part 2 below
+// 2^-15) and of its sign: a product falls short by up to 2^-22 of itself for binary16 elements,
+// 2^-21 for float32 ones, 2^-24.5 on average, the size of a float32 rounding.  The pairs left out
+// would be up to a third more instructions.
 //
 //   1. plan:   the rows sorted by adapter (those without one last), in tiles of 64 rows.
 //   2. inner:  block (tile half of 32 rows, part of k): u of all sections' ranks; its four
@@ -291,8 +298,8 @@ __global__ __launch_bounds__(kTileThreads) void lora_tiles_kernel(const uint8_t*
 //   4. outer:  block (tile, 128 outputs), 64 rows x 32 outputs a wave: u and B start out,
 //              then the product's values, and no barrier lies between.
 // Bound by the memory: x once, the product in and out.  6144 x 4096, three sections of rank
-// 32 and 2048 rows: 59 us (plan 4.6, inner 19, sum 5.8, outer 30: 100 MB of product in and out
-// at 3.4 TB/s).  Measured and not kept: u staged through LDS in the outer launch (37 us), the
+// 32 and 2048 rows: 59.8 us (plan 4.7, inner 19.2, sum 6.3, outer 29.6: 100 MB of product in
+// and out at 3.4 TB/s).  Measured and not kept: u staged through LDS in the outer launch (37 us), the
 // parts added by the last block of the inner one (33 us against 19 + 6), its next step's
 // loads ahead (25 us).
 

@@ -290,6 +290,13 @@ inline LoraWorkspace lora_workspace_layout(int64_t m, int32_t n_sections, int32_
 // in us, at 1 | 2 | 16 | 255 rows, rank 16: 6144 x 4096 on tiles 15.0 | 15.1 | 21 | 116, otherwise
 // 11.3 | 15.6 | 27.5 | 346; fused 24576 x 4096 28.0 | 28.3 | 37 | 377 and 23.4 | 31.7 | 59.9 |
 // 850; 4096 x 12288 24.3 | 24.2 | 33 | 262 and 16.6 | 26.3 | 48.5 | 633.
+// Neither m within its range nor the adapters decide, so that a row has the same bits whatever
+// rows share the call.  That costs where ranks are high and rows many, as every row reads its
+// adapter anew.  Measured, in us, at 16, 64, 128 and 255 rows, 16 adapters in use, the call | the
+// tiles without adapters and lora_add behind them: 6144 x 4096, three sections, rank 16 in bf16
+// 22.1 | 28.0, 39.4 | 45.2, 64.0 | 71.3, 117 | 123; rank 64 in bf16 30.0 | 35.2, 58.5 | 61.2, 97.1 |
+// 98.3, 180 | 147; rank 256 in float32 86 | 94, 221 | 187, 409 | 215, 782 | 279; 8192 x 12288, rank 64
+// in bf16 64.6 | 63.7, 187 | 167, 362 | 276, 712 | 501.
 constexpr int64_t kLoraTilesMaxK = 16384;
 constexpr int64_t kLoraTilesMaxRange = 16 * 256;  // of k without a cut
 constexpr int64_t kLoraMaxRanges = 6;             // at most two more than the fewest, 4
@@ -367,9 +374,9 @@ inline q8_status check_lora_add(const float* y, int64_t n_in, int64_t ldy, const
 // switch of the grouped call, up to kMoeLayerMaxTokens tokens (every block selects all tokens'
 // experts and holds their lists), at most 64 experts a token (a lane each) and widths of at
 // most 24 slices of 256 (three a wave); else the routing and the grouped mixture follow each
-// other.  Measured, in us, two launches | the calls one after the other: 8 of 128 experts
-// of 768 x 2048 at 1 token 29.1 | 41.4, 16 87.5 | 124, 64 152 | 288, 127 239 | 488; 2 of 64 at 128
-// tokens 96 | 163; 2 of 8 experts of 2048 x 2048 at 31 tokens 64 | 146.
+// other.  Measured, in us, two launches | the calls one after the other (routing in its two-pass
+// form): 8 of 128 experts of 768 x 2048 at 1 token 31.2 | 42.4, 16 95.6 | 129, 64 156 | 271, 127 236 |
+// 452; 2 of 64 at 128 tokens 102 | 163; 2 of 8 experts of 2048 x 2048 at 31 tokens 65.3 | 132.
 constexpr int64_t kMoeLayerMaxTokens = 128;
 constexpr int64_t kMoeLayerMaxWidth = 24 * 256;
 inline bool moe_layer_uses_tiles(int64_t m, int32_t k, int64_t n_exp, int64_t f, int64_t h) {

@@ -52,6 +52,8 @@
 extern "C" {
 #endif
 
+/* Raised where an existing call changes; calls that are only added leave it (a library
+ * without one lacks its symbol). */
 #define Q8_ABI_VERSION 8
 
 typedef enum q8_status {
@@ -367,17 +369,21 @@ size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_
  * The packed linears with adapters:
  *   q8_linear_lora                    : y = x . W^T + D,  W = Q8_0 [n][k]
  *   q8_linear_fused_gate_up_silu_lora : h = SiLU(g) * u with [g u] = x . W^T + D, W = Q8_0 [2f][k]
- * Arguments and errors as for q8_linear / q8_linear_fused_gate_up_silu;
+ * Arguments and errors as for q8_linear / q8_linear_fused_gate_up_silu, and m at most 2^22,
+ * f at most 2^29 (Q8_ERR_SHAPE otherwise);
  *   workspace : device memory of at least q8_linear_lora_workspace_bytes(...) bytes,
  *               256-byte aligned; its contents on entry do not matter.  Calls that can
  *               overlap (other streams, or captured graphs replayed side by side) need
  *               workspaces of their own.
  * A row of x that holds a NaN or an infinity gives outputs that are not finite; other rows
  * are not touched by it.  Below 256 rows the arithmetic is of float32 accuracy: products
- * accumulate in float32, and from two rows on (k <= 16384, W below 2 GiB) an element of x is taken to within
- * 2^-30 of its row's largest magnitude, and a row's outputs have the same bits whatever other
- * rows share the call.  From 256 rows on the shared product takes the bf16 matrix-core
- * tiles of q8_linear, the correction stays in float32.
+ * accumulate in float32, and from two rows on (k <= 16384, W below 2 GiB) an element of x is
+ * taken to within 2^-30 of its row's largest magnitude (an element below 2^-6 of it so keeps fewer
+ * than float32's 24 bits), and a row's outputs have the same bits whatever other rows share the
+ * call (their order of summation goes by k, above 4096 also by n and the device).  Beyond that k
+ * or size the correction is lora_add's.  From 256 rows on the shared product takes the bf16
+ * matrix-core tiles of q8_linear, the correction is lora_add's.  From about 128 rows of rank 64
+ * on, the call without adapters followed by lora_add is faster than the call with them.
  */
 q8_status q8_linear_lora(const void* w_q8, int64_t n, int64_t k, const float* x, int64_t m, int64_t ldx,
                          const q8_lora* lora, float* y, int64_t ldy, void* workspace, size_t workspace_bytes,
@@ -397,8 +403,11 @@ size_t lora_workspace_bytes(int64_t m, const q8_lora* lora);
  *   x  : float32 [m][ldx], the projection's input (rules as for q8_linear)
  *   out may be y itself (same pointer and leading dimension); otherwise the outputs must
  *   not overlap the inputs.
- *   workspace : at least lora_workspace_bytes(m, lora) bytes, rules as above.
- * Float32 accuracy at any m.
+ *   workspace : at least lora_workspace_bytes(m, lora) bytes, rules as above; m at most 2^22.
+ * Float32 accuracy at any m.  Calls whose rows read much of their adapters (48 rows and more,
+ * 160 MB together) run on the bf16 matrix cores with every float32 value as three bf16 parts.
+ * There nothing of a product is left out for bf16 elements of A and B; for others up to 2^-22
+ * (binary16) or 2^-21 (float32) of it, on average the size of a float32 rounding.
  */
 q8_status lora_add(const float* y, int64_t n, int64_t ldy, const float* x, int64_t m, int64_t k, int64_t ldx,
                    const q8_lora* lora, float* out, int64_t ldo, void* workspace, size_t workspace_bytes,
@@ -412,7 +421,7 @@ size_t q8_moe_layer_workspace_bytes(int64_t m, int32_t k, int64_t n_exp, int64_t
 
 /*
  * The whole mixture-of-experts layer: softmax top-k routing of x (as moe_route_topk_top_p:
- * the same experts, order and weights) followed by the expert mixture (as
+ * the same experts, order and weights, bit for bit) followed by the expert mixture (as
  * q8_moe_grouped_linear) of the chosen experts.
  *   w_router, k, normalize, top_p : as for moe_route_topk_top_p (top_p = 1: plain top-k)
  *   w_gate_up_exps, w_down_exps, n_exp, f, h, x, m, ldx, y, ldy : as for q8_moe_grouped_linear
@@ -424,8 +433,9 @@ size_t q8_moe_layer_workspace_bytes(int64_t m, int32_t k, int64_t n_exp, int64_t
  * expert on average (m * k < 8 * n_exp) the results are of float32 accuracy; from there on
  * the expert products run on the bf16 tiles of q8_moe_grouped_linear.  Up to 128 tokens, 64
  * experts a token and f, h <= 6144 the former is two launches, which take an element of x (and
- * of an expert's hidden row) to within 2^-30 of its row's largest magnitude; a token's
- * outputs then have the same bits whatever other tokens share the call.
+ * of an expert's hidden row) to within 2^-30 of its row's largest magnitude (below 2^-6 of it
+ * that is fewer than float32's 24 bits); a token's outputs then have the same bits whatever
+ * other tokens share the call.
  */
 q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const void* w_down_exps, int64_t n_exp,
                        int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, int32_t normalize,
