@@ -446,7 +446,8 @@ def _workspace(workspace, need, device):
 
 
 def q8_linear_lora_workspace_bytes(m: int, n: int, k: int, rank: int, n_sections: int = 1) -> int:
-    """Workspace bytes of q8_linear_lora (q8_linear_fused_gate_up_silu_lora: n = 2f)."""
+    """Workspace bytes of q8_linear_lora (q8_linear_fused_gate_up_silu_lora: n = 2f); from
+    256 rows on q8_linear_lora takes lora_workspace_bytes as well."""
     return int(lib.q8_linear_lora_workspace_bytes(m, n, k, _Lora(rank=rank, n_sections=n_sections)))
 
 
@@ -464,7 +465,10 @@ def _linear_lora(fn, w, n_w, n_out, k, x, a, b, adapter, scale, ranks, sections,
     if out is None:
         out = torch.empty((m, n_out), dtype=torch.float32, device=dev)
     _rows_out(out, m, n_out, "out", torch.float32, dev)
-    workspace = _workspace(workspace, lib.q8_linear_lora_workspace_bytes(m, n_w, k, lo), dev)
+    # from 256 rows on the plain call's product goes straight into out
+    need = (lib.lora_workspace_bytes(m, lo) if n_out == n_w and m >= 256
+            else lib.q8_linear_lora_workspace_bytes(m, n_w, k, lo))
+    workspace = _workspace(workspace, need, dev)
     _call(dev, fn, w.data_ptr(), n_out, k, x.data_ptr(), m, _ld(x, k), lo, out.data_ptr(), _ld(out, n_out),
           workspace.data_ptr(), workspace.numel(), _stream(x))
     return out

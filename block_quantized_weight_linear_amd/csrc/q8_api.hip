@@ -432,7 +432,7 @@ size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_
     if (!lora || m < 0 || n < 0 || n > q8v::kMaxDim || q8v::check_k("k", k, nullptr, 0) != Q8_OK ||
         q8v::check_lora_rows(m, nullptr, 0) != Q8_OK || !q8v::lora_sizes_valid(*lora))
         return 0;
-    return q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n, k)).total;
+    return q8v::lora_linear_bytes(m, n, k, true, lora->n_sections, lora->rank);
 }
 
 static q8_status linear_lora_common(const char* name, const void* w, int64_t n_out, int64_t k, bool silu,
@@ -446,9 +446,8 @@ static q8_status linear_lora_common(const char* name, const void* w, int64_t n_o
     if (s == Q8_OK) s = q8v::check_lora_rows(m, msg, sizeof msg);
     if (s == Q8_OK) s = q8v::check_lora(lora, n, m, msg, sizeof msg);
     if (s == Q8_OK && m > 0 && n_out > 0)
-        s = q8v::check_workspace(
-            q8v::lora_workspace_layout(m, lora->n_sections, lora->rank, q8v::lora_base_bytes(m, n, k)).total, workspace,
-            workspace_bytes, msg, sizeof msg);
+        s = q8v::check_workspace(q8v::lora_linear_bytes(m, n, k, silu, lora->n_sections, lora->rank), workspace,
+                                 workspace_bytes, msg, sizeof msg);
     if (s != Q8_OK) {
         set_err("%s: %s", name, msg);
         return s;

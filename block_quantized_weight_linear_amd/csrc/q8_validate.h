@@ -326,12 +326,18 @@ inline LoraTilesWorkspace lora_tiles_workspace_layout(int64_t m, int64_t n, int6
     return w;
 }
 
-// Workspace behind the adapters': that, or the shared product (one size for both packed
-// calls; only the fused one keeps its product there).
+// Workspace behind the adapters': that, or the fused call's shared product; the plain call,
+// whose product goes straight into y, needs nothing there (lora_linear_bytes).
 inline size_t lora_base_bytes(int64_t m, int64_t n, int64_t k) {
     if (lora_uses_one_row(m, k)) return 0;
     if (lora_uses_tiles(m, n, k)) return lora_tiles_workspace_layout(m, n, k).total;
     return sizeof(float) * size_t(m) * size_t(n);
+}
+
+// The whole workspace that a packed call needs.
+inline size_t lora_linear_bytes(int64_t m, int64_t n, int64_t k, bool fused, int32_t n_sections, int32_t rank) {
+    const size_t base = fused || lora_uses_tiles(m, n, k) ? lora_base_bytes(m, n, k) : 0;
+    return lora_workspace_layout(m, n_sections, rank, base).total;
 }
 
 inline q8_status check_workspace(size_t need, const void* ws, size_t ws_bytes, char* msg, size_t cap) {

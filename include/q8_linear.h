@@ -362,7 +362,8 @@ typedef struct q8_lora {
 } q8_lora;
 
 /* Workspace bytes of the two packed calls below for m rows and a matrix of n rows (the
- * gate_up call: n = 2f); 0 on invalid sizes.  Of lora, only rank and n_sections count. */
+ * gate_up call: n = 2f); 0 on invalid sizes.  Of lora, only rank and n_sections count.  From
+ * 256 rows on q8_linear_lora (not the gate_up call) takes lora_workspace_bytes(m, lora) as well. */
 size_t q8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, const q8_lora* lora);
 
 /*

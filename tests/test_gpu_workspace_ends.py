@@ -47,6 +47,15 @@ def test_packed_calls(q8, m, n, k, rank, sections):
            f"gate_up m={m}")
 
 
+@pytest.mark.parametrize("m,n,k", [(256, 96, 512), (300, 64, 1280), (2, 34, 16640)])
+def test_plain_call_without_room_for_a_product(q8, m, n, k):
+    lib, torch, dev = q8
+    c = Case(q8, 7050 + m, m, n, k, 3, 16, "float16", None)
+    w = to_dev(wl.q8_weight(7051, n, k)[0], dev)
+    fenced(q8, lib.lora_workspace_bytes(m, 16), lambda ws: lib.q8_linear_lora(w, n, k, c.xd, *c.args, **c.more, workspace=ws),
+           f"linear m={m}")
+
+
 @pytest.mark.parametrize("m,n,k,count,rank", [(1, 70, 256, 2, 8), (47, 66, 512, 3, 16), (300, 64, 512, 4, 256),
                                               (48, 130, 8192, 2, 256), (1300, 58, 256, 256, 256), (700, 514, 512, 40, 64)])
 def test_beside(q8, m, n, k, count, rank):
