@@ -10,6 +10,14 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     Q8Error,
     abi_version,
+    f8_linear,
+    f8_linear_backward,
+    f8_linear_backward_workspace_bytes,
+    f8_linear_fused_gate_up_silu,
+    f8_linear_fused_gate_up_silu_backward,
+    f8_linear_fused_gate_up_silu_backward_workspace_bytes,
+    f8_quantize_act,
+    f8_quantize_weight,
     lib,
     lora_add,
     lora_gate_up_silu,

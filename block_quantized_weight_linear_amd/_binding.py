@@ -98,6 +98,23 @@ lib.q8_moe_layer.restype = ctypes.c_int
 lib.q8_moe_layer.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i32, _i32, ctypes.c_float, _vp, _i64,
                              _vp, _sz, _vp]
 
+for _name in ("f8_quantize_act", "f8_quantize_weight"):
+    getattr(lib, _name).restype = ctypes.c_int
+    getattr(lib, _name).argtypes = [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]
+lib.f8_linear.restype = ctypes.c_int
+lib.f8_linear.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp]
+lib.f8_linear_fused_gate_up_silu.restype = ctypes.c_int
+lib.f8_linear_fused_gate_up_silu.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp, _i64, _vp]
+for _name in ("f8_linear_backward_workspace_bytes", "f8_linear_fused_gate_up_silu_backward_workspace_bytes"):
+    getattr(lib, _name).restype = _sz
+    getattr(lib, _name).argtypes = [_i64, _i64, _i64, _i32]
+lib.f8_linear_backward.restype = ctypes.c_int
+lib.f8_linear_backward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _i64, _vp,
+                                   _sz, _vp]
+lib.f8_linear_fused_gate_up_silu_backward.restype = ctypes.c_int
+lib.f8_linear_fused_gate_up_silu_backward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _i64,
+                                                      _vp, _i64, _vp, _i64, _vp, _sz, _vp]
+
 # measurement aids (include/q8_probe.h)
 lib.q8_probe_shape_count.restype = _i32
 lib.q8_probe_shape_count.argtypes = []
@@ -556,6 +573,184 @@ def q8_moe_layer(w_router, w_gate_up_exps, w_down_exps, n_exp: int, f: int, h: i
           x.data_ptr(), m, _ld(x, h), k, 1 if normalize else 0, 1.0 if top_p is None else float(top_p),
           out.data_ptr(), _ld(out, h), workspace.data_ptr(), workspace.numel(), _stream(x))
     return out
+
+
+# ------------------------------------------------- block-scaled 8-bit floating point
+
+_FLOAT_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _float_type(dtype, name):
+    if dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
+    return _FLOAT_TYPES[dtype]
+
+
+def _float_rows(t, name, device=None):
+    """A 2-D float tensor with contiguous, non-overlapping rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    _float_type(t.dtype, name)
+    _dev(t, t.dtype, name, device)
+    _rows_in(t, t.shape[1], name)
+    return t
+
+
+def _f8_ld(t, width):
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _f8_codes(q, d, name, device=None):
+    """Codes [rows][k] with scales of unit stride on the same device."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"the codes of {name} must be a 2-D float8_e4m3fn (or uint8) tensor")
+    _dev(q, q.dtype, name, device)
+    if not q.is_contiguous():
+        raise ValueError(f"the codes of {name} must be contiguous")
+    _dev(d, torch.float32, f"the scales of {name}", q.device)
+    return q.shape
+
+
+def _f8_blocks(size):
+    return (size + 127) // 128
+
+
+def _f8_operands(wq, wd, xq, xd, parts):
+    """(n of a part, k, m) of a product's codes and scales."""
+    rows, k = _f8_codes(wq, wd, "w")
+    m, kx = _f8_codes(xq, xd, "x", wq.device)
+    if kx != k:
+        raise ValueError(f"w has {k} inputs, x has {kx}")
+    if rows % parts:
+        raise ValueError(f"a gate_up matrix has an even number of rows, got {rows}")
+    n = rows // parts
+    _contig_out(wd, (parts * _f8_blocks(n), _f8_blocks(k)), "the scales of w", torch.float32, wq.device)
+    _contig_out(xd, (m, _f8_blocks(k)), "the scales of x", torch.float32, wq.device)
+    return n, k, m
+
+
+def _f8_quantize(fn, x, name, block_rows, pow2, q, d):
+    _float_rows(x, name)
+    dev = x.device
+    rows, k = x.shape
+    if q is None:
+        q = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=dev)
+    shape = ((rows + block_rows - 1) // block_rows, _f8_blocks(k))
+    if d is None:
+        d = torch.empty(shape, dtype=torch.float32, device=dev)
+    _contig_out(q, (rows, k), "q", torch.uint8 if q.dtype == torch.uint8 else torch.float8_e4m3fn, dev)
+    _contig_out(d, shape, "d", torch.float32, dev)
+    size = x.element_size()
+    # a single row: only its k values are touched, so any leading dimension of whole 16 bytes does
+    ld = x.stride(0) if rows > 1 else k + (-k % (16 // size))
+    _call(dev, fn, x.data_ptr(), _FLOAT_TYPES[x.dtype], rows, k, ld, 1 if pow2 else 0, q.data_ptr(), d.data_ptr(),
+          _stream(x))
+    return q, d
+
+
+def f8_quantize_act(x, pow2: bool = False, q=None, d=None):
+    """e4m3 codes [m][k] and float32 scales [m][ceil(k/128)] of rows x [m][k] (float32,
+    float16 or bfloat16): one scale for every 128 inputs, amax/448 or (pow2) the least power
+    of two that is not below it."""
+    return _f8_quantize(lib.f8_quantize_act, x, "x", 1, pow2, q, d)
+
+
+def f8_quantize_weight(w, pow2: bool = False, q=None, d=None):
+    """e4m3 codes [n][k] and float32 scales [ceil(n/128)][ceil(k/128)] of a matrix w [n][k]: one
+    scale for every block of 128 x 128.  The parts of a fused gate_up matrix are coded apart
+    and their codes and scales put one under the other."""
+    return _f8_quantize(lib.f8_quantize_weight, w, "w", 128, pow2, q, d)
+
+
+def f8_linear(wq, wd, xq, xd, dtype=torch.float32, out=None):
+    """y = x . W^T [m][n] in `dtype` from e4m3 codes wq [n][k] and xq [m][k] and their scales
+    (f8_quantize_weight, f8_quantize_act)."""
+    n, k, m = _f8_operands(wq, wd, xq, xd, 1)
+    dev = wq.device
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=dev)
+    kind = _float_type(out.dtype, "the output")
+    _rows_out(out, m, n, "out", out.dtype, dev)
+    _call(dev, lib.f8_linear, wq.data_ptr(), wd.data_ptr(), n, k, xq.data_ptr(), xd.data_ptr(), m, out.data_ptr(), kind,
+          _f8_ld(out, n), _stream(wq))
+    return out
+
+
+def f8_linear_fused_gate_up_silu(wq, wd, xq, xd, dtype=torch.float32, keep_gate_up=False, out=None):
+    """h = SiLU(g) * u [m][f] with [g u] = x . W^T; wq [2f][k] has gate rows first, wd gate's
+    scales first.  keep_gate_up: True (or a tensor [m][2f] to write) returns (h, gu), gu the
+    products g and u beside each other, as the backward call takes them."""
+    f, k, m = _f8_operands(wq, wd, xq, xd, 2)
+    dev = wq.device
+    if out is None:
+        out = torch.empty((m, f), dtype=dtype, device=dev)
+    kind = _float_type(out.dtype, "the output")
+    _rows_out(out, m, f, "out", out.dtype, dev)
+    gu = None
+    if isinstance(keep_gate_up, torch.Tensor):
+        gu = _rows_out(keep_gate_up, m, 2 * f, "keep_gate_up", out.dtype, dev)
+    elif keep_gate_up:
+        gu = torch.empty((m, 2 * f), dtype=out.dtype, device=dev)
+    _call(dev, lib.f8_linear_fused_gate_up_silu, wq.data_ptr(), wd.data_ptr(), f, k, xq.data_ptr(), xd.data_ptr(), m,
+          out.data_ptr(), kind, _f8_ld(out, f), None if gu is None else gu.data_ptr(),
+          0 if gu is None else _f8_ld(gu, 2 * f), _stream(wq))
+    return out if gu is None else (out, gu)
+
+
+def f8_linear_backward_workspace_bytes(m: int, n: int, k: int, dtype) -> int:
+    """Workspace bytes of f8_linear_backward for gradients of `dtype`."""
+    return int(lib.f8_linear_backward_workspace_bytes(m, n, k, _float_type(dtype, "dtype")))
+
+
+def f8_linear_fused_gate_up_silu_backward_workspace_bytes(m: int, f: int, k: int, dtype) -> int:
+    """Workspace bytes of f8_linear_fused_gate_up_silu_backward for gradients of `dtype`."""
+    return int(lib.f8_linear_fused_gate_up_silu_backward_workspace_bytes(m, f, k, _float_type(dtype, "dtype")))
+
+
+def _f8_gradient(want, m, width, name, dtype, device):
+    """The tensor that a gradient goes to: new (True), the caller's, or none (False)."""
+    if isinstance(want, torch.Tensor):
+        return _rows_out(want, m, width, name, dtype, device)
+    return torch.empty((m, width), dtype=dtype, device=device) if want else None
+
+
+def _f8_backward(fn, parts, wq, wd, xq, xd, gu, d, dx, dw, workspace, need):
+    n, k, m = _f8_operands(wq, wd, xq, xd, parts)
+    dev = wq.device
+    _float_rows(d, "the gradient", dev)
+    if tuple(d.shape) != (m, n):
+        raise ValueError(f"the gradient must be [{m}][{n}], got {tuple(d.shape)}")
+    more = ()
+    if parts == 2:
+        _float_rows(gu, "gu", dev)
+        if tuple(gu.shape) != (m, 2 * n) or gu.dtype != d.dtype:
+            raise ValueError(f"gu must be [{m}][{2 * n}] of {d.dtype}, got {tuple(gu.shape)} of {gu.dtype}")
+        more = (gu.data_ptr(), _f8_ld(gu, 2 * n))
+    dx = _f8_gradient(dx, m, k, "dx", d.dtype, dev)
+    dw = _f8_gradient(dw, parts * n, k, "dw", d.dtype, dev)
+    kind = _FLOAT_TYPES[d.dtype]
+    workspace = _workspace(workspace, need(m, n, k, kind), dev)
+    _call(dev, fn, wq.data_ptr(), wd.data_ptr(), n, k, xq.data_ptr(), xd.data_ptr(), m, *more, d.data_ptr(), kind,
+          _f8_ld(d, n), None if dx is None else dx.data_ptr(), k if dx is None else _f8_ld(dx, k),
+          None if dw is None else dw.data_ptr(), k if dw is None else _f8_ld(dw, k), workspace.data_ptr(),
+          workspace.numel(), _stream(wq))
+    return dx, dw
+
+
+def f8_linear_backward(wq, wd, xq, xd, dy, dx=True, dw=True, workspace=None):
+    """The gradients of f8_linear's inputs, dx = dy . W [m][k] and dw = dy^T . x [n][k], in dy's
+    type (float32, float16 or bfloat16); W and x are the values of their codes and scales.
+    dx, dw: True, a tensor to write, or False to leave the gradient out (None is returned)."""
+    return _f8_backward(lib.f8_linear_backward, 1, wq, wd, xq, xd, None, dy, dx, dw, workspace,
+                        lib.f8_linear_backward_workspace_bytes)
+
+
+def f8_linear_fused_gate_up_silu_backward(wq, wd, xq, xd, gu, dh, dx=True, dw=True, workspace=None):
+    """The gradients of f8_linear_fused_gate_up_silu's inputs from dh [m][f] and the products
+    gu [m][2f] that it kept: dx [m][k] and dw [2f][k], in dh's type; arguments as for
+    f8_linear_backward."""
+    return _f8_backward(lib.f8_linear_fused_gate_up_silu_backward, 2, wq, wd, xq, xd, gu, dh, dx, dw, workspace,
+                        lib.f8_linear_fused_gate_up_silu_backward_workspace_bytes)
 
 
 # ------------------------------------------------------------ measurement aids

@@ -504,6 +504,112 @@ q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const 
     return Q8_OK;
 }
 
+static q8_status f8_quantize_common(const char* name, bool weight, const void* x, int32_t type, int64_t rows,
+                                    int64_t k, int64_t ldx, int32_t pow2, uint8_t* q, float* d, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    const q8_status s = q8v::check_f8_quantize(x, type, rows, weight ? q8v::kF8MaxDim : q8v::kF8MaxRows, k, ldx, q, d,
+                                               msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("%s: %s", name, msg);
+        return s;
+    }
+    if (rows == 0) return Q8_OK;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t e = weight ? q8k::launch_f8_quantize_weight(x, type, rows, k, ldx, pow2 != 0, q, d, st)
+                                : q8k::launch_f8_quantize_act(x, type, rows, k, ldx, pow2 != 0, q, d, st);
+    if (e != hipSuccess) return device_fail(name, e);
+    return Q8_OK;
+}
+
+q8_status f8_quantize_act(const void* x, int32_t type, int64_t m, int64_t k, int64_t ldx, int32_t pow2, uint8_t* q,
+                          float* d, void* stream) {
+    return f8_quantize_common("f8_quantize_act", false, x, type, m, k, ldx, pow2, q, d, stream);
+}
+
+q8_status f8_quantize_weight(const void* w, int32_t type, int64_t n, int64_t k, int64_t ldw, int32_t pow2, uint8_t* q,
+                             float* d, void* stream) {
+    return f8_quantize_common("f8_quantize_weight", true, w, type, n, k, ldw, pow2, q, d, stream);
+}
+
+static q8_status f8_linear_common(const char* name, int parts, const uint8_t* wq, const float* wd, int64_t n_out,
+                                  int64_t k, const uint8_t* xq, const float* xd, int64_t m, void* y, int32_t type,
+                                  int64_t ldy, void* gu, int64_t ldgu, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    const q8_status s = q8v::check_f8_linear(wq, wd, n_out, parts, k, xq, xd, m, y, type, ldy, gu, ldgu, msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("%s: %s", name, msg);
+        return s;
+    }
+    if (m == 0 || n_out == 0) return Q8_OK;
+    q8k::DeviceInfo dev;
+    hipError_t e = q8k::current_device_info(&dev);
+    if (e != hipSuccess) return device_fail(name, e);
+    e = q8k::launch_f8_linear(dev, wq, wd, n_out, k, parts == 2, xq, xd, m, y, type, ldy, gu, ldgu,
+                              static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return device_fail(name, e);
+    return Q8_OK;
+}
+
+q8_status f8_linear(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq, const float* xd,
+                    int64_t m, void* y, int32_t type, int64_t ldy, void* stream) {
+    return f8_linear_common("f8_linear", 1, wq, wd, n, k, xq, xd, m, y, type, ldy, nullptr, 0, stream);
+}
+
+q8_status f8_linear_fused_gate_up_silu(const uint8_t* wq, const float* wd, int64_t f, int64_t k, const uint8_t* xq,
+                                       const float* xd, int64_t m, void* h, int32_t type, int64_t ldh, void* gu,
+                                       int64_t ldgu, void* stream) {
+    return f8_linear_common("f8_linear_fused_gate_up_silu", 2, wq, wd, f, k, xq, xd, m, h, type, ldh, gu, ldgu, stream);
+}
+
+size_t f8_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t type) {
+    return q8v::f8_backward_workspace_bytes(m, n, 1, k, type);
+}
+
+size_t f8_linear_fused_gate_up_silu_backward_workspace_bytes(int64_t m, int64_t f, int64_t k, int32_t type) {
+    return q8v::f8_backward_workspace_bytes(m, f, 2, k, type);
+}
+
+static q8_status f8_backward_common(const char* name, int parts, const uint8_t* wq, const float* wd, int64_t n,
+                                    int64_t k, const uint8_t* xq, const float* xd, int64_t m, const void* gu,
+                                    int64_t ldgu, const void* d, int32_t type, int64_t ldd, void* dx, int64_t lddx,
+                                    void* dw, int64_t lddw, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    char msg[256];
+    const q8_status s = q8v::check_f8_backward(wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw,
+                                               lddw, workspace, workspace_bytes, msg, sizeof msg);
+    if (s != Q8_OK) {
+        set_err("%s: %s", name, msg);
+        return s;
+    }
+    if ((!dx && !dw) || (m == 0 && n == 0)) return Q8_OK;
+    q8k::DeviceInfo dev;
+    hipError_t e = q8k::current_device_info(&dev);
+    if (e != hipSuccess) return device_fail(name, e);
+    e = q8k::launch_f8_backward(dev, wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
+                                workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return device_fail(name, e);
+    return Q8_OK;
+}
+
+q8_status f8_linear_backward(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq,
+                             const float* xd, int64_t m, const void* dy, int32_t type, int64_t lddy, void* dx,
+                             int64_t lddx, void* dw, int64_t lddw, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    return f8_backward_common("f8_linear_backward", 1, wq, wd, n, k, xq, xd, m, nullptr, 0, dy, type, lddy, dx, lddx,
+                              dw, lddw, workspace, workspace_bytes, stream);
+}
+
+q8_status f8_linear_fused_gate_up_silu_backward(const uint8_t* wq, const float* wd, int64_t f, int64_t k,
+                                                const uint8_t* xq, const float* xd, int64_t m, const void* gu,
+                                                int64_t ldgu, const void* dh, int32_t type, int64_t lddh, void* dx,
+                                                int64_t lddx, void* dw, int64_t lddw, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+    return f8_backward_common("f8_linear_fused_gate_up_silu_backward", 2, wq, wd, f, k, xq, xd, m, gu, ldgu, dh, type,
+                              lddh, dx, lddx, dw, lddw, workspace, workspace_bytes, stream);
+}
+
 int32_t q8_probe_shape_count(void) { return q8k::probe_shape_count(); }
 
 int64_t q8_probe_sink_words(int32_t shape) {

@@ -88,6 +88,22 @@ hipError_t launch_moe_layer(const DeviceInfo& dev, const float* w_router, const 
                             int64_t n_exp, int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int k,
                             bool normalize, float top_p, float* y, int64_t ldy, void* workspace, hipStream_t stream);
 
+// Block-scaled 8-bit floating point (types: q8_float_type).
+hipError_t launch_f8_quantize_act(const void* x, int type, int64_t m, int64_t k, int64_t ldx, bool pow2, uint8_t* q,
+                                  float* d, hipStream_t stream);
+hipError_t launch_f8_quantize_weight(const void* w, int type, int64_t n, int64_t k, int64_t ldw, bool pow2,
+                                     uint8_t* q, float* d, hipStream_t stream);
+// y[m][n_out] from codes; silu: W has 2 n_out rows, y is SiLU(gate) * up, gu (or NULL) the two.
+hipError_t launch_f8_linear(const DeviceInfo& dev, const uint8_t* wq, const float* wd, int64_t n_out, int64_t k,
+                            bool silu, const uint8_t* xq, const float* xd, int64_t m, void* y, int type, int64_t ldy,
+                            void* gu, int64_t ldgu, hipStream_t stream);
+// dx and dw (either may be NULL) of a matrix of `parts` parts of n rows; parts == 2: d is the
+// gradient of SiLU(gate) * up, gu the two products.  Workspace laid out by q8v::f8_backward_layout.
+hipError_t launch_f8_backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, int64_t n, int parts,
+                              int64_t k, const uint8_t* xq, const float* xd, int64_t m, const void* gu, int64_t ldgu,
+                              const void* d, int type, int64_t ldd, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                              void* workspace, hipStream_t stream);
+
 // Measurement aids (include/q8_probe.h): a plain streaming read of `bytes` (a multiple
 // of 4096) in launch shape `shape`, one xor word per lane into sink; an empty launch.
 int probe_shape_count();

@@ -437,4 +437,136 @@ inline q8_status check_moe_layer(const float* wr, const void* wgu, const void* w
     return check_workspace(moe_layer_workspace_layout(m, k, n_exp, f, h).total, ws, ws_bytes, msg, cap);
 }
 
+// ------------------------------------------------- block-scaled 8-bit floating point
+
+constexpr int64_t kF8Block = 128;
+constexpr int64_t kF8MaxDim = int64_t(1) << 20;    // k, matrix rows: 256 rows stay within 32-bit offsets
+constexpr int64_t kF8MaxRows = int64_t(1) << 24;   // m
+constexpr int64_t kF8MaxArea = int64_t(1) << 37;   // tiles of 256 x 256: a grid fits 32 bits of threads
+
+inline int64_t f8_type_bytes(int32_t type) { return type == Q8_F32 ? 4 : 2; }
+inline bool f8_type_valid(int32_t type) { return type >= Q8_F32 && type <= Q8_BF16; }
+
+// Matrix rows n (2f of a fused matrix), inputs k and activation rows m.
+inline q8_status check_f8_sizes(int64_t n, int64_t k, int64_t m, int32_t type, char* msg, size_t cap) {
+    if (!f8_type_valid(type)) return fail(msg, cap, Q8_ERR_SHAPE, "type=%lld is none of Q8_F32, Q8_F16, Q8_BF16", type);
+    if (n < 0 || n > kF8MaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "the matrix has %lld rows, not 0 .. 2^20", n);
+    if (k <= 0 || k > kF8MaxDim || k % 16 != 0)
+        return fail(msg, cap, Q8_ERR_SHAPE, "k=%lld must be a positive multiple of 16 (at most 2^20)", k);
+    if (m < 0 || m > kF8MaxRows) return fail(msg, cap, Q8_ERR_SHAPE, "m=%lld out of range [0, 2^24]", m);
+    if (m * n > kF8MaxArea || m * k > kF8MaxArea || n * k > kF8MaxArea)
+        return fail(msg, cap, Q8_ERR_SHAPE, "a product of two sizes is above 2^37 (m=%lld, k=%lld)", m, k);
+    return Q8_OK;
+}
+inline q8_status check_f8_ld(const char* what, int64_t ld, int64_t width, char* msg, size_t cap) {
+    if (ld >= width && ld <= kMaxDim) return Q8_OK;
+    if (msg && cap)
+        snprintf(msg, cap, "%s=%lld must be at least %lld and at most 2^30", what, (long long)ld, (long long)width);
+    return Q8_ERR_SHAPE;
+}
+inline q8_status check_f8_codes(const char* what, const void* q, const void* d, char* msg, size_t cap) {
+    if (!q || !d) {
+        if (msg && cap) snprintf(msg, cap, "null pointer (codes or scales of %s)", what);
+        return Q8_ERR_NULL;
+    }
+    if (!aligned(q, 16) || !aligned(d, 4)) {
+        if (msg && cap) snprintf(msg, cap, "codes of %s not 16-byte or scales not 4-byte aligned", what);
+        return Q8_ERR_ALIGN;
+    }
+    return Q8_OK;
+}
+inline q8_status check_f8_floats(const char* what, const void* p, int32_t type, char* msg, size_t cap) {
+    if (!p) {
+        if (msg && cap) snprintf(msg, cap, "null pointer (%s)", what);
+        return Q8_ERR_NULL;
+    }
+    if (!aligned(p, uintptr_t(f8_type_bytes(type)))) {
+        if (msg && cap) snprintf(msg, cap, "%s not aligned to its elements", what);
+        return Q8_ERR_ALIGN;
+    }
+    return Q8_OK;
+}
+
+inline q8_status check_f8_quantize(const void* x, int32_t type, int64_t rows, int64_t max_rows, int64_t k, int64_t ldx,
+                                   const void* q, const void* d, char* msg, size_t cap) {
+    q8_status s;
+    if ((s = check_f8_sizes(0, k, 0, type, msg, cap)) != Q8_OK) return s;
+    if (rows < 0 || rows > max_rows) return fail(msg, cap, Q8_ERR_SHAPE, "%lld rows, out of range [0, %lld]", rows, max_rows);
+    if (rows * k > kF8MaxArea) return fail(msg, cap, Q8_ERR_SHAPE, "%lld rows of k=%lld are above 2^37", rows, k);
+    if ((s = check_f8_ld("leading dimension", ldx, k, msg, cap)) != Q8_OK) return s;
+    if (rows == 0) return Q8_OK;
+    if (!x) return fail(msg, cap, Q8_ERR_NULL, "null pointer (the float operand)");
+    if (!aligned(x, 16)) return fail(msg, cap, Q8_ERR_ALIGN, "the float operand is not 16-byte aligned");
+    if (ldx * f8_type_bytes(type) % 16 != 0)
+        return fail(msg, cap, Q8_ERR_ALIGN, "leading dimension %lld: rows are not multiples of 16 bytes", ldx);
+    return check_f8_codes("the result", q, d, msg, cap);
+}
+
+// f8_linear (parts = 1, n_out = n) and the fused call (parts = 2, n_out = f).
+inline q8_status check_f8_linear(const void* wq, const void* wd, int64_t n_out, int parts, int64_t k, const void* xq,
+                                 const void* xd, int64_t m, const void* y, int32_t type, int64_t ldy, const void* gu,
+                                 int64_t ldgu, char* msg, size_t cap) {
+    q8_status s;
+    if (n_out < 0 || n_out > kF8MaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "%lld outputs, not 0 .. 2^20", n_out);
+    if ((s = check_f8_sizes(parts * n_out, k, m, type, msg, cap)) != Q8_OK) return s;
+    if ((s = check_f8_ld("leading dimension of the output", ldy, n_out, msg, cap)) != Q8_OK) return s;
+    if (gu && (s = check_f8_ld("ldgu", ldgu, 2 * n_out, msg, cap)) != Q8_OK) return s;
+    if (m == 0 || n_out == 0) return Q8_OK;
+    if ((s = check_f8_codes("W", wq, wd, msg, cap)) != Q8_OK) return s;
+    if ((s = check_f8_codes("x", xq, xd, msg, cap)) != Q8_OK) return s;
+    if ((s = check_f8_floats("the output", y, type, msg, cap)) != Q8_OK) return s;
+    if (gu && (s = check_f8_floats("gu", gu, type, msg, cap)) != Q8_OK) return s;
+    return Q8_OK;
+}
+
+// bf16 parts that a value of a gradient's type is taken as, and the pairs of parts whose
+// products the weights' gradient adds.
+inline int f8_terms(int32_t type) { return type == Q8_F32 ? 3 : type == Q8_F16 ? 2 : 1; }
+
+// Workspace of the backward calls: the gradients of the products as planes of bf16 parts
+// [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, and the inputs as planes
+// [terms][m][k].
+struct F8BackwardWorkspace {
+    int64_t ldd;
+    size_t d_off, x_off, total;
+};
+inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
+    F8BackwardWorkspace w{};
+    w.ldd = parts * int64_t(round_up(size_t(n_part), 8));
+    const size_t terms = size_t(f8_terms(type));
+    size_t off = 0;
+    w.d_off = off; off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
+    w.x_off = off; off = round_up(off + 2 * terms * size_t(m) * size_t(k), 256);
+    w.total = off ? off : 256;
+    return w;
+}
+inline size_t f8_backward_workspace_bytes(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
+    if (n_part < 0 || n_part > kF8MaxDim) return 0;
+    if (check_f8_sizes(parts * n_part, k, m, type, nullptr, 0) != Q8_OK) return 0;
+    return f8_backward_layout(m, n_part, parts, k, type).total;
+}
+
+// f8_linear_backward (parts = 1, gu = NULL) and the fused call (parts = 2, d = dh).
+inline q8_status check_f8_backward(const void* wq, const void* wd, int64_t n_part, int parts, int64_t k,
+                                   const void* xq, const void* xd, int64_t m, const void* gu, int64_t ldgu,
+                                   const void* d, int32_t type, int64_t ldd, const void* dx, int64_t lddx,
+                                   const void* dw, int64_t lddw, const void* ws, size_t ws_bytes, char* msg,
+                                   size_t cap) {
+    q8_status s;
+    if (n_part < 0 || n_part > kF8MaxDim) return fail(msg, cap, Q8_ERR_SHAPE, "%lld outputs, not 0 .. 2^20", n_part);
+    if ((s = check_f8_sizes(parts * n_part, k, m, type, msg, cap)) != Q8_OK) return s;
+    if ((s = check_f8_ld("leading dimension of the gradient", ldd, n_part, msg, cap)) != Q8_OK) return s;
+    if (parts == 2 && (s = check_f8_ld("ldgu", ldgu, 2 * n_part, msg, cap)) != Q8_OK) return s;
+    if (dx && (s = check_f8_ld("lddx", lddx, k, msg, cap)) != Q8_OK) return s;
+    if (dw && (s = check_f8_ld("lddw", lddw, k, msg, cap)) != Q8_OK) return s;
+    if (dx && (s = check_f8_floats("dx", dx, type, msg, cap)) != Q8_OK) return s;
+    if (dw && (s = check_f8_floats("dw", dw, type, msg, cap)) != Q8_OK) return s;
+    if (m == 0 || n_part == 0 || (!dx && !dw)) return Q8_OK;
+    if (dx && (s = check_f8_codes("W", wq, wd, msg, cap)) != Q8_OK) return s;
+    if (dw && (s = check_f8_codes("x", xq, xd, msg, cap)) != Q8_OK) return s;
+    if ((s = check_f8_floats("the gradient", d, type, msg, cap)) != Q8_OK) return s;
+    if (parts == 2 && (s = check_f8_floats("gu", gu, type, msg, cap)) != Q8_OK) return s;
+    return check_workspace(f8_backward_layout(m, n_part, parts, k, type).total, ws, ws_bytes, msg, cap);
+}
+
 }  // namespace q8v

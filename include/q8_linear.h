@@ -442,6 +442,112 @@ q8_status q8_moe_layer(const float* w_router, const void* w_gate_up_exps, const 
                        int64_t f, int64_t h, const float* x, int64_t m, int64_t ldx, int32_t k, int32_t normalize,
                        float top_p, float* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Block-scaled 8-bit floating point.  The DGX Spark README (Performance) serves checkpoints
+ * whose weights are FP8 blocks; the pages name the format without spelling it out.  Here:
+ *   codes  : OCP e4m3 (1 sign, 4 exponent, 3 fraction bits, bias 7, largest 448, no infinity,
+ *            0x7F and 0xFF are NaN), row-major and contiguous, k a positive multiple of 16
+ *   scales : float32, contiguous; value = code * scale.  Of a weight matrix [n][k] one scale for
+ *            every block of 128 rows x 128 inputs, [ceil(n/128)][ceil(k/128)]; of activations
+ *            [m][k] one for every 128 inputs of a row, [m][ceil(k/128)].  The last blocks of
+ *            either direction may be cut short.  A fused gate_up matrix [2f][k] is two matrices
+ *            of f rows with blocks of their own: its scales are [2 * ceil(f/128)][ceil(k/128)],
+ *            gate's first.
+ *   type   : of the float operand or result of a call, q8_float_type
+ * Sizes: k and the rows of a matrix (n, or 2f) at most 2^20, m at most 2^24, each of m * n, m * k and
+ * n * k (n = 2f) at most 2^37; leading dimensions at most 2^30; otherwise Q8_ERR_SHAPE.  Codes 16-byte aligned, scales
+ * 4-byte, float operands to their element where nothing else is said; otherwise Q8_ERR_ALIGN.
+ * m = 0 and n = 0 (f = 0) enqueue nothing, but that a backward call writes the zeros that an empty
+ * sum gives (dw for m = 0, dx for n = 0).  Outputs overlap no input of their call.
+ * NaN codes and scales that are not finite give outputs that are not finite where they take
+ * part (a row of x: its row; a block of W: its outputs), and nowhere else.
+ */
+typedef enum q8_float_type { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2 } q8_float_type;
+
+/*
+ * Codes and scales of float rows (blocks of 1 x 128) or of a matrix (blocks of 128 x 128).
+ * Of a block's largest magnitude a:
+ *   pow2 = 0 : scale = a / 448, code = e4m3(clamp(x * (448 / a), -448, 448))
+ *   pow2 = 1 : scale = the least power of two that is at least a / 448, code = e4m3(x / scale)
+ * Quotients and products are rounded to float32 once each, codes to nearest even: the result is
+ * bit-exact.  a < 2^-116: codes and scale 0.  A block that holds a NaN or an infinity: codes and
+ * scale NaN.
+ *   x : [m][ldx] (w: [n][ldw]) of element type `type`, 16-byte aligned with rows of a multiple of
+ *       16 bytes (Q8_ERR_ALIGN otherwise)
+ *   q : codes out [m][k]     d : scales out (above)
+ */
+q8_status f8_quantize_act(const void* x, int32_t type, int64_t m, int64_t k, int64_t ldx, int32_t pow2, uint8_t* q,
+                          float* d, void* stream);
+q8_status f8_quantize_weight(const void* w, int32_t type, int64_t n, int64_t k, int64_t ldw, int32_t pow2, uint8_t* q,
+                             float* d, void* stream);
+
+/*
+ * y[t][j] = sum over blocks b of xd[t][b] * wd[j/128][b] * sum_{i in b} xq[t][i] * wq[j][i]
+ *   wq, wd : codes [n][k], scales      xq, xd : codes [m][k], scales
+ *   y      : [m][ldy] out, element type `type`, ldy >= n
+ * acc += (xd * wd) * sum in float32 over the blocks, one rounding to `type` at the end.  With 16-bit
+ * results a block's sum runs on the 8-bit matrix cores, which cut a product off at 2^-13 of the largest
+ * of the eight that they add at once (sums of random codes are off by 2^-16 of their size, whatever k);
+ * with float32 results on the bf16 ones, which are of float32 accuracy.  For one m the order of every sum
+ * is fixed by the sizes; it is not the same for every m.
+ */
+q8_status f8_linear(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq, const float* xd,
+                    int64_t m, void* y, int32_t type, int64_t ldy, void* stream);
+
+/*
+ * h = SiLU(g) * u with [g u] = x . W^T, W = [2f][k] with gate rows first (scales: above), in one
+ * launch; SiLU(g) = g / (1 + exp(-g)).
+ *   h  : [m][ldh] out, element type `type`, ldh >= f
+ *   gu : NULL, or [m][ldgu] out of the same type, ldgu >= 2f: the gate products in columns 0 ..
+ *        f - 1, the up products in f .. 2f - 1, as the backward call takes them
+ */
+q8_status f8_linear_fused_gate_up_silu(const uint8_t* wq, const float* wd, int64_t f, int64_t k, const uint8_t* xq,
+                                       const float* xd, int64_t m, void* h, int32_t type, int64_t ldh, void* gu,
+                                       int64_t ldgu, void* stream);
+
+/* Workspace bytes of the two backward calls for these sizes (n: rows of the matrix, the fused
+ * call's 2f; 0 on invalid sizes). */
+size_t f8_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t type);
+size_t f8_linear_fused_gate_up_silu_backward_workspace_bytes(int64_t m, int64_t f, int64_t k, int32_t type);
+
+/*
+ * The gradients of f8_linear's inputs, the quantizers passed straight through:
+ *   dx[t][i] = sum_j dy[t][j] * W[j][i]         dw[j][i] = sum_t dy[t][j] * x[t][i]
+ * with W and x the values that the codes and scales stand for.
+ *   dy : [m][lddy] of element type `type`, lddy >= n
+ *   dx : NULL, or [m][lddx] out of that type, lddx >= k
+ *   dw : NULL, or [n][lddw] out of that type, lddw >= k (xq, xd: NULL is allowed without it)
+ *   workspace : device memory of at least f8_linear_backward_workspace_bytes(...) bytes, 256-byte
+ *               aligned; its contents on entry do not matter.  Calls that can overlap need
+ *               workspaces of their own.
+ * Products run on the bf16 matrix cores with float32 accumulation and one rounding at the end.
+ * Codes are exact in bf16.  Gradients of bf16 are taken as they are, binary16 ones as two bf16
+ * parts and float32 ones as three, exactly; a value of x (code * scale) is rounded to as many
+ * parts for dw: to bf16 with bf16 gradients (scales that are powers of two: not at all), to
+ * within 2^-16 with binary16, exactly as a float32 with float32.  Of the products of parts those
+ * below 2^-16 (binary16) and 2^-24 (float32) of the whole are left out.
+ */
+q8_status f8_linear_backward(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq,
+                             const float* xd, int64_t m, const void* dy, int32_t type, int64_t lddy, void* dx,
+                             int64_t lddx, void* dw, int64_t lddw, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * The gradients of f8_linear_fused_gate_up_silu's inputs from dh and the gate and up products
+ * that it kept.  With s = 1 / (1 + exp(-g)):
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s,  each rounded to `type` once;
+ *   dx = [dg du] . W          dw = [dg du]^T . x
+ *   gu : [m][ldgu], ldgu >= 2f;  dh : [m][lddh], lddh >= f, both of element type `type`
+ *   dx : NULL, or [m][lddx] out, lddx >= k;  dw : NULL, or [2f][lddw] out, lddw >= k
+ * Arithmetic, workspace (f8_linear_fused_gate_up_silu_backward_workspace_bytes) and rules as for
+ * f8_linear_backward.
+ */
+q8_status f8_linear_fused_gate_up_silu_backward(const uint8_t* wq, const float* wd, int64_t f, int64_t k,
+                                                const uint8_t* xq, const float* xd, int64_t m, const void* gu,
+                                                int64_t ldgu, const void* dh, int32_t type, int64_t lddh, void* dx,
+                                                int64_t lddx, void* dw, int64_t lddw, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
