@@ -171,7 +171,7 @@ struct F8InputGradArgs {
     void* dx;
     int64_t lddx;
     int n, parts, terms, m, k, kb;
-    int m_tiles, tiles;
+    int m_tiles, k_tiles;
     bool vec;
 };
 
@@ -197,10 +197,9 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wm = wave / WK;
-    const int tile = f8_tile_of_block((int)blockIdx.x, a.tiles);
-    if (tile >= a.tiles) return;  // block-uniform, before any barrier
-    const int mt = tile % a.m_tiles, kt = tile / a.m_tiles;
-    const int m0 = mt * BM, k0 = kt * BK;
+    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.m_tiles, a.k_tiles);
+    if (!tile.inside) return;  // block-uniform, before any barrier
+    const int m0 = tile.row * BM, k0 = tile.col * BK;
 
     const int lr = lane >> 3, lc = (lane & 7) ^ lr;
     uint32_t doff[DC], woff[WC];
@@ -269,7 +268,7 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
         next();
         if (c + 1 < total) copy(npart, nterm, ns, stage ^ 1);
         const uint32_t at = (uint32_t)(stage * STAGE);
-        const float scale = a.wd[(int64_t)(part * row_blocks + s / 2) * a.kb + kblock];
+        const float scale = f8_uniform(a.wd + (int64_t)(part * row_blocks + s / 2) * a.kb + kblock);
         u32x2 raw[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -339,9 +338,9 @@ hipError_t launch_input_grad_tile(F8InputGradArgs a, hipStream_t stream) {
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
     if (e != hipSuccess) return e;
     a.m_tiles = (a.m + WM * TM * 16 - 1) / (WM * TM * 16);
-    const int64_t tiles = (int64_t)a.m_tiles * ((a.k + WK * 128 - 1) / (WK * 128));
+    a.k_tiles = (a.k + WK * 128 - 1) / (WK * 128);
+    const int64_t tiles = (int64_t)a.m_tiles * a.k_tiles;
     if (f8_grid(tiles) * (64 * WK * WM) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-    a.tiles = (int)tiles;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WM), lds, stream, a);
     return hipGetLastError();
 }
@@ -356,7 +355,7 @@ struct F8WeightGradArgs {
     void* dw;
     int64_t lddw;
     int n, parts, pairs, m, k;
-    int k_tiles, n_tiles, tiles;  // n_tiles: of a part
+    int k_tiles, n_tiles;  // n_tiles: of a part
     bool vec;
 };
 
@@ -377,10 +376,9 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wn = wave / WK;
-    const int tile = f8_tile_of_block((int)blockIdx.x, a.tiles);
-    if (tile >= a.tiles) return;  // block-uniform, before any barrier
-    const int kt = tile % a.k_tiles, nt = tile / a.k_tiles;
-    const int part = nt / a.n_tiles, n0 = (nt - part * a.n_tiles) * BN, k0 = kt * BK;
+    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.k_tiles, a.n_tiles * a.parts);
+    if (!tile.inside) return;  // block-uniform, before any barrier
+    const int part = tile.col / a.n_tiles, n0 = (tile.col - part * a.n_tiles) * BN, k0 = tile.row * BK;
     const int n_cols = (a.n + 7) / 8 * 8;  // columns of a part's planes
 
     uint32_t xoff[XC], doff[DC];
@@ -514,7 +512,6 @@ hipError_t launch_weight_grad_tile(F8WeightGradArgs a, hipStream_t stream) {
     a.n_tiles = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)a.k_tiles * a.n_tiles * a.parts;
     if (f8_grid(tiles) * (64 * WK * WN) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-    a.tiles = (int)tiles;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WN), lds, stream, a);
     return hipGetLastError();
 }

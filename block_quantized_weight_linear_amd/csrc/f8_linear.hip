@@ -1,12 +1,14 @@
 // Block-scaled 8-bit floating-point linears on the matrix cores of gfx950
 // (v_mfma_f32_16x16x128_f8f6f4): y[t][j] = sum_b xd[t][b] wd[j/128][b] sum_{i in b} xq[t][i] wq[j][i].
 //
-// Tile: BN weight rows x BM activation rows, WN x WM waves, TN x TM fragments of 16 x 16 a wave.
-// A K step is one block of 128 inputs, 128 bytes a row: weight rows are the instruction's A (so a
-// lane ends up with four neighbouring outputs of one row), activation rows its B.  One
-// instruction is a whole block of a 16 x 16 fragment; its sum starts at zero and joins the
-// accumulators as acc += (xd * wd) * sum, the factor being one number a lane (the lane's
-// activation row) since a fragment's weight rows lie in one block of 128.
+// Tile: BN weight rows x BM activation rows, WN x WM waves, TN x TM fragments of 16 x 16 a wave.  A K
+// step is one block of 128 inputs, 128 bytes a row: weight rows are the instruction's A (so a lane ends
+// up with four neighbouring outputs of one row), activation rows its B.  One instruction is a whole
+// block of a fragment; its sum starts at zero and joins the accumulators as acc += (xd * wd) * sum, the
+// factor being one number a lane (the lane's activation row) since a fragment's weight rows lie in one
+// block of 128.  (Fragments of 32 x 32, two instructions a block, read their operands half as often, and
+// measured 263 us where these take 237, 4096 rows of 8192 x 8192: their sums are four times as long on
+// the way.)
 //
 // The instruction aligns the products of eight inputs at the largest of them and cuts them off
 // 2^-13 below it before they join its float32 sum (measured with pairs of products; sums of random
@@ -15,9 +17,9 @@
 // multiplied by v_mfma_f32_16x16x32_bf16, at half the rate, whose sums of them are off by 2^-26.
 //
 // Tile rows reach LDS by direct copies of 16 bytes a lane, two stages.  Within a row the eight
-// 16-byte chunks are stored at chunk ^ (row % 8), so that the fragments' reads (16 rows, one
-// chunk of each) fall on all banks; lane group g reads chunks g and g + 4 of its row, the same
-// for both operands, which makes the order of the inputs within a block immaterial.
+// 16-byte chunks are stored at chunk ^ (row % 8), so that the fragments' reads (16 rows, one chunk of
+// each) fall on all banks; lane group g reads chunks g and g + 4 of its row, the same for both operands,
+// which makes the order of the inputs within a block immaterial.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,20 +42,22 @@ struct F8LinearArgs {
     void* gu;  // gate and up products of the fused call, or NULL
     int64_t ldy, ldgu;
     int n_out, m, k, kb;
-    int m_tiles, n_tiles, tiles;
+    int m_tiles, n_tiles;
     bool vec, vec_gu;  // rows of y (gu) are aligned to four elements
 };
 
-// The 32 codes of a row that a lane supplies, and a block's sums of a 16 x 16 fragment.
+// The 32 codes of a row that a lane supplies, and a block's sums of a fragment.
 struct F8Codes {
     f8_i32x8 v;
-    __device__ __forceinline__ explicit F8Codes(f8_i32x8 codes) : v(codes) {}
+    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi) { v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 };
 struct F8Widened {
     f8_bf16x8 v[4];
-    __device__ __forceinline__ explicit F8Widened(f8_i32x8 codes) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = f8_widen(codes[2 * i], codes[2 * i + 1]);
+    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi) {
+        v[0] = f8_widen(lo[0], lo[1]);
+        v[1] = f8_widen(lo[2], lo[3]);
+        v[2] = f8_widen(hi[0], hi[1]);
+        v[3] = f8_widen(hi[2], hi[3]);
     }
 };
 __device__ __forceinline__ f8_f32x4 f8_block_sum(const F8Codes& a, const F8Codes& b) {
@@ -66,17 +70,28 @@ __device__ __forceinline__ f8_f32x4 f8_block_sum(const F8Widened& a, const F8Wid
     return t;
 }
 
+// Words of a stage of scales: those of the tile's rows in whole copies of 64 (of each of the first four
+// waves in the form of eight, which does not ask how many its tile has), then one copy of those of
+// its weight blocks (in the form of eight one of each of the other four waves, all alike).
+template <int WN, int WM, int TM>
+constexpr int f8_scale_rows() {
+    return WN * WM == 8 ? 256 : (WM * TM * 16 + 63) / 64 * 64;
+}
+template <int WN, int WM, int TM>
+constexpr int f8_scale_words() {
+    return f8_scale_rows<WN, WM, TM>() + 64;
+}
+constexpr int kF8ScaleStages = 4;
 template <int WN, int WM, int TN, int TM>
 constexpr size_t f8_linear_lds_bytes() {
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
-    return 2 * ((size_t)(BN + BM) * 128 + (BM < 64 ? 64 : BM) * 4);
+    return 2 * (size_t)(BN + BM) * 128 + kF8ScaleStages * (size_t)f8_scale_words<WN, WM, TM>() * 4;
 }
 
 template <int WN, int WM, int TN, int TM, bool SILU, class T>
 __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a) {
     constexpr int W = WN * WM, BN = WN * TN * 16, BM = WM * TM * 16, ROWS = BN + BM;
     constexpr int COPIES = (ROWS / 8 + W - 1) / W;  // of a wave and step, eight rows each
-    constexpr int SX = BM < 64 ? 64 : BM;
     constexpr int OUT = SILU ? TN * 8 : TN * 16;  // outputs of a wave
     using Codes = std::conditional_t<sizeof(T) == 4, F8Widened, F8Codes>;
     static_assert(128 % (TN * 16) == 0 && (!SILU || TN % 2 == 0), "a wave's weight rows lie in one block");
@@ -85,116 +100,198 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % WN, wm = wave / WN;
 
-    const int tile = f8_tile_of_block((int)blockIdx.x, a.tiles);
-    if (tile >= a.tiles) return;  // block-uniform, before any barrier
-    const int mt = tile % a.m_tiles, nt = tile / a.m_tiles;
-    const int n0 = nt * (SILU ? BN / 2 : BN), m0 = mt * BM;
+    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.m_tiles, a.n_tiles);
+    if (!tile.inside) return;  // block-uniform, before any barrier
+    const int n0 = tile.col * (SILU ? BN / 2 : BN), m0 = tile.row * BM;
 
-    // Copy c of the tile: rows 8c .. 8c + 7 of the stage (weights, then activations), lane l the
-    // stage's chunk l % 8 of row l / 8.  Rows past the operand's end are its last row again.
+    // Copy j of a wave: rows r .. r + 7 of the stage (weights, then activations), r = stage_row(j); lane l
+    // the stage's chunk l % 8 of row l / 8.  Eight waves take turns (f8_turns): first the copies of the
+    // piece X, the weights and each group's first activation rows, then those of Y, the groups' others.
+    constexpr int PARTS = W == 8 ? 2 : 1, PM = TM / PARTS;
+    constexpr int YC = W == 8 ? WM * PM * 2 / W : 0, XC = COPIES - YC;
+    static_assert(W != 8 || (WM == 2 && TM % 2 == 0 && WM * 2 * PM % W == 0 && ROWS / 8 % W == 0), "pieces divide evenly");
+    auto stage_row = [&](int j) __attribute__((always_inline)) {
+        const int c = wave + W * (j < XC ? j : j - XC);
+        if (W != 8 || c * 8 < BN && j < XC) return c * 8;
+        constexpr int OF = 2 * PM;  // copies a group
+        const int q = j < XC ? c - BN / 8 : c;
+        return BN + q / OF * (TM * 16) + q % OF * 8 + (j < XC ? 0 : PM * 16);
+    };
     const uint8_t* base[COPIES];
     uint32_t off[COPIES];
     const int lr = lane >> 3, lc = (lane & 7) ^ lr;
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
-        const int c = wave + W * j;
-        if (c * 8 < BN) {
-            const int wv = c * 8 / (TN * 16), in = c * 8 % (TN * 16);  // the wave whose rows these are
-            int first;
-            bool up = false;
+        const int r = stage_row(j);
+        int first, rows;
+        bool up = false;
+        const uint8_t* from = a.w;
+        if (r < BN) {
+            const int wv = r / (TN * 16), in = r % (TN * 16);  // the wave whose rows these are
+            rows = a.n_out;
             if constexpr (SILU) {
                 up = in >= TN * 8;
                 first = n0 + wv * (TN * 8) + (up ? in - TN * 8 : in);
             } else {
                 first = n0 + wv * (TN * 16) + in;
             }
-            const int start = first < a.n_out ? first : a.n_out - 1;
-            const int row = first + lr < a.n_out ? first + lr - start : a.n_out - 1 - start;
-            base[j] = a.w + (int64_t)(start + (up ? a.n_out : 0)) * a.k;
-            off[j] = (uint32_t)row * (uint32_t)a.k + 16u * lc;
         } else {
-            const int first = m0 + c * 8 - BN;
-            const int start = first < a.m ? first : a.m - 1;
-            const int row = first + lr < a.m ? first + lr - start : a.m - 1 - start;
-            base[j] = a.x + (int64_t)start * a.k;
-            off[j] = (uint32_t)row * (uint32_t)a.k + 16u * lc;
+            from = a.x;
+            rows = a.m;
+            first = m0 + r - BN;
         }
+        // rows past the operand's end are its last row again
+        const int start = first < rows ? first : rows - 1;
+        const int row = first + lr < rows ? first + lr - start : rows - 1 - start;
+        base[j] = from + (int64_t)(start + (up ? a.n_out : 0)) * a.k;
+        off[j] = (uint32_t)row * (uint32_t)a.k + 16u * lc;
     }
     const uint32_t lds = f8_lds_address(f8_smem);
     const uint32_t lds_sx = lds + 2 * ROWS * 128;
-    // the scales of 64 rows are one copy of four bytes a lane
+    // Scales, a copy of four bytes a lane: the waves w < SX / 64 those of rows 64w .., the others (the first
+    // wave in a second copy, if there are no others) word i the scale of the weight block of wave i / 2 (gate's
+    // and up's where they are fused); past the matrix: the last block, of rows that are not stored.
+    constexpr int SX = f8_scale_rows<WN, WM, TM>(), SW = f8_scale_words<WN, WM, TM>();
+    const int last_block = (a.n_out - 1) / 128;
+    auto weight_scale = [&](int i) __attribute__((always_inline)) {
+        const int b = (n0 + (i / 2 % WN) * OUT) / 128;
+        return (uint32_t)((b < last_block ? b : last_block) + (SILU && i % 2 ? last_block + 1 : 0));
+    };
     const int sx_row = m0 + 64 * wave + lane;
-    const float* sx_base = a.xd + (int64_t)m0 * a.kb;
-    const uint32_t sx_off = 4u * (uint32_t)((sx_row < a.m ? sx_row : a.m - 1) - m0) * (uint32_t)a.kb;
-    auto copy = [&](int s, int stage) __attribute__((always_inline)) {
-        const bool cut = s == a.kb - 1 && (a.k & 127);
+    const uint32_t wd_off = weight_scale(lane) * (uint32_t)a.kb;  // up to 2^14 * 2^13
+    const bool of_rows = 64 * wave < SX;
+    const float* sc_base = of_rows ? a.xd + (int64_t)m0 * a.kb : a.wd;
+    const uint32_t sc_off =
+        4u * (of_rows ? (uint32_t)((sx_row < a.m ? sx_row : a.m - 1) - m0) * (uint32_t)a.kb : wd_off);
+    auto scale_stage = [&](int s) __attribute__((always_inline)) { return lds_sx + (uint32_t)(s % kF8ScaleStages) * SW * 4; };
+    auto copy_scales = [&](int s) __attribute__((always_inline)) {
+        f8_copy4(reinterpret_cast<const uint8_t*>(sc_base + s), sc_off, scale_stage(s) + (uint32_t)(of_rows ? 256 * wave : SX * 4));
+    };
+
+    // copy j of step s into stage `to`; copy COPIES is the wave's of the scales, of which there are more stages
+    auto copy = [&](int s, int j, int to) __attribute__((always_inline)) {
+        if (j == COPIES) copy_scales(s);
+        else if (ROWS / 8 % W == 0 || wave + W * j < ROWS / 8)
+            f8_copy16(base[j] + (int64_t)s * 128, off[j], lds + (uint32_t)(to * ROWS + stage_row(j)) * 128);
+    };
+    // all of a step where no turns are taken; the step of a cut block into stage 0, zeros past its inputs
+    auto copy_step_scales = [&](int s) __attribute__((always_inline)) {
+        if (W == 8 || of_rows) copy_scales(s);
+        if (W != 8 && wave == W - 1)
+            f8_copy4(reinterpret_cast<const uint8_t*>(a.wd + s), 4u * wd_off, scale_stage(s) + SX * 4);
+    };
+    auto copy_cut = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < COPIES; ++j) {
-            const int c = wave + W * j;
-            if (ROWS / 8 % W != 0 && c >= ROWS / 8) break;
-            const uint32_t at = lds + (uint32_t)(stage * ROWS * 128 + c * 1024);
-            if (!cut) f8_copy16(base[j] + (int64_t)s * 128, off[j], at);
-            else f8_copy16_or_zeros(base[j] + (int64_t)s * 128, off[j], lc * 16 < (a.k & 127), at);
-        }
-        if (64 * wave < BM)
-            f8_copy4(reinterpret_cast<const uint8_t*>(sx_base + s), sx_off, lds_sx + (uint32_t)(stage * SX + 64 * wave) * 4);
+        for (int j = 0; j < COPIES; ++j)
+            if (ROWS / 8 % W == 0 || wave + W * j < ROWS / 8)
+                f8_copy16_or_zeros(base[j] + (int64_t)s * 128, off[j], lc * 16 < (a.k & 127),
+                                   lds + (uint32_t)stage_row(j) * 128);
+        copy_step_scales(s);
     };
 
     const int l16 = lane & 15, g = lane >> 4;
-    const uint32_t chunk = 16u * (uint32_t)(g ^ (l16 & 7));
-    const uint32_t a_at = (uint32_t)(wn * TN * 16 + l16) * 128 + chunk;
-    const uint32_t b_at = (uint32_t)(BN + wm * TM * 16 + l16) * 128 + chunk;
-    auto fragment = [&](uint32_t at) __attribute__((always_inline)) {
-        const f8_i32x4 lo = *reinterpret_cast<const f8_i32x4*>(f8_smem + at);
-        const f8_i32x4 hi = *reinterpret_cast<const f8_i32x4*>(f8_smem + (at ^ 64u));
-        return Codes(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    // fragment i of the rows from `row` of stage `from` on
+    const uint32_t lane_at = (uint32_t)l16 * 128 + 16u * (uint32_t)(g ^ (l16 & 7));
+    auto fragment = [&](int from, int row, int i) __attribute__((always_inline)) {
+        const uint8_t* at = f8_smem + (from * ROWS + row + i * 16) * 128;
+        Codes c;
+        c.set(*reinterpret_cast<const f8_i32x4*>(at + lane_at), *reinterpret_cast<const f8_i32x4*>(at + (lane_at ^ 64u)));
+        return c;
     };
 
-    // scale rows of the wave's weights (past the matrix: the last one, of rows that are not stored)
     const int out0 = n0 + wn * OUT;
-    const int last_block = (a.n_out - 1) / 128;
-    const int wb = out0 / 128 < last_block ? out0 / 128 : last_block;
-    const float* wd0 = a.wd + (int64_t)wb * a.kb;
-    const float* wd1 = SILU ? a.wd + (int64_t)(wb + last_block + 1) * a.kb : wd0;
-
     f8_f32x4 acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
 
-    copy(0, 0);
-    wait_vmcnt_mem<0>();
-    __syncthreads();
-    for (int s = 0; s < a.kb; ++s) {
-        const int stage = s & 1;
-        if (s + 1 < a.kb) copy(s + 1, stage ^ 1);
-        const uint32_t at = (uint32_t)(stage * ROWS * 128);
-        const float* sx = reinterpret_cast<const float*>(f8_smem + 2 * ROWS * 128) + stage * SX + wm * TM * 16 + l16;
-        float c0[TM], c1[TM];
-        const float w0 = wd0[s], w1 = wd1[s];
-        auto b = f8_each<TM>([&](int j) __attribute__((always_inline)) { return fragment(at + b_at + j * 2048); });
+    // A step's products in PARTS parts of its activation rows; the weights' fragments serve them all.
+    Codes av[TN], bv[PM];
+    float c0[PM] = {}, c1[PM] = {};
+    float sx[PM], w0 = 0.f, w1 = 0.f;
+    auto load_from = [&](int s, int h, int from) __attribute__((always_inline)) {
+        if (h == 0)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const float v = sx[16 * j];
-            c0[j] = v * w0;
-            c1[j] = SILU ? v * w1 : c0[j];
+            for (int i = 0; i < TN; ++i) av[i] = fragment(from, wn * TN * 16, i);
+#pragma unroll
+        for (int j = 0; j < PM; ++j) bv[j] = fragment(from, BN + wm * TM * 16, h * PM + j);
+        const float* at = reinterpret_cast<const float*>(f8_smem + 2 * ROWS * 128) + (s % kF8ScaleStages) * SW;
+#pragma unroll
+        for (int j = 0; j < PM; ++j) sx[j] = at[(wm * TM + h * PM + j) * 16 + l16];
+        w0 = at[SX + 2 * wn];
+        if (SILU) w1 = at[SX + 2 * wn + 1];
+    };
+    auto ready = [&](int, int) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < PM; ++j) {
+            c0[j] = sx[j] * w0;
+            c1[j] = SILU ? sx[j] * w1 : c0[j];
         }
+    };
+    // A sum joins the accumulators LAG instructions after it was asked for, in this order
+    // (scheduling fences): the lanes then work while the matrix cores do.  The last LAG join in finish().
+    constexpr int LAG = TN * PM < 3 ? TN * PM : 3;
+    f8_f32x4 t[LAG + 1] = {};
+    auto join = [&](int h, int p) __attribute__((always_inline)) {
+        const int i = p / PM, j = p % PM;
+        const float c = SILU && i >= TN / 2 ? c1[j] : c0[j];
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const Codes av = fragment(at + a_at + i * 2048);
-            f8_f32x4 t[TM];
+        for (int e = 0; e < 4; ++e)
+            acc[i][h * PM + j][e] = __builtin_fmaf(c, t[p % (LAG + 1)][e], acc[i][h * PM + j][e]);
+    };
+    auto multiply = [&](int h, auto&& side) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < TM; ++j) t[j] = f8_block_sum(av, b.at[j]);
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const float c = SILU && i >= TN / 2 ? c1[j] : c0[j];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c, t[j][e], acc[i][j][e]);
-            }
+        for (int p = 0; p < TN * PM; ++p) {
+            t[p % (LAG + 1)] = f8_block_sum(av[p / PM], bv[p % PM]);
+            if (p >= LAG) join(h, p - LAG);
+            side(p);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    auto finish = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = TN * PM - LAG; p < TN * PM; ++p) join(h, p);
+    };
+    auto load = [&](int s, int h) __attribute__((always_inline)) { load_from(s, h, s & 1); };
+    const int whole = a.k >> 7;  // steps; a cut block is a step of its own behind them
+    if constexpr (W == 8) {
+        if (whole)
+            f8_turns<XC + 1, YC>(
+                wave >> 2, whole,
+                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, i < XC ? i : COPIES, to); },
+                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, XC + i, to); }, load, finish, ready,
+                multiply);
+    } else {
+        auto copies = [&](int s, int to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < COPIES; ++j) copy(s, j, to);
+            copy_step_scales(s);
+        };
+        if (whole) copies(0, 0);
         wait_vmcnt_mem<0>();
         __syncthreads();
+        for (int s = 0; s < whole; ++s) {
+            if (s + 1 < whole) copies(s + 1, (s + 1) & 1);
+            load(s, 0);
+            ready(s, 0);
+            multiply(0, [](int) {});
+            finish(0);
+            wait_vmcnt_mem<0>();
+            __syncthreads();
+        }
+    }
+    if (a.k & 127) {
+        copy_cut(whole);
+        wait_vmcnt_mem<0>();
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+            load_from(whole, h, 0);
+            ready(whole, h);
+            multiply(h, [](int) {});
+            finish(h);
+        }
     }
 
     // element e of fragment (i, j): output 16i + 4g + e of the wave, row 16j + l16
@@ -235,7 +332,6 @@ hipError_t launch_tile(F8LinearArgs a, hipStream_t stream) {
     a.n_tiles = (a.n_out + COLS - 1) / COLS;
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
     if (f8_grid(tiles) * (64 * WN * WM) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-    a.tiles = (int)tiles;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WN * WM), lds, stream, a);
     return hipGetLastError();
 }

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "lds_dma.h"
@@ -68,13 +69,116 @@ __device__ __forceinline__ uint32_t f8_lds_address(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
 }
 
+// A float that no kernel of the launch writes, read through the scalar cache: a vector load would
+// be waited for together with every copy that is older than its use.  p is wave-uniform.
+__device__ __forceinline__ float f8_uniform(const float* p) {
+    typedef const float __attribute__((address_space(4))) * Constant;
+    return *(Constant)(uintptr_t)p;
+}
+
 // Blocks go to the eight XCDs in turn: give each XCD a run of neighbouring tiles, which share
-// their operands in its L2.
-constexpr int kF8Xcds = 8;
+// their operands in its L2; the run goes through bands of eight rows of tiles, column by column,
+// so that the 32 tiles that an XCD works at once read 8 + 4 pieces of the operands, not 32 + 1.
+constexpr int kF8Xcds = 8, kF8Band = 8;
 inline int64_t f8_grid(int64_t tiles) { return (tiles + kF8Xcds - 1) / kF8Xcds * kF8Xcds; }
-__device__ __forceinline__ int f8_tile_of_block(int block, int tiles) {
-    const int per_xcd = (tiles + kF8Xcds - 1) / kF8Xcds;
-    return block % kF8Xcds * per_xcd + block / kF8Xcds;
+struct F8Tile {
+    int row, col;
+    bool inside;
+};
+__device__ __forceinline__ F8Tile f8_tile_of_block(int block, int rows, int cols) {
+    const int tiles = rows * cols, per_xcd = (tiles + kF8Xcds - 1) / kF8Xcds;
+    const int t = block % kF8Xcds * per_xcd + block / kF8Xcds;
+    const int band = t / (kF8Band * cols), in = t - band * kF8Band * cols;
+    const int left = rows - band * kF8Band, height = left < kF8Band ? left : kF8Band;
+    // (t past the last tile: height may not be positive)
+    const int h = height > 0 ? height : 1;
+    return {band * kF8Band + in % h, in / h, t < tiles && block / kF8Xcds < per_xcd};
+}
+
+// The steps of a tile of eight waves, two on a SIMD, in turns: while the waves 0 .. 3 (group 0) read
+// fragments from LDS, the waves 4 .. 7 (group 1) multiply, and the other way round, so that the matrix
+// cores of a SIMD always have one wave's products.  A turn ends with a barrier of all eight.  A step is
+// two pairs of turns: group 0 reads its first fragments of step s in turn 4s, multiplies in 4s + 1, reads the
+// rest in 4s + 2 and multiplies in 4s + 3; group 1 is one turn behind.
+//
+// LDS has two stages.  The piece X of step s, what both groups read first, is done with after turn
+// 4s + 1, the piece Y, what they read last, after 4s + 3: each is asked for again, for step s + 2, as soon
+// as that, between products (X by group 1 in 4s + 2 and by group 0 in 4s + 3, Y in 4s + 4 and 4s + 5), and
+// waited for in the turn before it is read, 4s + 7 and 4s + 9, by a count of the copies that are younger, so
+// that a copy has at least four turns.  (4096 rows of 8192 x 8192 in e4m3: whole stages copied again, 260 us;
+// so, 237 us; asked for in the reading turns instead, 247 us; of which the products are about 150.)
+//   x(s, i, to), i < kX, y(s, i, to), i < kY: copies of step s, into stage `to`; past the end the last
+//                        step is copied again, unread
+//   load(s, h)         : asks for the fragments of part h
+//   finish(h)          : adds up what multiply(h) left, while the other group multiplies and the
+//                        fragments of the next part are on their way
+//   ready(s, h)        : what has to be done with the fragments of part h before they are multiplied
+//   multiply(h, side)  : the products; side(p) is called between them, p = 0, 1, .. (at least kX times)
+// At the end every copy has landed and no wave reads LDS any more.
+__device__ __forceinline__ void f8_end_turn() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int kX, int kY, class X, class Y, class Load, class Finish, class Ready, class Multiply>
+__device__ __forceinline__ void f8_turns(int group, int steps, X&& x, Y&& y, Load&& load, Finish&& finish,
+                                         Ready&& ready, Multiply&& multiply) {
+    const int last = steps - 1;
+    auto x_copy = [&](int s, int i) __attribute__((always_inline)) {
+        if (i < kX) x(s < last ? s : last, i, s & 1);
+    };
+    auto y_copy = [&](int s, int i) __attribute__((always_inline)) {
+        if (i < kY) y(s < last ? s : last, i, s & 1);
+    };
+    auto turns = [&](int s, auto hc, auto gc) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value, of = decltype(gc)::value;
+        load(s, h);
+        __builtin_amdgcn_sched_barrier(0);
+        finish(h ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_lgkmcnt_mem<0>();
+        ready(s, h);
+        if (of == 1) wait_vmcnt_mem<kX + kY>();  // h = 0: Y of step s, 1: X of step s + 1
+        f8_end_turn();
+        __builtin_amdgcn_s_setprio(1);
+        multiply(h, [&](int p) __attribute__((always_inline)) {
+            if (of == h) y_copy(s + 1 + of, p);
+            else x_copy(s + 2, p);
+        });
+        __builtin_amdgcn_s_setprio(0);
+        if (of == 0) wait_vmcnt_mem<kX + kY>();
+        f8_end_turn();
+    };
+#pragma unroll
+    for (int i = 0; i < kX; ++i) x_copy(0, i);
+#pragma unroll
+    for (int i = 0; i < kY; ++i) y_copy(0, i);
+#pragma unroll
+    for (int i = 0; i < kX; ++i) x_copy(1, i);
+    wait_vmcnt_mem<kX + kY>();
+    f8_end_turn();
+    // a loop for each group: with the waits under a branch in one loop the registers do not suffice
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
+    if (group == 0) {
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < steps; ++s) {
+            turns(s, zero, zero);
+            turns(s, one, zero);
+        }
+        f8_end_turn();
+    } else {
+#pragma unroll
+        for (int i = 0; i < kY; ++i) y_copy(1, i);
+        f8_end_turn();
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < steps; ++s) {
+            turns(s, zero, one);
+            turns(s, one, one);
+        }
+    }
+    finish(1);
+    wait_vmcnt_mem<0>();
 }
 
 // Eight codes (two words) as bf16, exactly.
@@ -87,7 +191,7 @@ __device__ __forceinline__ f8_bf16x8 f8_widen(int lo, int hi) {
     return f8_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// An array of f(0) .. f(N - 1), of a type that has no default.
+// An array of f(0) .. f(N - 1).
 template <class V, int N>
 struct F8Array {
     V at[N];
