@@ -70,9 +70,24 @@ __device__ __forceinline__ f8_f32x4 f8_block_sum(const F8Widened& a, const F8Wid
     return t;
 }
 
-// Words of a stage of scales: those of the tile's rows in whole copies of 64 (of each of the first four
-// waves in the form of eight, which does not ask how many its tile has), then one copy of those of
-// its weight blocks (in the form of eight one of each of the other four waves, all alike).
+// Four neighbouring outputs of a row from column n on: the products, or SiLU(gate) * up of the two.
+template <bool SILU, class T>
+__device__ __forceinline__ void f8_store_outputs(const F8LinearArgs& a, int row, int n, f8_f32x4 v, f8_f32x4 u) {
+    const int inside = a.n_out - n;
+    if constexpr (SILU) {
+        if (a.gu) {
+            T* gu = static_cast<T*>(a.gu) + (int64_t)row * a.ldgu + n;
+            f8_store4(gu, v, inside, a.vec_gu);
+            f8_store4(gu + a.n_out, u, inside, a.vec_gu && a.n_out % 4 == 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + __expf(-v[e])) * u[e];
+    }
+    f8_store4(static_cast<T*>(a.y) + (int64_t)row * a.ldy + n, v, inside, a.vec);
+}
+
+// Words of a stage of scales, which every wave copies 64 of: the first BM / 64 waves (of eight waves the
+// first four) the tile's rows', the others, all alike, those of its weight blocks.
 template <int WN, int WM, int TM>
 constexpr int f8_scale_rows() {
     return WN * WM == 8 ? 256 : (WM * TM * 16 + 63) / 64 * 64;
@@ -81,20 +96,27 @@ template <int WN, int WM, int TM>
 constexpr int f8_scale_words() {
     return f8_scale_rows<WN, WM, TM>() + 64;
 }
-constexpr int kF8ScaleStages = 4;
-template <int WN, int WM, int TN, int TM>
+// Stages of rows and of scales (the turns of eight waves free the rows earlier than the scales).
+template <int WN, int WM, int D>
+constexpr int f8_scale_stages() {
+    return WN * WM == 8 ? 4 : D;
+}
+template <int WN, int WM, int TN, int TM, int D>
 constexpr size_t f8_linear_lds_bytes() {
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
-    return 2 * (size_t)(BN + BM) * 128 + kF8ScaleStages * (size_t)f8_scale_words<WN, WM, TM>() * 4;
+    return D * (size_t)(BN + BM) * 128 + f8_scale_stages<WN, WM, D>() * (size_t)f8_scale_words<WN, WM, TM>() * 4;
 }
 
-template <int WN, int WM, int TN, int TM, bool SILU, class T>
+template <int WN, int WM, int TN, int TM, int D, bool SILU, class T>
 __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a) {
     constexpr int W = WN * WM, BN = WN * TN * 16, BM = WM * TM * 16, ROWS = BN + BM;
-    constexpr int COPIES = (ROWS / 8 + W - 1) / W;  // of a wave and step, eight rows each
+    constexpr int COPIES = ROWS / 8 / W;  // of a wave and step, eight rows each, and one of scales
+    constexpr int SCALE_STAGES = f8_scale_stages<WN, WM, D>();
     constexpr int OUT = SILU ? TN * 8 : TN * 16;  // outputs of a wave
     using Codes = std::conditional_t<sizeof(T) == 4, F8Widened, F8Codes>;
     static_assert(128 % (TN * 16) == 0 && (!SILU || TN % 2 == 0), "a wave's weight rows lie in one block");
+    static_assert(ROWS / 8 % W == 0 && f8_scale_rows<WN, WM, TM>() / 64 < W && (W != 8 || D == 2),
+                  "every wave has the same number of copies");
     extern __shared__ __attribute__((aligned(16))) uint8_t f8_smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -147,10 +169,10 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
         off[j] = (uint32_t)row * (uint32_t)a.k + 16u * lc;
     }
     const uint32_t lds = f8_lds_address(f8_smem);
-    const uint32_t lds_sx = lds + 2 * ROWS * 128;
-    // Scales, a copy of four bytes a lane: the waves w < SX / 64 those of rows 64w .., the others (the first
-    // wave in a second copy, if there are no others) word i the scale of the weight block of wave i / 2 (gate's
-    // and up's where they are fused); past the matrix: the last block, of rows that are not stored.
+    const uint32_t lds_sx = lds + D * ROWS * 128;
+    // Scales, a copy of four bytes a lane: the waves w < SX / 64 those of rows 64w .., the others word i the
+    // scale of the weight block of wave i / 2 (gate's and up's where they are fused); past the matrix: the
+    // last block, of rows that are not stored.
     constexpr int SX = f8_scale_rows<WN, WM, TM>(), SW = f8_scale_words<WN, WM, TM>();
     const int last_block = (a.n_out - 1) / 128;
     auto weight_scale = [&](int i) __attribute__((always_inline)) {
@@ -158,35 +180,27 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
         return (uint32_t)((b < last_block ? b : last_block) + (SILU && i % 2 ? last_block + 1 : 0));
     };
     const int sx_row = m0 + 64 * wave + lane;
-    const uint32_t wd_off = weight_scale(lane) * (uint32_t)a.kb;  // up to 2^14 * 2^13
     const bool of_rows = 64 * wave < SX;
     const float* sc_base = of_rows ? a.xd + (int64_t)m0 * a.kb : a.wd;
     const uint32_t sc_off =
-        4u * (of_rows ? (uint32_t)((sx_row < a.m ? sx_row : a.m - 1) - m0) * (uint32_t)a.kb : wd_off);
-    auto scale_stage = [&](int s) __attribute__((always_inline)) { return lds_sx + (uint32_t)(s % kF8ScaleStages) * SW * 4; };
+        4u * (of_rows ? (uint32_t)((sx_row < a.m ? sx_row : a.m - 1) - m0) * (uint32_t)a.kb : weight_scale(lane) * (uint32_t)a.kb);
+    auto scale_stage = [&](int s) __attribute__((always_inline)) { return lds_sx + (uint32_t)(s % SCALE_STAGES) * SW * 4; };
     auto copy_scales = [&](int s) __attribute__((always_inline)) {
         f8_copy4(reinterpret_cast<const uint8_t*>(sc_base + s), sc_off, scale_stage(s) + (uint32_t)(of_rows ? 256 * wave : SX * 4));
     };
 
-    // copy j of step s into stage `to`; copy COPIES is the wave's of the scales, of which there are more stages
+    // copy j of step s into stage `to`; copy COPIES is the wave's of the scales
     auto copy = [&](int s, int j, int to) __attribute__((always_inline)) {
         if (j == COPIES) copy_scales(s);
-        else if (ROWS / 8 % W == 0 || wave + W * j < ROWS / 8)
-            f8_copy16(base[j] + (int64_t)s * 128, off[j], lds + (uint32_t)(to * ROWS + stage_row(j)) * 128);
+        else f8_copy16(base[j] + (int64_t)s * 128, off[j], lds + (uint32_t)(to * ROWS + stage_row(j)) * 128);
     };
-    // all of a step where no turns are taken; the step of a cut block into stage 0, zeros past its inputs
-    auto copy_step_scales = [&](int s) __attribute__((always_inline)) {
-        if (W == 8 || of_rows) copy_scales(s);
-        if (W != 8 && wave == W - 1)
-            f8_copy4(reinterpret_cast<const uint8_t*>(a.wd + s), 4u * wd_off, scale_stage(s) + SX * 4);
-    };
+    // the step of a cut block into stage 0, zeros past its inputs
     auto copy_cut = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < COPIES; ++j)
-            if (ROWS / 8 % W == 0 || wave + W * j < ROWS / 8)
-                f8_copy16_or_zeros(base[j] + (int64_t)s * 128, off[j], lc * 16 < (a.k & 127),
-                                   lds + (uint32_t)stage_row(j) * 128);
-        copy_step_scales(s);
+            f8_copy16_or_zeros(base[j] + (int64_t)s * 128, off[j], lc * 16 < (a.k & 127),
+                               lds + (uint32_t)stage_row(j) * 128);
+        copy_scales(s);
     };
 
     const int l16 = lane & 15, g = lane >> 4;
@@ -216,7 +230,7 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
             for (int i = 0; i < TN; ++i) av[i] = fragment(from, wn * TN * 16, i);
 #pragma unroll
         for (int j = 0; j < PM; ++j) bv[j] = fragment(from, BN + wm * TM * 16, h * PM + j);
-        const float* at = reinterpret_cast<const float*>(f8_smem + 2 * ROWS * 128) + (s % kF8ScaleStages) * SW;
+        const float* at = reinterpret_cast<const float*>(f8_smem + D * ROWS * 128) + (s % SCALE_STAGES) * SW;
 #pragma unroll
         for (int j = 0; j < PM; ++j) sx[j] = at[(wm * TM + h * PM + j) * 16 + l16];
         w0 = at[SX + 2 * wn];
@@ -253,33 +267,36 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
 #pragma unroll
         for (int p = TN * PM - LAG; p < TN * PM; ++p) join(h, p);
     };
-    auto load = [&](int s, int h) __attribute__((always_inline)) { load_from(s, h, s & 1); };
     const int whole = a.k >> 7;  // steps; a cut block is a step of its own behind them
     if constexpr (W == 8) {
         if (whole)
             f8_turns<XC + 1, YC>(
                 wave >> 2, whole,
                 [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, i < XC ? i : COPIES, to); },
-                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, XC + i, to); }, load, finish, ready,
-                multiply);
+                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, XC + i, to); },
+                [&](int s, int h) __attribute__((always_inline)) { load_from(s, h, s & 1); }, finish, ready, multiply);
     } else {
+        // D stages: step s + D - 1 is asked for when every wave has read step s - 1, whose stage it takes
         auto copies = [&](int s, int to) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < COPIES; ++j) copy(s, j, to);
-            copy_step_scales(s);
+            for (int j = 0; j <= COPIES; ++j) copy(s, j, to);
         };
-        if (whole) copies(0, 0);
-        wait_vmcnt_mem<0>();
-        __syncthreads();
+#pragma unroll
+        for (int d = 0; d + 1 < D; ++d)
+            if (d < whole) copies(d, d);
+        int stage = 0, free = D - 1;
         for (int s = 0; s < whole; ++s) {
-            if (s + 1 < whole) copies(s + 1, (s + 1) & 1);
-            load(s, 0);
+            f8_wait_stages<D - 2, COPIES + 1>(whole - 1 - s);
+            __syncthreads();
+            if (s + D - 1 < whole) copies(s + D - 1, free);
+            load_from(s, 0, stage);
             ready(s, 0);
             multiply(0, [](int) {});
             finish(0);
-            wait_vmcnt_mem<0>();
-            __syncthreads();
+            free = stage;
+            stage = stage + 1 < D ? stage + 1 : 0;
         }
+        __syncthreads();
     }
     if (a.k & 127) {
         copy_cut(whole);
@@ -299,31 +316,17 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
     for (int j = 0; j < TM; ++j) {
         const int row = m0 + (wm * TM + j) * 16 + l16;
         if (row >= a.m) continue;
-        T* y = static_cast<T*>(a.y) + (int64_t)row * a.ldy;
 #pragma unroll
-        for (int i = 0; i < (SILU ? TN / 2 : TN); ++i) {
-            const int n = out0 + 16 * i + 4 * g, inside = a.n_out - n;
-            f8_f32x4 v = acc[i][j];
-            if constexpr (SILU) {
-                const f8_f32x4 u = acc[i + TN / 2][j];
-                if (a.gu) {
-                    T* gu = static_cast<T*>(a.gu) + (int64_t)row * a.ldgu + n;
-                    f8_store4(gu, v, inside, a.vec_gu);
-                    f8_store4(gu + a.n_out, u, inside, a.vec_gu && a.n_out % 4 == 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + __expf(-v[e])) * u[e];
-            }
-            f8_store4(y + n, v, inside, a.vec);
-        }
+        for (int i = 0; i < (SILU ? TN / 2 : TN); ++i)
+            f8_store_outputs<SILU, T>(a, row, out0 + 16 * i + 4 * g, acc[i][j], acc[SILU ? i + TN / 2 : i][j]);
     }
 }
 
-template <int WN, int WM, int TN, int TM, bool SILU, class T>
+template <int WN, int WM, int TN, int TM, int D, bool SILU, class T>
 hipError_t launch_tile(F8LinearArgs a, hipStream_t stream) {
     constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-    auto kernel = f8_linear_kernel<WN, WM, TN, TM, SILU, T>;
-    constexpr size_t lds = f8_linear_lds_bytes<WN, WM, TN, TM>();
+    auto kernel = f8_linear_kernel<WN, WM, TN, TM, D, SILU, T>;
+    constexpr size_t lds = f8_linear_lds_bytes<WN, WM, TN, TM, D>();
     static thread_local uint64_t allowed = 0;
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
     if (e != hipSuccess) return e;
@@ -336,12 +339,224 @@ hipError_t launch_tile(F8LinearArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------------------- few activation rows
+//
+// Bound by the weights' bytes.  A workgroup owns R x 16 weight rows (fused: half of them gate rows, half
+// their up rows) and all activation rows (MT fragments of 16; rows past the call's are its last one); its
+// WK waves share the blocks of inputs, block b to wave b % WK, and their sums meet in LDS and are added in
+// the order of the waves.  A wave has D stages of LDS of its own, filled D blocks ahead by direct copies:
+// loads into the instruction's registers, whose neighbouring lanes are rows apart, reached a sixth of
+// the rate at 64 rows (4096 x 24576: 88 us).
+template <int WK, int R, int MT, int D>
+constexpr size_t f8_rows_stage_bytes() {
+    return (size_t)(R + MT) * 2048 + (MT * 16 + R <= 64 ? 1 : 2) * 256;
+}
+template <int WK, int R, int MT, int D>
+constexpr size_t f8_rows_lds_bytes() {
+    const size_t ring = WK * D * f8_rows_stage_bytes<WK, R, MT, D>(), sums = (size_t)WK * MT * R * 64 * 16;
+    return ring > sums ? ring : sums;
+}
+
+template <int WK, int R, int MT, int D, bool SILU, class T>
+__global__ __launch_bounds__(64 * WK) void f8_rows_kernel(F8LinearArgs a) {
+    constexpr int HALF = SILU ? R / 2 : R;  // fragments of outputs
+    constexpr int STAGE = f8_rows_stage_bytes<WK, R, MT, D>();
+    constexpr int SCALES = MT * 16 + R <= 64 ? 1 : 2, COPIES = 2 * (R + MT) + SCALES;  // of a stage
+    static_assert(R <= 64 && MT <= 4 && (D - 1) * COPIES < 64 && (!SILU || R % 2 == 0), "copies are counted");
+    using Codes = std::conditional_t<sizeof(T) == 4, F8Widened, F8Codes>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t f8_smem[];
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * (16 * HALF);
+
+    // copy c of a stage: rows 8(c % 2) .. + 7 of fragment c / 2 (weights, then activations), lane l the
+    // chunk l % 8 of row l / 8 as in the tiles; past the operand: its last row
+    const int lr = lane >> 3, lc = (lane & 7) ^ lr;
+    uint32_t off[2 * (R + MT)];
+#pragma unroll
+    for (int c = 0; c < 2 * (R + MT); ++c) {
+        const int f = c / 2, rows = f < R ? a.n_out - n0 : a.m;
+        const int row = (f < R ? 16 * (f % HALF) : 16 * (f - R)) + 8 * (c % 2) + lr;
+        off[c] = (uint32_t)(row < rows ? row : rows - 1) * (uint32_t)a.k + 16u * lc;
+    }
+    const uint8_t* w[2] = {a.w + (int64_t)n0 * a.k, a.w + (int64_t)(n0 + (SILU ? a.n_out : 0)) * a.k};
+    // word i of a stage's scales: row i's, then those of the weights' fragments
+    auto scale_word = [&](int i) __attribute__((always_inline)) {
+        const int f = i - MT * 16;
+        const int blocks = (a.n_out + 127) / 128, at = (n0 + 16 * (f % HALF)) / 128;
+        const int b = (at < blocks ? at : blocks - 1) + (SILU && f >= HALF ? blocks : 0);
+        return i < MT * 16 ? a.xd + (int64_t)(i < a.m ? i : a.m - 1) * a.kb : a.wd + (int64_t)(f < R ? b : 0) * a.kb;
+    };
+    const float* scale_at[SCALES];
+#pragma unroll
+    for (int i = 0; i < SCALES; ++i) scale_at[i] = scale_word(64 * i + lane);
+
+    // Workgroups start at different blocks: rows are often a multiple of 4 KB apart, and all of them in step
+    // would ask the same few channels of the L2 (24576 x 4096 fused, 8 rows: 24.4 us, so 21.4).
+    const int whole = a.k >> 7;
+    const int turns = (whole - wave + WK - 1) / WK;  // whole blocks of this wave
+    const int first = turns > 0 ? blockIdx.x % turns : 0;
+    const uint32_t lds = f8_lds_address(f8_smem) + (uint32_t)(wave * D * STAGE);
+    auto copy_scales = [&](int b, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i) f8_copy4_from(scale_at[i] + b, to + (uint32_t)((R + MT) * 2048 + 256 * i));
+    };
+    auto copies = [&](int turn, int slot) __attribute__((always_inline)) {
+        const int from = turn + first - (turn + first < turns ? 0 : turns), b = from * WK + wave;
+        const uint32_t to = lds + (uint32_t)(slot * STAGE);
+#pragma unroll
+        for (int c = 0; c < 2 * (R + MT); ++c)
+            f8_copy16((c / 2 < R ? w[c / 2 / HALF] : a.x) + (int64_t)b * 128, off[c], to + (uint32_t)(c * 1024));
+        copy_scales(b, to);
+    };
+    f8_f32x4 acc[MT][R];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[j][r] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t lane_at = (uint32_t)l16 * 128 + 16u * (uint32_t)(g ^ (l16 & 7));
+    struct Stage {
+        f8_i32x4 w[R][2], x[MT][2];
+        float wd[R], xd[MT];
+    };
+    auto read = [&](int slot) __attribute__((always_inline)) {
+        const uint8_t* at = f8_smem + (wave * D + slot) * STAGE;
+        const float* scales = reinterpret_cast<const float*>(at + (R + MT) * 2048);
+        Stage v;
+#pragma unroll
+        for (int f = 0; f < R + MT; ++f) {
+            f8_i32x4(&to)[2] = f < R ? v.w[f < R ? f : 0] : v.x[f < R ? 0 : f - R];
+            to[0] = *reinterpret_cast<const f8_i32x4*>(at + f * 2048 + lane_at);
+            to[1] = *reinterpret_cast<const f8_i32x4*>(at + f * 2048 + (lane_at ^ 64u));
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) v.xd[j] = scales[16 * j + l16];
+#pragma unroll
+        for (int r = 0; r < R; ++r) v.wd[r] = scales[16 * MT + r];
+        return v;
+    };
+    auto multiply = [&](const Stage& v) __attribute__((always_inline)) {
+        Codes wc[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) wc[r].set(v.w[r][0], v.w[r][1]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            Codes xc;
+            xc.set(v.x[j][0], v.x[j][1]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const f8_f32x4 t = f8_block_sum(wc[r], xc);
+                const float c = v.xd[j] * v.wd[r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][r][e] = __builtin_fmaf(c, t[e], acc[j][r][e]);
+            }
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < turns) copies(d, d);
+    int t = 0, slot = 0;
+    for (; t + D < turns; ++t) {
+        wait_vmcnt_mem<(D - 1) * COPIES>();
+        const Stage v = read(slot);
+        wait_lgkmcnt_mem<0>();  // read before it is copied over
+        copies(t + D, slot);
+        multiply(v);
+        slot = slot + 1 < D ? slot + 1 : 0;
+    }
+    auto drain = [&](auto dc) __attribute__((always_inline)) {
+        constexpr int d = decltype(dc)::value;
+        if (turns - t > d) {
+            wait_vmcnt_mem<d * COPIES>();
+            multiply(read(slot));
+            ++t;
+            slot = slot + 1 < D ? slot + 1 : 0;
+        }
+    };
+    if constexpr (D > 2) drain(std::integral_constant<int, 2>{});
+    if constexpr (D > 1) drain(std::integral_constant<int, 1>{});
+    drain(std::integral_constant<int, 0>{});
+    static_assert(D <= 3, "stages are drained one by one");
+    if ((a.k & 127) && whole % WK == wave) {  // the cut block, zeros past its inputs
+        wait_lgkmcnt_mem<0>();
+#pragma unroll
+        for (int c = 0; c < 2 * (R + MT); ++c)
+            f8_copy16_or_zeros((c / 2 < R ? w[c / 2 / HALF] : a.x) + (int64_t)whole * 128, off[c],
+                               16 * lc < (a.k & 127), lds + (uint32_t)(c * 1024));
+        copy_scales(whole, lds);
+        wait_vmcnt_mem<0>();
+        multiply(read(0));
+    }
+
+    __syncthreads();  // every wave is done with its stages
+    f8_f32x4* sums = reinterpret_cast<f8_f32x4*>(f8_smem);
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) sums[((wave * MT + j) * R + r) * 64 + lane] = acc[j][r];
+    __syncthreads();
+    for (int i = threadIdx.x; i < MT * HALF * 64; i += 64 * WK) {
+        const int at = i & 63, r = (i >> 6) % HALF, j = (i >> 6) / HALF;
+        auto sum = [&](int r) __attribute__((always_inline)) {
+            f8_f32x4 v = sums[(j * R + r) * 64 + at];
+#pragma unroll
+            for (int o = 1; o < WK; ++o) v += sums[((o * MT + j) * R + r) * 64 + at];
+            return v;
+        };
+        const int row = 16 * j + (at & 15);
+        if (row < a.m) f8_store_outputs<SILU, T>(a, row, n0 + 16 * r + 4 * (at >> 4), sum(r), sum(SILU ? r + HALF : r));
+    }
+}
+
+template <int WK, int R, int MT, int D, bool SILU, class T>
+hipError_t launch_rows(const F8LinearArgs& a, hipStream_t stream) {
+    auto kernel = f8_rows_kernel<WK, R, MT, D, SILU, T>;
+    constexpr size_t lds = f8_rows_lds_bytes<WK, R, MT, D>();
+    static thread_local uint64_t allowed = 0;
+    const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
+    if (e != hipSuccess) return e;
+    constexpr int COLS = 16 * (SILU ? R / 2 : R);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.n_out + COLS - 1) / COLS)), dim3(64 * WK), lds, stream, a);
+    return hipGetLastError();
+}
+
 template <bool SILU, class T>
 hipError_t launch_type(const DeviceInfo& dev, const F8LinearArgs& a, hipStream_t stream) {
-    if (a.m <= 16) return launch_tile<4, 1, 2, 1, SILU, T>(a, stream);
-    if (a.m <= 128) return launch_tile<4, 1, 2, 4, SILU, T>(a, stream);
-    if constexpr (sizeof(T) == 4) return launch_tile<4, 2, 4, 4, SILU, T>(a, stream);
-    else return launch_tile<4, 2, 4, 8, SILU, T>(a, stream);
+    const int64_t cus = dev.cu_count, cols = SILU ? 2 : 1;
+    const bool few = (a.n_out + 31) / 32 < cus;  // 16 outputs a workgroup then, not 32
+    if (a.m <= 16) return launch_rows<8, SILU ? 2 : 1, 1, SILU ? 3 : 2, SILU, T>(a, stream);
+    if constexpr (!SILU) {
+        if (a.m <= 32 && few) return launch_rows<8, 1, 2, 2, SILU, T>(a, stream);
+        if (a.m <= 48 && few) return launch_rows<8, 1, 3, 2, SILU, T>(a, stream);
+        if (a.m <= 64 && few) return launch_rows<4, 1, 4, 3, SILU, T>(a, stream);
+    }
+    if (a.m <= 32) return launch_rows<4, 2, 2, 2, SILU, T>(a, stream);
+    if (a.m <= 48) return launch_rows<4, 2, 3, 3, SILU, T>(a, stream);
+    if (a.m <= 64) return launch_rows<4, 2, 4, 3, SILU, T>(a, stream);
+    // The tile whose rounds (a workgroup a CU) cost least, a round by its measured time for 32 blocks of
+    // inputs, in us: 16-bit results 59, 30, 23 and 16; float32 results 57, 46, 29 and 19.  Measured for
+    // 6144 x 4096 in bfloat16, in that order of tiles: 128 rows 49.6, 30.4, 23.4, 16.9; 256 rows 58.6, 30.5,
+    // 23.3, 30.9; 512 rows 58.3, 30.9, 44.2, 45.4; 4096 rows 121, 176, 254, 333.
+    constexpr bool WIDE = sizeof(T) == 4;
+    constexpr int BIG = WIDE ? 4 : 8;
+    const int64_t bn[4] = {256, 128, 128, 64}, bm[4] = {32 * BIG, 128, 64, 64};
+    const int64_t cost[4] = {WIDE ? 57 : 59, WIDE ? 46 : 30, WIDE ? 29 : 23, WIDE ? 19 : 16};
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t tiles = (a.n_out * cols + bn[i] - 1) / bn[i] * ((a.m + bm[i] - 1) / bm[i]);
+        const int64_t time = (tiles + cus - 1) / cus * cost[i];
+        if (time < least) {
+            least = time;
+            best = i;
+        }
+    }
+    switch (best) {
+        case 0: return launch_tile<4, 2, 4, BIG, 2, SILU, T>(a, stream);
+        case 1: return launch_tile<2, 2, 4, 4, 4, SILU, T>(a, stream);
+        case 2: return launch_tile<4, 1, 2, 4, 6, SILU, T>(a, stream);
+        default: return launch_tile<2, 2, 2, 2, 6, SILU, T>(a, stream);
+    }
 }
 
 template <class T>

@@ -49,6 +49,19 @@ __device__ __forceinline__ void f8_copy4(const uint8_t* base, uint32_t off, uint
         : "v"(off), "s"(base), "s"(lds)
         : "memory");
 }
+// Four bytes a lane from addresses of their own.
+__device__ __forceinline__ void f8_copy4_from(const float* src, uint32_t lds) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(src), "s"(lds)
+        : "memory");
+}
 // The same where valid, zeros where not (the cut last step of an operand).
 __device__ __forceinline__ void f8_copy16_or_zeros(const uint8_t* base, uint32_t off, bool valid, uint32_t lds) {
     asm volatile("" : "+v"(off));  // else the lanes' addresses are kept in registers for this one step
@@ -93,6 +106,18 @@ __device__ __forceinline__ F8Tile f8_tile_of_block(int block, int rows, int cols
     // (t past the last tile: height may not be positive)
     const int h = height > 0 ? height : 1;
     return {band * kF8Band + in % h, in / h, t < tiles && block / kF8Xcds < per_xcd};
+}
+
+// Waits until at most MOST stages of COPIES copies each, or `younger` if those are fewer, are on their way.
+template <int MOST, int COPIES>
+__device__ __forceinline__ void f8_wait_stages(int younger) {
+    static_assert(MOST * COPIES < 64, "copies are counted");
+    if constexpr (MOST == 0) {
+        wait_vmcnt_mem<0>();
+    } else {
+        if (younger >= MOST) wait_vmcnt_mem<MOST * COPIES>();
+        else f8_wait_stages<MOST - 1, COPIES>(younger);
+    }
 }
 
 // The steps of a tile of eight waves, two on a SIMD, in turns: while the waves 0 .. 3 (group 0) read
