@@ -9,10 +9,13 @@
 // the planes (dw: over the pairs of planes that matter) as if they were further terms of its sum.
 //
 // Both sums run over an axis that is not the contiguous one of W (dx), or of both operands (dw).
-// Fragments are turned in registers: a lane reads eight rows' neighbouring elements of its columns
-// from LDS and puts the rows of each column side by side with byte permutes.  A fragment's 16
-// columns so are every fourth (eighth) of a run of 64 (128); the lane that holds four neighbouring
-// results of each of these fragments has 16 (32) neighbouring columns of one output row.
+// Fragments are turned on their way from LDS: ds_read_b64_tr_b16 gives a lane of 16 the four rows of its
+// column from four rows of 16 two-byte columns, ds_read_b64_tr_b8 eight rows of 16 one-byte columns (by reads
+// of whole words and byte permutes instead, the fused 24576 x 4096 took 909 + 886 us at 4096 rows).
+//
+// Sums run in steps of 64 terms.  Planes have zeros up to whole steps (d's columns, the values' rows); the
+// other operand's rows past its end are its last row again, which adds zeros where it is finite, and where it
+// is not changes nothing that is finite without it.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -34,6 +37,22 @@ __device__ __forceinline__ f8_f32x4 mfma_bf16(u32x4 a, u32x4 b, f8_f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(f8_bf16x8, a), __builtin_bit_cast(f8_bf16x8, b), c,
                                                    0, 0, 0);
 }
+
+// A lane's share of a turned read, from its LDS address.
+__device__ __forceinline__ u32x2 read_turned16(const uint8_t* p) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* Lds;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(uint32_t)(uintptr_t)p));
+}
+__device__ __forceinline__ u32x2 read_turned8(const uint8_t* p) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) i32x2* Lds;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((Lds)(uint32_t)(uintptr_t)p));
+}
+
+// The bf16 parts of a float operand: 1 (bf16), 2 (binary16), 3 (float32).
+template <class T>
+constexpr int kTerms = sizeof(T) == 4 ? 3 : __is_same(T, __bf16) ? 1 : 2;
 
 // ------------------------------------------------------------------------------ bf16 parts
 
@@ -124,17 +143,21 @@ __global__ __launch_bounds__(kPartThreads) void f8_gate_up_gradient_kernel(const
     }
 }
 
-// The planes of the inputs' values [m][k].
+// The planes of the inputs' values [m][k], rows from m to `rows` zeros.
 template <int TERMS>
 __global__ __launch_bounds__(kPartThreads) void f8_values_kernel(const uint8_t* __restrict__ q,
-                                                                const float* __restrict__ d, int64_t m, int k, int kb,
-                                                                uint16_t* __restrict__ out) {
-    const int64_t per_row = k / 8, total = m * per_row;
+                                                                const float* __restrict__ d, int64_t m, int64_t rows,
+                                                                int k, int kb, uint16_t* __restrict__ out) {
+    const int64_t per_row = k / 8, total = rows * per_row;
     for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
         const int64_t row = i / per_row, col = 8 * (i - row * per_row);
+        float v[8] = {};
+        if (row >= m) {
+            store_parts<TERMS>(out + row * k + col, rows * k, v);
+            continue;
+        }
         const u32x2 c = *reinterpret_cast<const u32x2*>(q + row * k + col);
         const float s = d[row * kb + col / 128];
-        float v[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 0) * s;
@@ -142,7 +165,7 @@ __global__ __launch_bounds__(kPartThreads) void f8_values_kernel(const uint8_t* 
             v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 2) * s;
             v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 3) * s;
         }
-        store_parts<TERMS>(out + row * k + col, m * k, v);
+        store_parts<TERMS>(out + row * k + col, rows * k, v);
     }
 }
 
@@ -161,6 +184,8 @@ unsigned part_blocks(int64_t threads) {
 
 // -------------------------------------------------------------------------------- dx = d . W
 
+constexpr int kGStep = q8v::kF8Step;  // terms of the sum a step
+
 struct F8InputGradArgs {
     const uint16_t* d;  // planes of bf16 parts
     int64_t plane;      // elements from one to the next
@@ -170,29 +195,34 @@ struct F8InputGradArgs {
     const float* wd;
     void* dx;
     int64_t lddx;
-    int n, parts, terms, m, k, kb;
+    int n, parts, m, k, kb;
     int m_tiles, k_tiles;
     bool vec;
 };
 
-constexpr int kGStep = 64;  // terms of the sum a step
-
-template <int WK, int WM, int TM>
+// D stages of a tile of eight waves are two, with scale stages of their own (f8_turns).
+template <int W, int D>
+constexpr int input_grad_scale_stages() {
+    return W == 8 ? 4 : D;
+}
+template <int WK, int WM, int TM, int D>
 constexpr size_t input_grad_lds_bytes() {
-    return 2 * ((size_t)WM * TM * 16 * 2 * kGStep + (size_t)WK * 128 * kGStep);
+    return D * ((size_t)WM * TM * 16 * 2 * kGStep + (size_t)WK * 64 * kGStep) + input_grad_scale_stages<WK * WM, D>() * 256;
 }
 
-// WK x WM waves, a wave 128 columns of dx (eight fragments) x 16 TM rows.  A step is 64 rows of W,
-// all in one block of its scales: the step's sums start at zero and join the accumulators times
-// the scale.
-template <int WK, int WM, int TM, class T>
+// WK x WM waves, a wave 64 columns of dx (four fragments) x 16 TM rows.  A step is 64 rows of W, all in one
+// block of its scales: the step's sums start at zero and join the accumulators times the scale.
+template <int WK, int WM, int TM, int D, class T>
 __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGradArgs a) {
-    constexpr int W = WK * WM, BK = WK * 128, BM = WM * TM * 16;
-    constexpr int DC = BM / 8 / W;             // copies of d of a wave: eight rows of 128 bytes each
+    constexpr int W = WK * WM, BK = WK * 64, BM = WM * TM * 16;
+    constexpr int PARTS = W == 8 ? 2 : 1, PM = TM / PARTS;
     constexpr int CPR = BK / 16;               // 16-byte chunks of a row of W
     constexpr int WC = kGStep * CPR / 64 / W;  // copies of W of a wave
+    constexpr int DC = BM / 8 / W;             // copies of d of a wave: eight rows of 128 bytes each
+    constexpr int YC = W == 8 ? DC / 2 : 0, XC = WC + DC - YC;  // pieces of f8_turns: Y is the groups' last rows
     static_assert(BM / 8 % W == 0 && kGStep * CPR / 64 % W == 0, "copies divide evenly");
-    constexpr int STAGE = BM * 2 * kGStep + BK * kGStep;
+    static_assert(W != 8 || (D == 2 && WM == 2 && DC % 2 == 0 && PM * 2 % 4 == 0), "pieces divide evenly");
+    constexpr int STAGE = BM * 2 * kGStep + BK * kGStep, SCALES = input_grad_scale_stages<W, D>();
     extern __shared__ __attribute__((aligned(16))) uint8_t f8_smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -201,144 +231,199 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
     if (!tile.inside) return;  // block-uniform, before any barrier
     const int m0 = tile.row * BM, k0 = tile.col * BK;
 
+    // d: copy j is rows r .. r + 7 of the tile, r = d_row(j), chunks as in the forward tiles
     const int lr = lane >> 3, lc = (lane & 7) ^ lr;
-    uint32_t doff[DC], woff[WC];
+    auto d_row = [&](int j) __attribute__((always_inline)) {
+        const int half = j < DC - YC ? 0 : 1;
+        if (W != 8) return 8 * (wave + W * j);
+        const int q = wave + W * (half ? j - (DC - YC) : j);  // of 2 PM copies a group and half
+        return q / (2 * PM) * (TM * 16) + half * PM * 16 + q % (2 * PM) * 8;
+    };
+    uint32_t doff[DC];
 #pragma unroll
     for (int j = 0; j < DC; ++j) {
-        const int row = m0 + 8 * (wave + W * j) + lr;
+        const int row = m0 + d_row(j) + lr;
         doff[j] = (uint32_t)((row < a.m ? row : a.m - 1) - m0) * (uint32_t)(2 * a.ldd) + 16u * lc;
     }
+    // W: copy j is chunks 64c .. of the tile, c = wave + W j; chunk i of row r is stored at i ^ turn_of(r), so that
+    // the 32 rows of a turned read, 16 bytes of each, fall on all banks
+    auto turn_of = [](int r) __attribute__((always_inline)) { return CPR == 16 ? r & 15 : (r >> 1 & 3) | (r >> 3 & 1) << 2; };
+    int w_row[WC];
+    uint32_t w_col[WC];
 #pragma unroll
     for (int j = 0; j < WC; ++j) {
         const int i = 64 * (wave + W * j) + lane;
-        const int col = k0 + 16 * (i % CPR);  // past the matrix: its last columns, whose results are not stored
-        woff[j] = (uint32_t)(i / CPR) * (uint32_t)a.k + (uint32_t)(col < a.k ? col : a.k - 16);
+        w_row[j] = i / CPR;
+        const int col = k0 + 16 * (i % CPR ^ turn_of(w_row[j]));  // past the matrix: its last columns, not stored
+        w_col[j] = (uint32_t)(col < a.k ? col : a.k - 16);
     }
     const uint32_t lds = f8_lds_address(f8_smem);
-    const int steps = (a.n + kGStep - 1) / kGStep;
-    const uint8_t* d0 = reinterpret_cast<const uint8_t*>(a.d + (int64_t)m0 * a.ldd);
-    auto copy = [&](int part, int term, int s, int stage) __attribute__((always_inline)) {
-        const uint8_t* db = d0 + 2 * (term * a.plane + part * a.part_cols + (int64_t)s * kGStep);
-        const uint8_t* wb = a.w + ((int64_t)part * a.n + (int64_t)s * kGStep) * a.k;
-        const uint32_t at = lds + (uint32_t)(stage * STAGE);
-        const int left = a.n - s * kGStep;  // rows of W; d has zeros from there to a multiple of eight
-        const bool cut = left < kGStep;
+    const int steps = (a.n + kGStep - 1) / kGStep, row_blocks = (a.n + 127) / 128;
+    const int64_t rows = (int64_t)a.parts * a.n;
+    const uint32_t scale_col = [&]() {  // word i of the scales: of wave column i's block
+        const int b = (k0 + 64 * (lane % WK)) / 128;
+        return 4u * (uint32_t)(b < a.kb ? b : a.kb - 1);
+    }();
+    // Where a step's operands are.  Steps are asked for in order (the last one again past the end), s of `steps`
+    // fastest, then the term, then the part; without branches, which between the products cost the large tile
+    // its registers.
+    constexpr int TERMS = kTerms<T>;
+    struct Place {
+        int step = 0, s = 0, term = 0, part = 0;
+        const uint8_t *d, *w;
+        uint32_t woff[WC];
+    };
+    const int rows_m1 = a.parts * a.n - 1;
+    // what a step adds, the first of a term more than that, the first of a part more than both
+    const int64_t d_term = 2 * a.plane - (int64_t)steps * 128, d_part = 2 * (a.part_cols - TERMS * a.plane);
+    const int64_t w_next = (int64_t)kGStep * a.k, w_term = -(int64_t)steps * w_next, w_part = (int64_t)a.n * a.k;
+    auto advance = [&](Place& p, int step) __attribute__((always_inline)) {
+        const int on = step != p.step, next = on & (p.s == steps - 1), over = next & (p.term == TERMS - 1);
+        p.step = step;
+        p.s = (p.s + on) & (next - 1);
+        p.term = (p.term + next) & (over - 1);
+        p.part += over;
+        p.d += (int64_t)128 * on + (d_term & -(int64_t)next) + (d_part & -(int64_t)over);
+        p.w += (w_next & -(int64_t)on) + (w_term & -(int64_t)next) + (w_part & -(int64_t)over);
+        const int left = rows_m1 - (p.part * a.n + p.s * kGStep);  // rows past the matrix: its last one
 #pragma unroll
-        for (int j = 0; j < DC; ++j) {
-            const uint32_t to = at + (uint32_t)(wave + W * j) * 1024;
-            if (!cut) f8_copy16(db, doff[j], to);
-            else f8_copy16_or_zeros(db, doff[j], lc * 8 < left, to);
-        }
-#pragma unroll
-        for (int j = 0; j < WC; ++j) {
-            const uint32_t to = at + (uint32_t)(BM * 2 * kGStep) + (uint32_t)(wave + W * j) * 1024;
-            if (!cut) f8_copy16(wb, woff[j], to);
-            else f8_copy16_or_zeros(wb, woff[j], (64 * (wave + W * j) + lane) / CPR < left, to);
-        }
+        for (int j = 0; j < WC; ++j) p.woff[j] = __umul24(min(+w_row[j], +left), a.k) + w_col[j];
+    };
+    auto copy_d = [&](const Place& p, int j, int to) __attribute__((always_inline)) {
+        f8_copy16(p.d, doff[j], lds + (uint32_t)(to * STAGE + d_row(j) * 128));
+    };
+    auto copy_w = [&](const Place& p, int j, int to) __attribute__((always_inline)) {
+        f8_copy16(p.w, p.woff[j], lds + (uint32_t)(to * STAGE + BM * 2 * kGStep + (wave + W * j) * 1024));
+    };
+    auto copy_scale = [&](const Place& p, int step) __attribute__((always_inline)) {
+        f8_copy4(reinterpret_cast<const uint8_t*>(a.wd + __builtin_amdgcn_readfirstlane((p.part * row_blocks + (p.s >> 1)) * a.kb)), scale_col,
+                 lds + (uint32_t)(D * STAGE + step % SCALES * 256));
     };
 
     const int l16 = lane & 15, g = lane >> 4;
     const uint32_t d_at = (uint32_t)(wm * TM * 16 + l16) * 128 + 16u * (uint32_t)(g ^ (l16 & 7));
-    const uint32_t w_at = (uint32_t)(BM * 2 * kGStep) + (uint32_t)(8 * g) * BK + (uint32_t)(wk * 128 + 8 * l16);
-    const int kblock = (k0 + wk * 128) / 128 < a.kb ? (k0 + wk * 128) / 128 : a.kb - 1;
-    const int row_blocks = (a.n + 127) / 128;
+    // a turned read's source lanes: row 8g + l16 / 2 (and 32 on), 8 bytes l16 % 2 of its 16 columns
+    const int t_row = 8 * g + (l16 >> 1);
+    const uint32_t w_at = (uint32_t)(BM * 2 * kGStep + t_row * BK + 8 * (l16 & 1)), w_turn = 16u * (uint32_t)turn_of(t_row);
+    static_assert(CPR != 16 || kGStep == 64, "rows 32 apart are stored alike");
 
-    f8_f32x4 acc[8][TM];
+    f8_f32x4 acc[4][TM];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int total = steps * a.parts * a.terms;
-    int part = 0, term = 0, s = 0, npart = 0, nterm = 0, ns = 0;
-    auto next = [&]() __attribute__((always_inline)) {  // the step after (npart, nterm, ns)
-        if (++ns == steps) {
-            ns = 0;
-            if (++nterm == a.terms) {
-                nterm = 0;
-                ++npart;
-            }
+    u32x2 raw[4][2];  // codes of a column, rows 8g .. and 32 + 8g ..
+    u32x4 av[4][2], bv[PM][2];
+    float scale = 0.f, factor = 0.f;
+    auto load = [&](int step, int h, int from) __attribute__((always_inline)) {
+        const uint8_t* at = f8_smem + from * STAGE;
+        if (h == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+                    raw[i][o] = read_turned8(at + w_at + o * 32 * BK + ((uint32_t)(64 * wk + 16 * i) ^ w_turn));
+            scale = reinterpret_cast<const float*>(f8_smem + D * STAGE)[step % SCALES * 64 + wk];
+        }
+#pragma unroll
+        for (int j = 0; j < PM; ++j) {
+            bv[j][0] = *reinterpret_cast<const u32x4*>(at + d_at + (h * PM + j) * 2048);
+            bv[j][1] = *reinterpret_cast<const u32x4*>(at + (d_at ^ 64u) + (h * PM + j) * 2048);
         }
     };
-    copy(0, 0, 0, 0);
-    wait_vmcnt_mem<0>();
-    __syncthreads();
-    for (int c = 0; c < total; ++c) {
-        const int stage = c & 1;
-        next();
-        if (c + 1 < total) copy(npart, nterm, ns, stage ^ 1);
-        const uint32_t at = (uint32_t)(stage * STAGE);
-        const float scale = f8_uniform(a.wd + (int64_t)(part * row_blocks + s / 2) * a.kb + kblock);
-        u32x2 raw[2][8];
+    auto ready = [&](int, int h) __attribute__((always_inline)) {
+        if (h) return;
+        factor = scale;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                raw[h][i] = *reinterpret_cast<const u32x2*>(f8_smem + at + w_at + (32 * h + i) * BK);
-        u32x4 b[TM][2];
+            for (int o = 0; o < 2; ++o)
+                av[i][o] = __builtin_bit_cast(u32x4, f8_widen((int)raw[i][o][0], (int)raw[i][o][1]));
+    };
+    // The sums of a fragment of columns join the accumulators while the next one's are on their way.
+    f8_f32x4 t[PM] = {};
+    auto join = [&](int h, int i, int j) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            b[j][0] = *reinterpret_cast<const u32x4*>(f8_smem + at + d_at + j * 2048);
-            b[j][1] = *reinterpret_cast<const u32x4*>(f8_smem + ((at + d_at + j * 2048) ^ 64u));
-        }
+        for (int e = 0; e < 4; ++e) acc[i][h * PM + j][e] = __builtin_fmaf(factor, t[j][e], acc[i][h * PM + j][e]);
+    };
+    auto multiply = [&](int h, auto&& side) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // columns 2q and 2q + 1 of the lane's eight
-            u32x4 av[2][2];            // [column][half of the step]
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const uint32_t v = __builtin_amdgcn_perm(raw[h][2 * p + 1][q >> 1], raw[h][2 * p][q >> 1],
-                                                             q & 1 ? 0x07030602u : 0x05010400u);
-                    av[0][h][p] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
-                    av[1][h][p] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
-                }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int o = 0; o < 2; ++o)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) {
-                    f8_f32x4 t = mfma_bf16(av[o][0], b[j][0], f8_f32x4{0.f, 0.f, 0.f, 0.f});
-                    t = mfma_bf16(av[o][1], b[j][1], t);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[2 * q + o][j][e] = __builtin_fmaf(scale, t[e], acc[2 * q + o][j][e]);
+                for (int j = 0; j < PM; ++j) {
+                    if (o == 0 && i) join(h, i - 1, j);
+                    t[j] = mfma_bf16(av[i][o], bv[j][o], o ? t[j] : f8_f32x4{0.f, 0.f, 0.f, 0.f});
+                    if (j % 2 == 1) side((i * 2 + o) * (PM / 2) + j / 2);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-        }
-        part = npart;
-        term = nterm;
-        s = ns;
-        wait_vmcnt_mem<0>();
-        __syncthreads();
-    }
-    (void)term;
+    };
+    auto finish = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < PM; ++j) join(h, 3, j);
+    };
 
-    // element e of fragment i: column 32g + 8e + i of the wave's 128
+    const int total = steps * a.parts * TERMS;
+    Place px, py;
+    px.d = py.d = reinterpret_cast<const uint8_t*>(a.d + (int64_t)m0 * a.ldd);
+    px.w = py.w = a.w;
+    if constexpr (W == 8) {
+        f8_turns<XC + 1, YC>(
+            wave >> 2, total,
+            [&](int step, int i, int to) __attribute__((always_inline)) {
+                if (i < 0) advance(px, step);
+                else if (i < WC) copy_w(px, i, to);
+                else if (i < XC) copy_d(px, i - WC, to);
+                else copy_scale(px, step);
+            },
+            [&](int step, int i, int to) __attribute__((always_inline)) {
+                if (i < 0) advance(py, step);
+                else copy_d(py, DC - YC + i, to);
+            },
+            [&](int step, int h) __attribute__((always_inline)) { load(step, h, step & 1); }, finish, ready, multiply);
+    } else {
+        f8_ring<D, WC + DC + 1>(
+            total,
+            [&](int step, int to) __attribute__((always_inline)) {
+                advance(px, step);
+#pragma unroll
+                for (int j = 0; j < WC; ++j) copy_w(px, j, to);
+#pragma unroll
+                for (int j = 0; j < DC; ++j) copy_d(px, j, to);
+                copy_scale(px, step);
+            },
+            [&](int step, int from) __attribute__((always_inline)) {
+                load(step, 0, from);
+                ready(step, 0);
+                multiply(0, [](int) {});
+                finish(0);
+            });
+    }
+
+    // element e of fragment i: column 16i + 4g + e of the wave's 64
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
         const int row = m0 + (wm * TM + j) * 16 + l16;
         if (row >= a.m) continue;
         T* out = static_cast<T*>(a.dx) + (int64_t)row * a.lddx;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int col = k0 + wk * 128 + 32 * g + 8 * e;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                f8_store4(out + col + 4 * h,
-                          f8_f32x4{acc[4 * h][j][e], acc[4 * h + 1][j][e], acc[4 * h + 2][j][e], acc[4 * h + 3][j][e]},
-                          a.k - col - 4 * h, a.vec);
+        for (int i = 0; i < 4; ++i) {
+            const int col = k0 + wk * 64 + 16 * i + 4 * g;
+            f8_store4(out + col, acc[i][j], a.k - col, a.vec);
         }
     }
 }
 
-template <int WK, int WM, int TM, class T>
+template <int WK, int WM, int TM, int D, class T>
 hipError_t launch_input_grad_tile(F8InputGradArgs a, hipStream_t stream) {
-    auto kernel = f8_input_grad_kernel<WK, WM, TM, T>;
-    constexpr size_t lds = input_grad_lds_bytes<WK, WM, TM>();
+    auto kernel = f8_input_grad_kernel<WK, WM, TM, D, T>;
+    constexpr size_t lds = input_grad_lds_bytes<WK, WM, TM, D>();
     static thread_local uint64_t allowed = 0;
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
     if (e != hipSuccess) return e;
     a.m_tiles = (a.m + WM * TM * 16 - 1) / (WM * TM * 16);
-    a.k_tiles = (a.k + WK * 128 - 1) / (WK * 128);
+    a.k_tiles = (a.k + WK * 64 - 1) / (WK * 64);
     const int64_t tiles = (int64_t)a.m_tiles * a.k_tiles;
     if (f8_grid(tiles) * (64 * WK * WM) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WM), lds, stream, a);
@@ -350,28 +435,32 @@ hipError_t launch_input_grad_tile(F8InputGradArgs a, hipStream_t stream) {
 struct F8WeightGradArgs {
     const uint16_t* d;
     int64_t d_plane, ldd, part_cols;
-    const uint16_t* x;  // planes of the inputs' values [m][k]
+    const uint16_t* x;  // planes of the inputs' values [m up to a whole step][k]
     int64_t x_plane;
     void* dw;
     int64_t lddw;
-    int n, parts, pairs, m, k;
+    int n, parts, m, k;
     int k_tiles, n_tiles;  // n_tiles: of a part
     bool vec;
 };
 
-template <int WK, int WN, int GK, int GN>
+template <int WK, int WN, int GN, int D>
 constexpr size_t weight_grad_lds_bytes() {
-    return 2 * (size_t)(WK * GK + WN * GN) * 64 * 2 * kGStep;
+    return D * (size_t)(WK + WN * GN) * 64 * 2 * kGStep;
 }
 
-// WK x WN waves, a wave 64 GK columns x 64 GN rows of dw.  A step is 64 activation rows.
-template <int WK, int WN, int GK, int GN, class T>
+// WK x WN waves, a wave 64 columns x 64 GN rows of dw.  A step is 64 activation rows; a tile's operands lie
+// in LDS as runs of 64 columns, [64 rows][128 bytes] each.
+template <int WK, int WN, int GN, int D, class T>
 __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGradArgs a) {
-    constexpr int W = WK * WN, BK = WK * GK * 64, BN = WN * GN * 64;
-    constexpr int XR = BK / 8, DR = BN / 8;  // 16-byte chunks of a row of x, of d
-    constexpr int XC = kGStep * XR / 64 / W, DC = kGStep * DR / 64 / W;
-    static_assert(kGStep * XR / 64 % W == 0 && kGStep * DR / 64 % W == 0, "copies divide evenly");
-    constexpr int STAGE = (BK + BN) * 2 * kGStep;
+    constexpr int W = WK * WN, BK = WK * 64, BN = WN * GN * 64;
+    constexpr int PARTS = W == 8 ? 2 : 1, PN = GN / PARTS;
+    constexpr int XR = WK, DR = WN * GN, RUN = 128 * kGStep;     // runs of x and of d, bytes of one
+    constexpr int XC = XR * 8 / W, DC = DR * 8 / W;              // copies of a wave: eight rows of a run each
+    constexpr int YC = W == 8 ? DC / 2 : 0, FIRST = XC + DC - YC;  // pieces of f8_turns: Y is the groups' last runs
+    static_assert(XR * 8 % W == 0 && DR * 8 % W == 0, "copies divide evenly");
+    static_assert(W != 8 || (D == 2 && WN == 2 && GN == 2), "pieces divide evenly");
+    constexpr int STAGE = (XR + DR) * RUN;
     extern __shared__ __attribute__((aligned(16))) uint8_t f8_smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -379,135 +468,165 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.k_tiles, a.n_tiles * a.parts);
     if (!tile.inside) return;  // block-uniform, before any barrier
     const int part = tile.col / a.n_tiles, n0 = (tile.col - part * a.n_tiles) * BN, k0 = tile.row * BK;
-    const int n_cols = (a.n + 7) / 8 * 8;  // columns of a part's planes
 
-    uint32_t xoff[XC], doff[DC];
+    // Copy c of an operand: rows 8(c % 8) .. of run c / 8.  The 32-byte blocks of row r are stored at
+    // block ^ turn_of(r), so that the 16 rows of a turned read, 32 bytes of each, fall on all banks.
+    auto turn_of = [](int r) __attribute__((always_inline)) { return (r >> 1 & 1) | (r >> 3 & 1) << 1; };
+    auto run_of = [&](int j) __attribute__((always_inline)) {  // d's copy j: half 0 first, then half 1 of every group
+        const int c = wave + W * (j < DC - YC ? j : j - (DC - YC));
+        return W != 8 ? c / 8 : c / 8 * GN + (j < DC - YC ? 0 : 1);
+    };
+    auto row_of = [&](int j) __attribute__((always_inline)) { return (wave + W * j) % 8 * 8 + (lane >> 3); };
+    auto chunk_of = [&](int j) __attribute__((always_inline)) { return (lane & 7) ^ turn_of(row_of(j)) << 1; };
+    uint32_t xoff[XC];
+    int dcol[DC];
 #pragma unroll
     for (int j = 0; j < XC; ++j) {
-        const int i = 64 * (wave + W * j) + lane, col = k0 + 8 * (i % XR);
-        xoff[j] = (uint32_t)(i / XR) * (uint32_t)(2 * a.k) + 2u * (uint32_t)(col < a.k ? col : a.k - 8);
+        const int at = k0 + 64 * ((wave + W * j) / 8) + 8 * chunk_of(j);  // past the matrix: its last columns, not stored
+        xoff[j] = 2u * ((uint32_t)row_of(j) * (uint32_t)a.k + (uint32_t)(at < a.k ? at : a.k - 8));
     }
 #pragma unroll
     for (int j = 0; j < DC; ++j) {
-        const int i = 64 * (wave + W * j) + lane, col = n0 + 8 * (i % DR);
-        doff[j] = (uint32_t)(i / DR) * (uint32_t)(2 * a.ldd) + 2u * (uint32_t)(col < n_cols ? col : n_cols - 8);
+        const int at = n0 + 64 * run_of(j) + 8 * chunk_of(j), columns = (a.n + 7) / 8 * 8;
+        dcol[j] = 2 * (at < columns ? at : columns - 8);
     }
     const uint32_t lds = f8_lds_address(f8_smem);
     const int steps = (a.m + kGStep - 1) / kGStep;
     // the pairs of planes whose products count: (0, 0), then (0, 1), (1, 0), then (0, 2), (1, 1), (2, 0)
     auto d_of = [](int pair) { return pair < 2 ? 0 : pair == 2 ? 1 : pair - 3; };
     auto x_of = [](int pair) { return pair < 2 ? pair : pair == 2 ? 0 : 5 - pair; };
-    auto copy = [&](int pair, int s, int stage) __attribute__((always_inline)) {
-        const uint8_t* xb = reinterpret_cast<const uint8_t*>(a.x + x_of(pair) * a.x_plane + (int64_t)s * kGStep * a.k);
-        const uint8_t* db = reinterpret_cast<const uint8_t*>(a.d + d_of(pair) * a.d_plane + part * a.part_cols +
-                                                             (int64_t)s * kGStep * a.ldd);
-        const uint32_t at = lds + (uint32_t)(stage * STAGE);
-        const int left = a.m - s * kGStep;
-        const bool cut = left < kGStep;
-#pragma unroll
-        for (int j = 0; j < XC; ++j) {
-            const uint32_t to = at + (uint32_t)(wave + W * j) * 1024;
-            if (!cut) f8_copy16(xb, xoff[j], to);
-            else f8_copy16_or_zeros(xb, xoff[j], (64 * (wave + W * j) + lane) / XR < left, to);
+    constexpr int PAIRS = kTerms<T> * (kTerms<T> + 1) / 2;
+    struct Place {
+        int step = 0, s = 0, pair = 0;
+        const uint8_t *x, *d;
+    };
+    const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.x);
+    const uint8_t* d0 = reinterpret_cast<const uint8_t*>(a.d + part * a.part_cols);
+    const int64_t x_next = (int64_t)2 * kGStep * a.k, d_next = (int64_t)2 * kGStep * a.ldd;
+    auto advance = [&](Place& p, int step) __attribute__((always_inline)) {
+        const bool on = step != p.step, next = PAIRS > 1 && on && p.s == steps - 1;
+        p.step = step;
+        p.s = next ? 0 : p.s + (on ? 1 : 0);
+        p.x += on ? x_next : 0;
+        p.d += on ? d_next : 0;
+        if constexpr (PAIRS > 1) {
+            p.pair += next ? 1 : 0;
+            p.x = next ? x0 + 2 * x_of(p.pair) * a.x_plane : p.x;
+            p.d = next ? d0 + 2 * d_of(p.pair) * a.d_plane : p.d;
         }
-#pragma unroll
-        for (int j = 0; j < DC; ++j) {
-            const uint32_t to = at + (uint32_t)(BK * 2 * kGStep) + (uint32_t)(wave + W * j) * 1024;
-            if (!cut) f8_copy16(db, doff[j], to);
-            else f8_copy16_or_zeros(db, doff[j], (64 * (wave + W * j) + lane) / DR < left, to);
-        }
+    };
+    auto copy_x = [&](const Place& p, int j, int to) __attribute__((always_inline)) {
+        f8_copy16(p.x, xoff[j], lds + (uint32_t)(to * STAGE + (wave + W * j) * 1024));
+    };
+    auto copy_d = [&](const Place& p, int j, int to) __attribute__((always_inline)) {
+        const int left = a.m - 1 - p.s * kGStep, row = row_of(j);  // rows past the operand: its last one
+        f8_copy16(p.d, 2u * __umul24(min(+row, +left), (int)a.ldd) + (uint32_t)dcol[j],
+                  lds + (uint32_t)(to * STAGE + (XR + run_of(j)) * RUN + (wave + W * j) % 8 * 1024));
     };
 
     const int l16 = lane & 15, g = lane >> 4;
-    const uint32_t x_at = (uint32_t)(8 * g) * (2 * BK) + (uint32_t)(wk * GK * 64 + 4 * l16) * 2;
-    const uint32_t d_at = (uint32_t)(BK * 2 * kGStep) + (uint32_t)(8 * g) * (2 * BN) + (uint32_t)(wn * GN * 64 + 4 * l16) * 2;
-    // fragments of four neighbouring columns a lane, 32 rows from LDS rows of ROW bytes
-    auto turn = [&](auto row_bytes, uint32_t at, u32x4 (&f)[4]) __attribute__((always_inline)) {
-        constexpr int ROW = decltype(row_bytes)::value;
-        u32x2 raw[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const u32x2*>(f8_smem + at + i * ROW);
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                f[c][p] = __builtin_amdgcn_perm(raw[2 * p + 1][c >> 1], raw[2 * p][c >> 1],
-                                                c & 1 ? 0x07060302u : 0x05040100u);
+    // a turned read's source lanes: row 8g + l16 / 4 (and 4, 32, 36 on), 8 bytes l16 % 4 of its 16 columns
+    const int t_row = 8 * g + (l16 >> 2);
+    const uint32_t lane_at = (uint32_t)(t_row * 128 + 8 * (l16 & 3)), lane_turn = 32u * (uint32_t)turn_of(t_row);
+    // fragment c (16 columns) of the run at `at`, half h of a step
+    auto fragment = [&](const uint8_t* at, int c, int h) __attribute__((always_inline)) {
+        const uint8_t* from = at + 32 * h * 128 + lane_at + ((uint32_t)(32 * c) ^ lane_turn);
+        const u32x2 lo = read_turned16(from), hi = read_turned16(from + 4 * 128);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
 
-    f8_f32x4 acc[GK][4][GN][4];
+    f8_f32x4 acc[4][GN][4];
 #pragma unroll
-    for (int i = 0; i < GK; ++i)
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < GN; ++j)
+#pragma unroll
+            for (int o = 0; o < 4; ++o) acc[c][j][o] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 fa[4][2], fb[PN][4][2];
+    auto load = [&](int h, int from) __attribute__((always_inline)) {
+        const uint8_t* at = f8_smem + from * STAGE;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int j = 0; j < GN; ++j)
+            for (int o = 0; o < 2; ++o) {
 #pragma unroll
-                for (int o = 0; o < 4; ++o) acc[i][c][j][o] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int total = steps * a.pairs;
-    int npair = 0, ns = 0;
-    copy(0, 0, 0);
-    wait_vmcnt_mem<0>();
-    __syncthreads();
-    for (int c = 0; c < total; ++c) {
-        const int stage = c & 1;
-        if (++ns == steps) {
-            ns = 0;
-            ++npair;
-        }
-        if (c + 1 < total) copy(npair, ns, stage ^ 1);
-        const uint32_t at = (uint32_t)(stage * STAGE);
+                for (int j = 0; j < PN; ++j) fb[j][c][o] = fragment(at + (XR + wn * GN + h * PN + j) * RUN, c, o);
+                if (h == 0) fa[c][o] = fragment(at + wk * RUN, c, o);
+            }
+    };
+    auto multiply = [&](int h, auto&& side) __attribute__((always_inline)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 fb[GN][4];
+        for (int j = 0; j < PN; ++j)
 #pragma unroll
-            for (int j = 0; j < GN; ++j)
-                turn(std::integral_constant<int, 2 * BN>{}, at + d_at + 128 * j + 32 * h * 2 * BN, fb[j]);
-#pragma unroll
-            for (int i = 0; i < GK; ++i) {
-                u32x4 fa[4];
-                turn(std::integral_constant<int, 2 * BK>{}, at + x_at + 128 * i + 32 * h * 2 * BK, fa);
+            for (int o = 0; o < 2; ++o)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int j = 0; j < GN; ++j)
+                    for (int v = 0; v < 4; ++v) {
+                        acc[q][h * PN + j][v] = mfma_bf16(fa[q][o], fb[j][v][o], acc[q][h * PN + j][v]);
+                        const int p = ((j * 2 + o) * 4 + q) * 4 + v;
+                        if (p % 2 == 1) side(p / 2);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+    };
+
+    const int total = steps * PAIRS;
+    Place px, py;
+    px.x = py.x = x0;
+    px.d = py.d = d0;
+    if constexpr (W == 8) {
+        f8_turns<FIRST, YC>(
+            wave >> 2, total,
+            [&](int step, int i, int to) __attribute__((always_inline)) {
+                if (i < 0) advance(px, step);
+                else if (i < XC) copy_x(px, i, to);
+                else copy_d(px, i - XC, to);
+            },
+            [&](int step, int i, int to) __attribute__((always_inline)) {
+                if (i < 0) advance(py, step);
+                else copy_d(py, DC - YC + i, to);
+            },
+            [&](int step, int h) __attribute__((always_inline)) { load(h, step & 1); }, [](int) {}, [](int, int) {}, multiply);
+    } else {
+        f8_ring<D, XC + DC>(
+            total,
+            [&](int step, int to) __attribute__((always_inline)) {
+                advance(px, step);
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) acc[i][q][j][o] = mfma_bf16(fa[q], fb[j][o], acc[i][q][j][o]);
-            }
-        }
-        wait_vmcnt_mem<0>();
-        __syncthreads();
+                for (int j = 0; j < XC; ++j) copy_x(px, j, to);
+#pragma unroll
+                for (int j = 0; j < DC; ++j) copy_d(px, j, to);
+            },
+            [&](int, int from) __attribute__((always_inline)) {
+                load(0, from);
+                multiply(0, [](int) {});
+            });
     }
 
-    // element e of fragment (i, q): column 64i + 16g + 4e + q of the wave; fragment (j, o): row 64j + 4 l16 + o
+    // element e of fragment q: column 16q + 4g + e of the wave's 64; fragment (j, v): row 64j + 16v + l16
 #pragma unroll
     for (int j = 0; j < GN; ++j)
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-            const int row = n0 + wn * GN * 64 + 64 * j + 4 * l16 + o;
+        for (int v = 0; v < 4; ++v) {
+            const int row = n0 + (wn * GN + j) * 64 + 16 * v + l16;
             if (row >= a.n) continue;
             T* out = static_cast<T*>(a.dw) + ((int64_t)part * a.n + row) * a.lddw;
 #pragma unroll
-            for (int i = 0; i < GK; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = k0 + wk * GK * 64 + 64 * i + 16 * g + 4 * e;
-                    f8_store4(out + col,
-                              f8_f32x4{acc[i][0][j][o][e], acc[i][1][j][o][e], acc[i][2][j][o][e], acc[i][3][j][o][e]},
-                              a.k - col, a.vec);
-                }
+            for (int q = 0; q < 4; ++q) {
+                const int c = k0 + wk * 64 + 16 * q + 4 * g;
+                f8_store4(out + c, acc[q][j][v], a.k - c, a.vec);
+            }
         }
 }
 
-template <int WK, int WN, int GK, int GN, class T>
+template <int WK, int WN, int GN, int D, class T>
 hipError_t launch_weight_grad_tile(F8WeightGradArgs a, hipStream_t stream) {
-    auto kernel = f8_weight_grad_kernel<WK, WN, GK, GN, T>;
-    constexpr size_t lds = weight_grad_lds_bytes<WK, WN, GK, GN>();
+    auto kernel = f8_weight_grad_kernel<WK, WN, GN, D, T>;
+    constexpr size_t lds = weight_grad_lds_bytes<WK, WN, GN, D>();
     static thread_local uint64_t allowed = 0;
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
     if (e != hipSuccess) return e;
-    constexpr int BK = WK * GK * 64, BN = WN * GN * 64;
+    constexpr int BK = WK * 64, BN = WN * GN * 64;
     a.k_tiles = (a.k + BK - 1) / BK;
     a.n_tiles = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)a.k_tiles * a.n_tiles * a.parts;
@@ -553,7 +672,7 @@ hipError_t backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, i
         hipLaunchKernelGGL(kernel, dim3(part_blocks(m * (ldp / 16))), dim3(kPartThreads), 0, stream,
                            static_cast<const T*>(gu), ldgu, static_cast<const T*>(d), ldd, m, (int)n, vec, planes, ldp);
         e = hipGetLastError();
-    } else if (TERMS == 1 && n % 8 == 0 && ldd <= (int64_t(1) << 22) && rows_aligned<T>(d, ldd, 8)) {
+    } else if (TERMS == 1 && n % kGStep == 0 && ldd <= (int64_t(1) << 22) && rows_aligned<T>(d, ldd, 8)) {
         dp = static_cast<const uint16_t*>(d);  // bf16 rows are their own plane
         ldp = ldd;
     } else {
@@ -568,25 +687,26 @@ hipError_t backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, i
         F8InputGradArgs a{};
         a.d = dp; a.plane = m * ldp; a.ldd = ldp; a.part_cols = ldp / parts;
         a.w = wq; a.wd = wd; a.dx = dx; a.lddx = lddx;
-        a.n = (int)n; a.parts = parts; a.terms = TERMS; a.m = (int)m; a.k = (int)k; a.kb = kb;
+        a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k; a.kb = kb;
         a.vec = rows_aligned<T>(dx, lddx, 4);
         const int64_t big = ((m + 255) / 256) * ((k + 255) / 256);
-        e = big >= dev.cu_count / 2 ? launch_input_grad_tile<2, 4, 4, T>(a, stream) : launch_input_grad_tile<1, 4, 1, T>(a, stream);
+        e = big >= dev.cu_count / 2 ? launch_input_grad_tile<4, 2, 8, 2, T>(a, stream) : launch_input_grad_tile<2, 2, 2, 6, T>(a, stream);
         if (e != hipSuccess) return e;
     }
     if (dw) {
+        const int64_t rows = (m + kGStep - 1) / kGStep * kGStep;
         auto kernel = f8_values_kernel<TERMS>;
-        hipLaunchKernelGGL(kernel, dim3(part_blocks(m * (k / 8))), dim3(kPartThreads), 0, stream, xq, xd, m, (int)k, kb,
-                           values);
+        hipLaunchKernelGGL(kernel, dim3(part_blocks(rows * (k / 8))), dim3(kPartThreads), 0, stream, xq, xd, m, rows,
+                           (int)k, kb, values);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         F8WeightGradArgs a{};
         a.d = dp; a.d_plane = m * ldp; a.ldd = ldp; a.part_cols = ldp / parts;
-        a.x = values; a.x_plane = m * k; a.dw = dw; a.lddw = lddw;
-        a.n = (int)n; a.parts = parts; a.pairs = TERMS * (TERMS + 1) / 2; a.m = (int)m; a.k = (int)k;
+        a.x = values; a.x_plane = rows * k; a.dw = dw; a.lddw = lddw;
+        a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k;
         a.vec = rows_aligned<T>(dw, lddw, 4);
         const int64_t big = parts * ((n + 255) / 256) * ((k + 255) / 256);
-        e = big >= dev.cu_count / 2 ? launch_weight_grad_tile<2, 4, 2, 1, T>(a, stream)
-                                    : launch_weight_grad_tile<2, 2, 1, 1, T>(a, stream);
+        e = big >= dev.cu_count / 2 ? launch_weight_grad_tile<4, 2, 2, 2, T>(a, stream)
+                                    : launch_weight_grad_tile<2, 2, 1, 4, T>(a, stream);
     }
     return e;
 }

@@ -272,31 +272,22 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
         if (whole)
             f8_turns<XC + 1, YC>(
                 wave >> 2, whole,
-                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, i < XC ? i : COPIES, to); },
-                [&](int s, int i, int to) __attribute__((always_inline)) { copy(s, XC + i, to); },
+                [&](int s, int i, int to) __attribute__((always_inline)) { if (i >= 0) copy(s, i < XC ? i : COPIES, to); },
+                [&](int s, int i, int to) __attribute__((always_inline)) { if (i >= 0) copy(s, XC + i, to); },
                 [&](int s, int h) __attribute__((always_inline)) { load_from(s, h, s & 1); }, finish, ready, multiply);
     } else {
-        // D stages: step s + D - 1 is asked for when every wave has read step s - 1, whose stage it takes
-        auto copies = [&](int s, int to) __attribute__((always_inline)) {
+        f8_ring<D, COPIES + 1>(
+            whole,
+            [&](int s, int to) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j <= COPIES; ++j) copy(s, j, to);
-        };
-#pragma unroll
-        for (int d = 0; d + 1 < D; ++d)
-            if (d < whole) copies(d, d);
-        int stage = 0, free = D - 1;
-        for (int s = 0; s < whole; ++s) {
-            f8_wait_stages<D - 2, COPIES + 1>(whole - 1 - s);
-            __syncthreads();
-            if (s + D - 1 < whole) copies(s + D - 1, free);
-            load_from(s, 0, stage);
-            ready(s, 0);
-            multiply(0, [](int) {});
-            finish(0);
-            free = stage;
-            stage = stage + 1 < D ? stage + 1 : 0;
-        }
-        __syncthreads();
+                for (int j = 0; j <= COPIES; ++j) copy(s, j, to);
+            },
+            [&](int s, int from) __attribute__((always_inline)) {
+                load_from(s, 0, from);
+                ready(s, 0);
+                multiply(0, [](int) {});
+                finish(0);
+            });
     }
     if (a.k & 127) {
         copy_cut(whole);

@@ -22,43 +22,36 @@ typedef __bf16 f8_bf16x8 __attribute__((ext_vector_type(8)));
 static __device__ const f8_i32x4 f8_zeros = {0, 0, 0, 0};
 
 // One wave-wide direct-to-LDS copy from a scalar base: lane l copies the 16 (4) bytes at
-// base + off to lds + 16*l (lds + 4*l).  base and lds are wave-uniform; M0 is saved and restored,
-// and a write of M0 needs one wait state before the copy reads it.  It counts as one
+// base + off to lds + 16*l (lds + 4*l).  base and lds are wave-uniform; a write of M0 needs one
+// wait state before the copy reads it.  M0 is left written: the compiler keeps nothing there and writes it
+// itself where an instruction of its own reads it (with M0 saved around each copy the copies between a
+// wave's products took two instructions more).  It counts as one
 // vector-memory load.
 __device__ __forceinline__ void f8_copy16(const uint8_t* base, uint32_t off, uint32_t lds) {
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %3\n\t"
+        "s_mov_b32 m0, %2\n\t"
         "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, %2\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "global_load_lds_dwordx4 %0, %1"
+        :
         : "v"(off), "s"(base), "s"(lds)
         : "memory");
 }
 __device__ __forceinline__ void f8_copy4(const uint8_t* base, uint32_t off, uint32_t lds) {
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %3\n\t"
+        "s_mov_b32 m0, %2\n\t"
         "s_nop 0\n\t"
-        "global_load_lds_dword %1, %2\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "global_load_lds_dword %0, %1"
+        :
         : "v"(off), "s"(base), "s"(lds)
         : "memory");
 }
 // Four bytes a lane from addresses of their own.
 __device__ __forceinline__ void f8_copy4_from(const float* src, uint32_t lds) {
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
+        "s_mov_b32 m0, %1\n\t"
         "s_nop 0\n\t"
-        "global_load_lds_dword %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "global_load_lds_dword %0, off"
+        :
         : "v"(src), "s"(lds)
         : "memory");
 }
@@ -66,14 +59,11 @@ __device__ __forceinline__ void f8_copy4_from(const float* src, uint32_t lds) {
 __device__ __forceinline__ void f8_copy16_or_zeros(const uint8_t* base, uint32_t off, bool valid, uint32_t lds) {
     asm volatile("" : "+v"(off));  // else the lanes' addresses are kept in registers for this one step
     const uint8_t* src = valid ? base + off : reinterpret_cast<const uint8_t*>(&f8_zeros);
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
+        "s_mov_b32 m0, %1\n\t"
         "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "global_load_lds_dwordx4 %0, off"
+        :
         : "v"(src), "s"(lds)
         : "memory");
 }
@@ -120,6 +110,26 @@ __device__ __forceinline__ void f8_wait_stages(int younger) {
     }
 }
 
+// The steps of a tile whose waves work alike, on D stages of LDS: step s + D - 1 is asked for when every wave
+// has read step s - 1, whose stage it takes.  copies(s, to): kCopies of a wave; work(s, from).  At the end
+// every copy has landed and no wave reads LDS any more.
+template <int D, int kCopies, class Copies, class Work>
+__device__ __forceinline__ void f8_ring(int steps, Copies&& copies, Work&& work) {
+#pragma unroll
+    for (int d = 0; d + 1 < D; ++d)
+        if (d < steps) copies(d, d);
+    int stage = 0, free = D - 1;
+    for (int s = 0; s < steps; ++s) {
+        f8_wait_stages<D - 2, kCopies>(steps - 1 - s);
+        __syncthreads();
+        if (s + D - 1 < steps) copies(s + D - 1, free);
+        work(s, stage);
+        free = stage;
+        stage = stage + 1 < D ? stage + 1 : 0;
+    }
+    __syncthreads();
+}
+
 // The steps of a tile of eight waves, two on a SIMD, in turns: while the waves 0 .. 3 (group 0) read
 // fragments from LDS, the waves 4 .. 7 (group 1) multiply, and the other way round, so that the matrix
 // cores of a SIMD always have one wave's products.  A turn ends with a barrier of all eight.  A step is
@@ -133,7 +143,8 @@ __device__ __forceinline__ void f8_wait_stages(int younger) {
 // that a copy has at least four turns.  (4096 rows of 8192 x 8192 in e4m3: whole stages copied again, 260 us;
 // so, 237 us; asked for in the reading turns instead, 247 us; of which the products are about 150.)
 //   x(s, i, to), i < kX, y(s, i, to), i < kY: copies of step s, into stage `to`; past the end the last
-//                        step is copied again, unread
+//                        step is copied again, unread.  i = -1 comes first, in the reading turn: what
+//                        the copies need to know (a wave's instructions between its products bound a turn)
 //   load(s, h)         : asks for the fragments of part h
 //   finish(h)          : adds up what multiply(h) left, while the other group multiplies and the
 //                        fragments of the next part are on their way
@@ -160,6 +171,8 @@ __device__ __forceinline__ void f8_turns(int group, int steps, X&& x, Y&& y, Loa
         load(s, h);
         __builtin_amdgcn_sched_barrier(0);
         finish(h ^ 1);
+        if (of == h) y_copy(s + 1 + of, -1);
+        else x_copy(s + 2, -1);
         __builtin_amdgcn_sched_barrier(0);
         wait_lgkmcnt_mem<0>();
         ready(s, h);
@@ -175,11 +188,11 @@ __device__ __forceinline__ void f8_turns(int group, int steps, X&& x, Y&& y, Loa
         f8_end_turn();
     };
 #pragma unroll
-    for (int i = 0; i < kX; ++i) x_copy(0, i);
+    for (int i = -1; i < kX; ++i) x_copy(0, i);
 #pragma unroll
-    for (int i = 0; i < kY; ++i) y_copy(0, i);
+    for (int i = -1; i < kY; ++i) y_copy(0, i);
 #pragma unroll
-    for (int i = 0; i < kX; ++i) x_copy(1, i);
+    for (int i = -1; i < kX; ++i) x_copy(1, i);
     wait_vmcnt_mem<kX + kY>();
     f8_end_turn();
     // a loop for each group: with the waits under a branch in one loop the registers do not suffice
@@ -194,7 +207,7 @@ __device__ __forceinline__ void f8_turns(int group, int steps, X&& x, Y&& y, Loa
         f8_end_turn();
     } else {
 #pragma unroll
-        for (int i = 0; i < kY; ++i) y_copy(1, i);
+        for (int i = -1; i < kY; ++i) y_copy(1, i);
         f8_end_turn();
 #pragma clang loop unroll(disable)
         for (int s = 0; s < steps; ++s) {

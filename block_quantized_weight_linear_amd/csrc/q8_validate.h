@@ -525,18 +525,20 @@ inline int f8_terms(int32_t type) { return type == Q8_F32 ? 3 : type == Q8_F16 ?
 
 // Workspace of the backward calls: the gradients of the products as planes of bf16 parts
 // [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, and the inputs as planes
-// [terms][m][k].
+// [terms][rows][k]; columns of a part and rows in whole steps of 64.
+constexpr int64_t kF8Step = 64;
 struct F8BackwardWorkspace {
     int64_t ldd;
     size_t d_off, x_off, total;
 };
 inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
     F8BackwardWorkspace w{};
-    w.ldd = parts * int64_t(round_up(size_t(n_part), 8));
+    w.ldd = parts * int64_t(round_up(size_t(n_part), kF8Step));
+    const size_t rows = round_up(size_t(m), kF8Step);
     const size_t terms = size_t(f8_terms(type));
     size_t off = 0;
     w.d_off = off; off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
-    w.x_off = off; off = round_up(off + 2 * terms * size_t(m) * size_t(k), 256);
+    w.x_off = off; off = round_up(off + 2 * terms * rows * size_t(k), 256);
     w.total = off ? off : 256;
     return w;
 }
