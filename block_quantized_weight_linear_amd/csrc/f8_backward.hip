@@ -105,68 +105,81 @@ __device__ __forceinline__ void store_parts(uint16_t* at, int64_t plane, const f
     }
 }
 
-// The planes of a gradient [m][n].
-template <class T, int TERMS>
-__global__ __launch_bounds__(kPartThreads) void f8_split_kernel(const T* __restrict__ d, int64_t m, int n, int64_t ldd,
-                                                               bool vec, uint16_t* __restrict__ out, int64_t ldo) {
-    const int64_t per_row = ldo / 8, total = m * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
-        const int64_t row = i / per_row, col = 8 * (i - row * per_row);
-        float v[8];
-        load_row8(d + row * ldd, col, n, vec, v);
-        store_parts<TERMS>(out + row * ldo + col, m * ldo, v);
-    }
-}
+// What the products read, in one launch: the gradient's planes by the first blocks, the inputs' by the others.
+struct F8PlanesArgs {
+    const void* d;    // the call's gradient [m][n]; kind kNoPlanes: it is its own plane
+    const void* gu;   // kind kBehindSilu: gate and up products [m][2n]
+    const uint8_t* q;  // codes and scales of the inputs
+    const float* xd;
+    uint16_t *planes, *values;
+    int64_t ldd, ldgu, ldo, m, rows;  // rows: of the values, zeros from m on
+    int n, k, kb;
+    unsigned d_blocks;
+    bool vec;
+};
+enum { kNoPlanes, kSplit, kBehindSilu };
 
-// The planes of the gate's and up's gradients, [m][dg | du]; each a value of type T.
-template <class T, int TERMS>
-__global__ __launch_bounds__(kPartThreads) void f8_gate_up_gradient_kernel(const T* __restrict__ gu, int64_t ldgu,
-                                                                          const T* __restrict__ dh, int64_t lddh,
-                                                                          int64_t m, int f, bool vec,
-                                                                          uint16_t* __restrict__ out, int64_t ldo) {
-    const int64_t per_row = ldo / 16, total = m * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
+template <class T, int TERMS, int KIND>
+__device__ __forceinline__ void f8_gradient_planes(const F8PlanesArgs& a, int64_t first, int64_t step) {
+    const int64_t per_row = a.ldo / (KIND == kBehindSilu ? 16 : 8), total = a.m * per_row;
+    const T* d = static_cast<const T*>(a.d);
+    const T* gu = static_cast<const T*>(a.gu);
+    for (int64_t i = first; i < total; i += step) {
         const int64_t row = i / per_row, col = 8 * (i - row * per_row);
-        float g[8], u[8], h[8], dg[8], du[8];
-        load_row8(gu + row * ldgu, col, f, vec, g);
-        load_row8(gu + row * ldgu + f, col, f, vec && f % 8 == 0, u);
-        load_row8(dh + row * lddh, col, f, vec, h);
+        uint16_t* at = a.planes + row * a.ldo + col;
+        float h[8];
+        load_row8(d + row * a.ldd, col, a.n, a.vec, h);
+        if constexpr (KIND == kSplit) {
+            store_parts<TERMS>(at, a.m * a.ldo, h);
+        } else {
+            // the gate's and up's gradients beside each other, each a value of type T
+            float g[8], u[8], dg[8], du[8];
+            load_row8(gu + row * a.ldgu, col, a.n, a.vec, g);
+            load_row8(gu + row * a.ldgu + a.n, col, a.n, a.vec && a.n % 8 == 0, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float s = 1.0f / (1.0f + __expf(-g[e]));
-            dg[e] = (float)f8_round<T>(h[e] * u[e] * (s * (1.0f + g[e] * (1.0f - s))));
-            du[e] = (float)f8_round<T>(h[e] * (g[e] * s));
+            for (int e = 0; e < 8; ++e) {
+                const float s = 1.0f / (1.0f + __expf(-g[e]));
+                dg[e] = (float)f8_round<T>(h[e] * u[e] * (s * (1.0f + g[e] * (1.0f - s))));
+                du[e] = (float)f8_round<T>(h[e] * (g[e] * s));
+            }
+            store_parts<TERMS>(at, a.m * a.ldo, dg);
+            store_parts<TERMS>(at + a.ldo / 2, a.m * a.ldo, du);
         }
-        uint16_t* at = out + row * ldo + col;
-        store_parts<TERMS>(at, m * ldo, dg);
-        store_parts<TERMS>(at + ldo / 2, m * ldo, du);
     }
 }
 
-// The planes of the inputs' values [m][k], rows from m to `rows` zeros.
 template <int TERMS>
-__global__ __launch_bounds__(kPartThreads) void f8_values_kernel(const uint8_t* __restrict__ q,
-                                                                const float* __restrict__ d, int64_t m, int64_t rows,
-                                                                int k, int kb, uint16_t* __restrict__ out) {
-    const int64_t per_row = k / 8, total = rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
+__device__ __forceinline__ void f8_input_planes(const F8PlanesArgs& a, int64_t first, int64_t step) {
+    const int64_t per_row = a.k / 8, total = a.rows * per_row;
+    for (int64_t i = first; i < total; i += step) {
         const int64_t row = i / per_row, col = 8 * (i - row * per_row);
         float v[8] = {};
-        if (row >= m) {
-            store_parts<TERMS>(out + row * k + col, rows * k, v);
-            continue;
-        }
-        const u32x2 c = *reinterpret_cast<const u32x2*>(q + row * k + col);
-        const float s = d[row * kb + col / 128];
+        if (row < a.m) {
+            const u32x2 c = *reinterpret_cast<const u32x2*>(a.q + row * a.k + col);
+            const float s = a.xd[row * a.kb + col / 128];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 0) * s;
-            v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 1) * s;
-            v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 2) * s;
-            v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 3) * s;
+            for (int h = 0; h < 2; ++h) {
+                v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 0) * s;
+                v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 1) * s;
+                v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 2) * s;
+                v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 3) * s;
+            }
         }
-        store_parts<TERMS>(out + row * k + col, rows * k, v);
+        store_parts<TERMS>(a.values + row * a.k + col, a.rows * a.k, v);
     }
+}
+
+template <class T, int TERMS, int KIND>
+__global__ __launch_bounds__(kPartThreads) void f8_planes_kernel(F8PlanesArgs a) {
+    if constexpr (KIND != kNoPlanes) {
+        if (blockIdx.x < a.d_blocks) {
+            f8_gradient_planes<T, TERMS, KIND>(a, (int64_t)blockIdx.x * kPartThreads + threadIdx.x,
+                                               (int64_t)a.d_blocks * kPartThreads);
+            return;
+        }
+    }
+    f8_input_planes<TERMS>(a, (int64_t)(blockIdx.x - a.d_blocks) * kPartThreads + threadIdx.x,
+                           (int64_t)(gridDim.x - a.d_blocks) * kPartThreads);
 }
 
 template <class T>
@@ -175,6 +188,20 @@ __global__ __launch_bounds__(kPartThreads) void f8_zero_rows_kernel(T* __restric
     const int64_t total = rows * cols;
     for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads)
         out[i / cols * ld + i % cols] = (T)0.f;
+}
+
+// Results of ranges [ranges][rows][k] added in their order.
+template <class T>
+__global__ __launch_bounds__(kPartThreads) void f8_add_ranges_kernel(const float* __restrict__ sums, int ranges, int64_t rows,
+                                                                    int k, T* __restrict__ out, int64_t ld, bool vec) {
+    const int64_t per_row = k / 4, total = rows * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
+        const int64_t row = i / per_row, col = 4 * (i - row * per_row);
+        const float* at = sums + row * k + col;
+        f8_f32x4 v = *reinterpret_cast<const f8_f32x4*>(at);
+        for (int r = 1; r < ranges; ++r) v += *reinterpret_cast<const f8_f32x4*>(at + r * rows * k);
+        f8_store4(out + row * ld + col, v, 4, vec);
+    }
 }
 
 unsigned part_blocks(int64_t threads) {
@@ -197,6 +224,8 @@ struct F8InputGradArgs {
     int64_t lddx;
     int n, parts, m, k, kb;
     int m_tiles, k_tiles;
+    int ranges, range_steps;  // of the sum; a range's results go range_stride elements behind the one's before
+    int64_t range_stride;
     bool vec;
 };
 
@@ -212,7 +241,8 @@ constexpr size_t input_grad_lds_bytes() {
 
 // WK x WM waves, a wave 64 columns of dx (four fragments) x 16 TM rows.  A step is 64 rows of W, all in one
 // block of its scales: the step's sums start at zero and join the accumulators times the scale.
-template <int WK, int WM, int TM, int D, class T>
+// T: the gradients' type, O: the results'.
+template <int WK, int WM, int TM, int D, class T, class O>
 __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGradArgs a) {
     constexpr int W = WK * WM, BK = WK * 64, BM = WM * TM * 16;
     constexpr int PARTS = W == 8 ? 2 : 1, PM = TM / PARTS;
@@ -227,9 +257,10 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wm = wave / WK;
-    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.m_tiles, a.k_tiles);
+    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.m_tiles, a.k_tiles * a.ranges);
     if (!tile.inside) return;  // block-uniform, before any barrier
-    const int m0 = tile.row * BM, k0 = tile.col * BK;
+    const int range = tile.col / a.k_tiles;
+    const int m0 = tile.row * BM, k0 = (tile.col - range * a.k_tiles) * BK;
 
     // d: copy j is rows r .. r + 7 of the tile, r = d_row(j), chunks as in the forward tiles
     const int lr = lane >> 3, lc = (lane & 7) ^ lr;
@@ -364,10 +395,15 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
         for (int j = 0; j < PM; ++j) join(h, 3, j);
     };
 
-    const int total = steps * a.parts * TERMS;
-    Place px, py;
-    px.d = py.d = reinterpret_cast<const uint8_t*>(a.d + (int64_t)m0 * a.ldd);
-    px.w = py.w = a.w;
+    const int all = steps * a.parts * TERMS, begin = range * a.range_steps;
+    const int total = all - begin < a.range_steps ? all - begin : a.range_steps;  // steps of this range
+    Place px;
+    px.s = begin % steps;
+    px.term = begin / steps % TERMS;
+    px.part = begin / steps / TERMS;
+    px.d = reinterpret_cast<const uint8_t*>(a.d + (int64_t)m0 * a.ldd + px.part * a.part_cols + px.term * a.plane) + px.s * 128;
+    px.w = a.w + px.part * ((int64_t)a.n * a.k) + px.s * w_next;
+    Place py = px;
     if constexpr (W == 8) {
         f8_turns<XC + 1, YC>(
             wave >> 2, total,
@@ -406,7 +442,7 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
     for (int j = 0; j < TM; ++j) {
         const int row = m0 + (wm * TM + j) * 16 + l16;
         if (row >= a.m) continue;
-        T* out = static_cast<T*>(a.dx) + (int64_t)row * a.lddx;
+        O* out = static_cast<O*>(a.dx) + range * a.range_stride + (int64_t)row * a.lddx;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int col = k0 + wk * 64 + 16 * i + 4 * g;
@@ -415,16 +451,16 @@ __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGrad
     }
 }
 
-template <int WK, int WM, int TM, int D, class T>
+template <int WK, int WM, int TM, int D, class T, class O = T>
 hipError_t launch_input_grad_tile(F8InputGradArgs a, hipStream_t stream) {
-    auto kernel = f8_input_grad_kernel<WK, WM, TM, D, T>;
+    auto kernel = f8_input_grad_kernel<WK, WM, TM, D, T, O>;
     constexpr size_t lds = input_grad_lds_bytes<WK, WM, TM, D>();
     static thread_local uint64_t allowed = 0;
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
     if (e != hipSuccess) return e;
     a.m_tiles = (a.m + WM * TM * 16 - 1) / (WM * TM * 16);
     a.k_tiles = (a.k + WK * 64 - 1) / (WK * 64);
-    const int64_t tiles = (int64_t)a.m_tiles * a.k_tiles;
+    const int64_t tiles = (int64_t)a.m_tiles * a.k_tiles * a.ranges;
     if (f8_grid(tiles) * (64 * WK * WM) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WM), lds, stream, a);
     return hipGetLastError();
@@ -441,6 +477,8 @@ struct F8WeightGradArgs {
     int64_t lddw;
     int n, parts, m, k;
     int k_tiles, n_tiles;  // n_tiles: of a part
+    int ranges, range_steps;
+    int64_t range_stride;
     bool vec;
 };
 
@@ -451,7 +489,7 @@ constexpr size_t weight_grad_lds_bytes() {
 
 // WK x WN waves, a wave 64 columns x 64 GN rows of dw.  A step is 64 activation rows; a tile's operands lie
 // in LDS as runs of 64 columns, [64 rows][128 bytes] each.
-template <int WK, int WN, int GN, int D, class T>
+template <int WK, int WN, int GN, int D, class T, class O>
 __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGradArgs a) {
     constexpr int W = WK * WN, BK = WK * 64, BN = WN * GN * 64;
     constexpr int PARTS = W == 8 ? 2 : 1, PN = GN / PARTS;
@@ -465,9 +503,10 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wn = wave / WK;
-    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.k_tiles, a.n_tiles * a.parts);
+    const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.k_tiles, a.n_tiles * a.parts * a.ranges);
     if (!tile.inside) return;  // block-uniform, before any barrier
-    const int part = tile.col / a.n_tiles, n0 = (tile.col - part * a.n_tiles) * BN, k0 = tile.row * BK;
+    const int range = tile.col / (a.n_tiles * a.parts), col = tile.col - range * (a.n_tiles * a.parts);
+    const int part = col / a.n_tiles, n0 = (col - part * a.n_tiles) * BN, k0 = tile.row * BK;
 
     // Copy c of an operand: rows 8(c % 8) .. of run c / 8.  The 32-byte blocks of row r are stored at
     // block ^ turn_of(r), so that the 16 rows of a turned read, 32 bytes of each, fall on all banks.
@@ -570,10 +609,14 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
                     }
     };
 
-    const int total = steps * PAIRS;
-    Place px, py;
-    px.x = py.x = x0;
-    px.d = py.d = d0;
+    const int all = steps * PAIRS, begin = range * a.range_steps;
+    const int total = all - begin < a.range_steps ? all - begin : a.range_steps;  // steps of this range
+    Place px;
+    px.s = begin % steps;
+    px.pair = begin / steps;
+    px.x = x0 + 2 * x_of(px.pair) * a.x_plane + px.s * x_next;
+    px.d = d0 + 2 * d_of(px.pair) * a.d_plane + px.s * d_next;
+    Place py = px;
     if constexpr (W == 8) {
         f8_turns<FIRST, YC>(
             wave >> 2, total,
@@ -610,7 +653,7 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
         for (int v = 0; v < 4; ++v) {
             const int row = n0 + (wn * GN + j) * 64 + 16 * v + l16;
             if (row >= a.n) continue;
-            T* out = static_cast<T*>(a.dw) + ((int64_t)part * a.n + row) * a.lddw;
+            O* out = static_cast<O*>(a.dw) + range * a.range_stride + ((int64_t)part * a.n + row) * a.lddw;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = k0 + wk * 64 + 16 * q + 4 * g;
@@ -619,9 +662,9 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
         }
 }
 
-template <int WK, int WN, int GN, int D, class T>
+template <int WK, int WN, int GN, int D, class T, class O = T>
 hipError_t launch_weight_grad_tile(F8WeightGradArgs a, hipStream_t stream) {
-    auto kernel = f8_weight_grad_kernel<WK, WN, GN, D, T>;
+    auto kernel = f8_weight_grad_kernel<WK, WN, GN, D, T, O>;
     constexpr size_t lds = weight_grad_lds_bytes<WK, WN, GN, D>();
     static thread_local uint64_t allowed = 0;
     const hipError_t e = f8_allow_lds(kernel, lds, &allowed);
@@ -629,7 +672,7 @@ hipError_t launch_weight_grad_tile(F8WeightGradArgs a, hipStream_t stream) {
     constexpr int BK = WK * 64, BN = WN * GN * 64;
     a.k_tiles = (a.k + BK - 1) / BK;
     a.n_tiles = (a.n + BN - 1) / BN;
-    const int64_t tiles = (int64_t)a.k_tiles * a.n_tiles * a.parts;
+    const int64_t tiles = (int64_t)a.k_tiles * a.n_tiles * a.parts * a.ranges;
     if (f8_grid(tiles) * (64 * WK * WN) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WN), lds, stream, a);
     return hipGetLastError();
@@ -650,8 +693,15 @@ hipError_t zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, hipStrea
     return hipGetLastError();
 }
 
+template <class T>
+hipError_t add_ranges(const float* sums, int ranges, int64_t rows, int64_t k, void* out, int64_t ld, hipStream_t stream) {
+    hipLaunchKernelGGL(f8_add_ranges_kernel<T>, dim3(part_blocks(rows * (k / 4))), dim3(kPartThreads), 0, stream, sums,
+                       ranges, rows, (int)k, static_cast<T*>(out), ld, rows_aligned<T>(out, ld, 4));
+    return hipGetLastError();
+}
+
 template <class T, int TERMS>
-hipError_t backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, int64_t n, int parts, int64_t k,
+hipError_t backward(const uint8_t* wq, const float* wd, int64_t n, int parts, int64_t k,
                     const uint8_t* xq, const float* xd, int64_t m, const void* gu, int64_t ldgu, const void* d,
                     int type, int64_t ldd, void* dx, int64_t lddx, void* dw, int64_t lddw, void* workspace,
                     hipStream_t stream) {
@@ -661,27 +711,32 @@ hipError_t backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, i
     uint8_t* base = static_cast<uint8_t*>(workspace);
     uint16_t* planes = reinterpret_cast<uint16_t*>(base + ws.d_off);
     uint16_t* values = reinterpret_cast<uint16_t*>(base + ws.x_off);
+    float* sums = reinterpret_cast<float*>(base + ws.sums_off);
     const int kb = (int)((k + 127) / 128);
     hipError_t e = hipSuccess;
 
+    F8PlanesArgs p{};
+    p.d = d; p.gu = gu; p.q = xq; p.xd = xd; p.planes = planes; p.values = values;
+    p.ldd = ldd; p.ldgu = ldgu; p.ldo = ws.ldd; p.m = m; p.rows = (m + kGStep - 1) / kGStep * kGStep;
+    p.n = (int)n; p.k = (int)k; p.kb = kb;
+    p.vec = rows_aligned<T>(d, ldd, 8) && (parts == 1 || rows_aligned<T>(gu, ldgu, 8));
     const uint16_t* dp = planes;
     int64_t ldp = ws.ldd;
-    if (parts == 2) {
-        const bool vec = rows_aligned<T>(gu, ldgu, 8) && rows_aligned<T>(d, ldd, 8);
-        auto kernel = f8_gate_up_gradient_kernel<T, TERMS>;
-        hipLaunchKernelGGL(kernel, dim3(part_blocks(m * (ldp / 16))), dim3(kPartThreads), 0, stream,
-                           static_cast<const T*>(gu), ldgu, static_cast<const T*>(d), ldd, m, (int)n, vec, planes, ldp);
-        e = hipGetLastError();
-    } else if (TERMS == 1 && n % kGStep == 0 && ldd <= (int64_t(1) << 22) && rows_aligned<T>(d, ldd, 8)) {
+    int kind = parts == 2 ? kBehindSilu : kSplit;
+    if (parts == 1 && TERMS == 1 && n % kGStep == 0 && ldd <= (int64_t(1) << 22) && rows_aligned<T>(d, ldd, 8)) {
         dp = static_cast<const uint16_t*>(d);  // bf16 rows are their own plane
         ldp = ldd;
-    } else {
-        auto kernel = f8_split_kernel<T, TERMS>;
-        hipLaunchKernelGGL(kernel, dim3(part_blocks(m * (ldp / 8))), dim3(kPartThreads), 0, stream,
-                           static_cast<const T*>(d), m, (int)n, ldd, rows_aligned<T>(d, ldd, 8), planes, ldp);
-        e = hipGetLastError();
+        kind = kNoPlanes;
     }
-    if (e != hipSuccess) return e;
+    p.d_blocks = kind == kNoPlanes ? 0 : part_blocks(m * (ws.ldd / (parts == 2 ? 16 : 8)));
+    const unsigned blocks = p.d_blocks + (dw ? part_blocks(p.rows * (k / 8)) : 0);
+    if (blocks) {
+        auto kernel = kind == kNoPlanes ? f8_planes_kernel<T, TERMS, kNoPlanes>
+                      : kind == kSplit  ? f8_planes_kernel<T, TERMS, kSplit>
+                                        : f8_planes_kernel<T, TERMS, kBehindSilu>;
+        hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kPartThreads), 0, stream, p);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
 
     if (dx) {
         F8InputGradArgs a{};
@@ -689,43 +744,55 @@ hipError_t backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, i
         a.w = wq; a.wd = wd; a.dx = dx; a.lddx = lddx;
         a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k; a.kb = kb;
         a.vec = rows_aligned<T>(dx, lddx, 4);
-        const int64_t big = ((m + 255) / 256) * ((k + 255) / 256);
-        e = big >= dev.cu_count / 2 ? launch_input_grad_tile<4, 2, 8, 2, T>(a, stream) : launch_input_grad_tile<2, 2, 2, 6, T>(a, stream);
+        const q8v::F8GradPlan plan = q8v::f8_dx_plan(m, n, parts, k, type);
+        const int64_t steps = parts * TERMS * ((n + kGStep - 1) / kGStep);
+        a.range_steps = (int)((steps + plan.ranges - 1) / plan.ranges);
+        a.ranges = (int)((steps + a.range_steps - 1) / a.range_steps);
+        if (a.ranges > 1) {
+            a.dx = sums; a.lddx = k; a.vec = true; a.range_stride = m * k;
+            if ((e = launch_input_grad_tile<2, 2, 2, 6, T, float>(a, stream)) != hipSuccess) return e;
+            e = add_ranges<T>(sums, a.ranges, m, k, dx, lddx, stream);
+        } else {
+            e = plan.big ? launch_input_grad_tile<4, 2, 8, 2, T>(a, stream) : launch_input_grad_tile<2, 2, 2, 6, T>(a, stream);
+        }
         if (e != hipSuccess) return e;
     }
     if (dw) {
-        const int64_t rows = (m + kGStep - 1) / kGStep * kGStep;
-        auto kernel = f8_values_kernel<TERMS>;
-        hipLaunchKernelGGL(kernel, dim3(part_blocks(rows * (k / 8))), dim3(kPartThreads), 0, stream, xq, xd, m, rows,
-                           (int)k, kb, values);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
         F8WeightGradArgs a{};
         a.d = dp; a.d_plane = m * ldp; a.ldd = ldp; a.part_cols = ldp / parts;
-        a.x = values; a.x_plane = rows * k; a.dw = dw; a.lddw = lddw;
+        a.x = values; a.x_plane = p.rows * k; a.dw = dw; a.lddw = lddw;
         a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k;
         a.vec = rows_aligned<T>(dw, lddw, 4);
-        const int64_t big = parts * ((n + 255) / 256) * ((k + 255) / 256);
-        e = big >= dev.cu_count / 2 ? launch_weight_grad_tile<4, 2, 2, 2, T>(a, stream)
-                                    : launch_weight_grad_tile<2, 2, 1, 4, T>(a, stream);
+        const q8v::F8GradPlan plan = q8v::f8_dw_plan(m, n, parts, k, type);
+        const int64_t steps = TERMS * (TERMS + 1) / 2 * (p.rows / kGStep);
+        a.range_steps = (int)((steps + plan.ranges - 1) / plan.ranges);
+        a.ranges = (int)((steps + a.range_steps - 1) / a.range_steps);
+        if (a.ranges > 1) {
+            a.dw = sums; a.lddw = k; a.vec = true; a.range_stride = parts * n * k;
+            if ((e = launch_weight_grad_tile<2, 2, 1, 4, T, float>(a, stream)) != hipSuccess) return e;
+            e = add_ranges<T>(sums, a.ranges, parts * n, k, dw, lddw, stream);
+        } else {
+            e = plan.big ? launch_weight_grad_tile<4, 2, 2, 2, T>(a, stream) : launch_weight_grad_tile<2, 2, 1, 4, T>(a, stream);
+        }
     }
     return e;
 }
 
 }  // namespace
 
-hipError_t launch_f8_backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, int64_t n, int parts,
+hipError_t launch_f8_backward(const uint8_t* wq, const float* wd, int64_t n, int parts,
                               int64_t k, const uint8_t* xq, const float* xd, int64_t m, const void* gu, int64_t ldgu,
                               const void* d, int type, int64_t ldd, void* dx, int64_t lddx, void* dw, int64_t lddw,
                               void* workspace, hipStream_t stream) {
     switch (type) {
         case Q8_F32:
-            return backward<float, 3>(dev, wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
+            return backward<float, 3>(wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
                                       workspace, stream);
         case Q8_F16:
-            return backward<_Float16, 2>(dev, wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw,
+            return backward<_Float16, 2>(wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw,
                                          lddw, workspace, stream);
         default:
-            return backward<__bf16, 1>(dev, wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
+            return backward<__bf16, 1>(wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
                                        workspace, stream);
     }
 }

@@ -584,10 +584,7 @@ static q8_status f8_backward_common(const char* name, int parts, const uint8_t* 
         return s;
     }
     if ((!dx && !dw) || (m == 0 && n == 0)) return Q8_OK;
-    q8k::DeviceInfo dev;
-    hipError_t e = q8k::current_device_info(&dev);
-    if (e != hipSuccess) return device_fail(name, e);
-    e = q8k::launch_f8_backward(dev, wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
+    const hipError_t e = q8k::launch_f8_backward(wq, wd, n, parts, k, xq, xd, m, gu, ldgu, d, type, ldd, dx, lddx, dw, lddw,
                                 workspace, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return device_fail(name, e);
     return Q8_OK;

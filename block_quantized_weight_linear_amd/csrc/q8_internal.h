@@ -99,7 +99,7 @@ hipError_t launch_f8_linear(const DeviceInfo& dev, const uint8_t* wq, const floa
                             void* gu, int64_t ldgu, hipStream_t stream);
 // dx and dw (either may be NULL) of a matrix of `parts` parts of n rows; parts == 2: d is the
 // gradient of SiLU(gate) * up, gu the two products.  Workspace laid out by q8v::f8_backward_layout.
-hipError_t launch_f8_backward(const DeviceInfo& dev, const uint8_t* wq, const float* wd, int64_t n, int parts,
+hipError_t launch_f8_backward(const uint8_t* wq, const float* wd, int64_t n, int parts,
                               int64_t k, const uint8_t* xq, const float* xd, int64_t m, const void* gu, int64_t ldgu,
                               const void* d, int type, int64_t ldd, void* dx, int64_t lddx, void* dw, int64_t lddw,
                               void* workspace, hipStream_t stream);

@@ -523,22 +523,55 @@ inline q8_status check_f8_linear(const void* wq, const void* wd, int64_t n_out, 
 // products the weights' gradient adds.
 inline int f8_terms(int32_t type) { return type == Q8_F32 ? 3 : type == Q8_F16 ? 2 : 1; }
 
-// Workspace of the backward calls: the gradients of the products as planes of bf16 parts
-// [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, and the inputs as planes
-// [terms][rows][k]; columns of a part and rows in whole steps of 64.
+// How a gradient's product runs: on tiles of 256 x 256 where they fill half of the device, else on tiles of
+// `rows` x 128 whose sums, if the tiles are few, are cut into ranges that run beside each other and are
+// added behind (at least four steps of 64 terms each).  Measured, in us, float32 gradients of 2001 x 1040 at 77
+// rows, 18 tiles: dx in one range 65.6, in 14 ranges 10.4 and 5.0 to add them.
 constexpr int64_t kF8Step = 64;
+constexpr int64_t kF8Cus = 256;  // workgroups that a device runs at once, one a CU
+constexpr int64_t kF8MaxRanges = 16;
+struct F8GradPlan {
+    bool big;
+    int64_t ranges;
+};
+inline F8GradPlan f8_grad_plan(int64_t rows, int64_t parts, int64_t cols, int64_t tile_rows, int64_t steps) {
+    F8GradPlan p{parts * ((rows + 255) / 256) * ((cols + 255) / 256) >= kF8Cus / 2, 1};
+    if (p.big || rows == 0) return p;  // no rows: nothing runs
+    const int64_t tiles = parts * ((rows + tile_rows - 1) / tile_rows) * ((cols + 127) / 128);
+    p.ranges = kF8Cus / tiles;
+    if (p.ranges > steps / 4) p.ranges = steps / 4;
+    if (p.ranges > kF8MaxRanges) p.ranges = kF8MaxRanges;
+    if (p.ranges < 1) p.ranges = 1;
+    return p;
+}
+inline F8GradPlan f8_dx_plan(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
+    return f8_grad_plan(m, 1, k, 64, parts * f8_terms(type) * ((n_part + kF8Step - 1) / kF8Step));
+}
+inline F8GradPlan f8_dw_plan(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
+    const int64_t pairs = f8_terms(type) * (f8_terms(type) + 1) / 2;
+    return f8_grad_plan(n_part, parts, k, 128, pairs * ((m + kF8Step - 1) / kF8Step));
+}
+
+// Workspace of the backward calls: the gradients of the products as planes of bf16 parts
+// [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, the inputs as planes
+// [terms][rows][k] (columns of a part and rows in whole steps), and the ranges' sums of dx, then of dw.
 struct F8BackwardWorkspace {
     int64_t ldd;
-    size_t d_off, x_off, total;
+    size_t d_off, x_off, sums_off, total;
 };
 inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
     F8BackwardWorkspace w{};
     w.ldd = parts * int64_t(round_up(size_t(n_part), kF8Step));
     const size_t rows = round_up(size_t(m), kF8Step);
     const size_t terms = size_t(f8_terms(type));
+    const size_t dx_ranges = size_t(f8_dx_plan(m, n_part, parts, k, type).ranges);
+    const size_t dw_ranges = size_t(f8_dw_plan(m, n_part, parts, k, type).ranges);
+    const size_t dx_sums = dx_ranges > 1 ? dx_ranges * size_t(m) * size_t(k) : 0;
+    const size_t dw_sums = dw_ranges > 1 ? dw_ranges * size_t(parts * n_part) * size_t(k) : 0;
     size_t off = 0;
-    w.d_off = off; off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
-    w.x_off = off; off = round_up(off + 2 * terms * rows * size_t(k), 256);
+    w.d_off = off;    off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
+    w.x_off = off;    off = round_up(off + 2 * terms * rows * size_t(k), 256);
+    w.sums_off = off; off = round_up(off + sizeof(float) * (dx_sums > dw_sums ? dx_sums : dw_sums), 256);
     w.total = off ? off : 256;
     return w;
 }

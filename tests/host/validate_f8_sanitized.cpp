@@ -75,7 +75,19 @@ int main() {
                 const F8BackwardWorkspace w = f8_backward_layout(7, 21, parts, 144, type);
                 EXPECT(w.ldd, 64 * parts);
                 EXPECT(w.x_off >= w.d_off + size_t(2 * f8_terms(type) * 7) * size_t(w.ldd), 1);
-                EXPECT(w.total >= w.x_off + size_t(2 * f8_terms(type) * 64 * 144), 1);
+                EXPECT(w.sums_off >= w.x_off + size_t(2 * f8_terms(type) * 64 * 144), 1);
+                EXPECT(w.total >= w.sums_off, 1);
+                // ranges are whole and leave room for their sums
+                for (int64_t m : {int64_t(0), int64_t(1), int64_t(64), int64_t(77), int64_t(1000), int64_t(1) << 14})
+                    for (int64_t n : {int64_t(0), int64_t(1), int64_t(300), int64_t(2001), int64_t(1) << 15})
+                        for (int64_t k : {int64_t(16), int64_t(1040), int64_t(1) << 14}) {
+                            const F8GradPlan dx = f8_dx_plan(m, n, parts, k, type), dw = f8_dw_plan(m, n, parts, k, type);
+                            const F8BackwardWorkspace l = f8_backward_layout(m, n, parts, k, type);
+                            EXPECT(dx.ranges >= 1 && dx.ranges <= kF8MaxRanges && (!dx.big || dx.ranges == 1), 1);
+                            EXPECT(dw.ranges >= 1 && dw.ranges <= kF8MaxRanges && (!dw.big || dw.ranges == 1), 1);
+                            if (dx.ranges > 1) EXPECT(l.total - l.sums_off >= size_t(4 * dx.ranges * m * k), 1);
+                            if (dw.ranges > 1) EXPECT(l.total - l.sums_off >= size_t(4 * dw.ranges * parts * n * k), 1);
+                        }
                 // the largest sizes stay within 64 bits
                 EXPECT(f8_backward_workspace_bytes(int64_t(1) << 17, kF8MaxDim / parts, parts, int64_t(1) << 17, type) >
                            (size_t(1) << 38), 1);
