@@ -24,7 +24,6 @@
 #include <stdint.h>
 
 #include <type_traits>
-#include <utility>
 
 #include "f8_tile.h"
 #include "q8_internal.h"

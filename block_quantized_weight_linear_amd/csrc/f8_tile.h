@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include <type_traits>
-#include <utility>
 
 #include "lds_dma.h"
 
@@ -70,13 +69,6 @@ __device__ __forceinline__ void f8_copy16_or_zeros(const uint8_t* base, uint32_t
 
 __device__ __forceinline__ uint32_t f8_lds_address(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
-}
-
-// A float that no kernel of the launch writes, read through the scalar cache: a vector load would
-// be waited for together with every copy that is older than its use.  p is wave-uniform.
-__device__ __forceinline__ float f8_uniform(const float* p) {
-    typedef const float __attribute__((address_space(4))) * Constant;
-    return *(Constant)(uintptr_t)p;
 }
 
 // Blocks go to the eight XCDs in turn: give each XCD a run of neighbouring tiles, which share
@@ -227,20 +219,6 @@ __device__ __forceinline__ f8_bf16x8 f8_widen(int lo, int hi) {
     const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
     return f8_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// An array of f(0) .. f(N - 1).
-template <class V, int N>
-struct F8Array {
-    V at[N];
-};
-template <class F, int... I>
-__device__ __forceinline__ auto f8_each_of(F&& f, std::integer_sequence<int, I...>) {
-    return F8Array<decltype(f(0)), sizeof...(I)>{{f(I)...}};
-}
-template <int N, class F>
-__device__ __forceinline__ auto f8_each(F&& f) {
-    return f8_each_of(f, std::make_integer_sequence<int, N>{});
 }
 
 // Float results: one rounding to the element type (to nearest even).

@@ -439,7 +439,6 @@ inline q8_status check_moe_layer(const float* wr, const void* wgu, const void* w
 
 // ------------------------------------------------- block-scaled 8-bit floating point
 
-constexpr int64_t kF8Block = 128;
 constexpr int64_t kF8MaxDim = int64_t(1) << 20;    // k, matrix rows: 256 rows stay within 32-bit offsets
 constexpr int64_t kF8MaxRows = int64_t(1) << 24;   // m
 constexpr int64_t kF8MaxArea = int64_t(1) << 37;   // tiles of 256 x 256: a grid fits 32 bits of threads
