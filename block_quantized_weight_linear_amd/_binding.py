@@ -638,7 +638,7 @@ def _f8_quantize(fn, x, name, block_rows, pow2, q, d):
     shape = ((rows + block_rows - 1) // block_rows, _f8_blocks(k))
     if d is None:
         d = torch.empty(shape, dtype=torch.float32, device=dev)
-    _contig_out(q, (rows, k), "q", torch.uint8 if q.dtype == torch.uint8 else torch.float8_e4m3fn, dev)
+    _contig_out(q, (rows, k), "q", torch.uint8 if getattr(q, "dtype", None) == torch.uint8 else torch.float8_e4m3fn, dev)
     _contig_out(d, shape, "d", torch.float32, dev)
     size = x.element_size()
     # a single row: only its k values are touched, so any leading dimension of whole 16 bytes does
@@ -669,7 +669,7 @@ def f8_linear(wq, wd, xq, xd, dtype=torch.float32, out=None):
     dev = wq.device
     if out is None:
         out = torch.empty((m, n), dtype=dtype, device=dev)
-    kind = _float_type(out.dtype, "the output")
+    kind = _float_type(getattr(out, "dtype", None), "the output")
     _rows_out(out, m, n, "out", out.dtype, dev)
     _call(dev, lib.f8_linear, wq.data_ptr(), wd.data_ptr(), n, k, xq.data_ptr(), xd.data_ptr(), m, out.data_ptr(), kind,
           _f8_ld(out, n), _stream(wq))
@@ -684,7 +684,7 @@ def f8_linear_fused_gate_up_silu(wq, wd, xq, xd, dtype=torch.float32, keep_gate_
     dev = wq.device
     if out is None:
         out = torch.empty((m, f), dtype=dtype, device=dev)
-    kind = _float_type(out.dtype, "the output")
+    kind = _float_type(getattr(out, "dtype", None), "the output")
     _rows_out(out, m, f, "out", out.dtype, dev)
     gu = None
     if isinstance(keep_gate_up, torch.Tensor):

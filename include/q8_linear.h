@@ -505,8 +505,8 @@ q8_status f8_linear_fused_gate_up_silu(const uint8_t* wq, const float* wd, int64
                                        const float* xd, int64_t m, void* h, int32_t type, int64_t ldh, void* gu,
                                        int64_t ldgu, void* stream);
 
-/* Workspace bytes of the two backward calls for these sizes (n: rows of the matrix, the fused
- * call's 2f; 0 on invalid sizes). */
+/* Workspace bytes of the two backward calls for these sizes (n and f as the calls take them: the
+ * fused matrix has 2f rows; 0 on invalid sizes). */
 size_t f8_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t type);
 size_t f8_linear_fused_gate_up_silu_backward_workspace_bytes(int64_t m, int64_t f, int64_t k, int32_t type);
 

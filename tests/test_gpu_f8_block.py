@@ -187,3 +187,18 @@ def test_large_batch(q8):
     del dx, dw
     q, d = lib.f8_quantize_act(value(torch, x[-70000:]).bfloat16(), pow2=True)
     assert (d[:, -1] <= 2.0 ** -8).all() and torch.equal(value(torch, q) * d.repeat_interleave(128, 1)[:, :k], value(torch, x[-70000:]))
+
+
+def test_refuses_what_is_no_tensor(q8):
+    """Operands and outputs that are not tensors: a ValueError, as for every wrong one."""
+    lib, torch, dev = q8
+    x, w = torch.ones(3, 256, device=dev), torch.ones(130, 256, device=dev)
+    (xq, xd), (wq, wd) = lib.f8_quantize_act(x), lib.f8_quantize_weight(w)
+    calls = (lambda: lib.f8_quantize_act(x, q=[0]), lambda: lib.f8_quantize_act(x, d=[0.0]),
+             lambda: lib.f8_quantize_weight(w, q=7), lambda: lib.f8_linear(wq, wd, xq, xd, out=[1.0]),
+             lambda: lib.f8_linear_fused_gate_up_silu(wq, wd, xq, xd, out=1),
+             lambda: lib.f8_linear(wq, None, xq, xd), lambda: lib.f8_linear(wq, wd, [1], xd),
+             lambda: lib.f8_linear_backward(wq, wd, xq, xd, [1.0]))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
