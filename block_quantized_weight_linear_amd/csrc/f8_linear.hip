@@ -5,8 +5,8 @@
 // step is one block of 128 inputs, 128 bytes a row: weight rows are the instruction's A (so a lane ends
 // up with four neighbouring outputs of one row), activation rows its B.  One instruction is a whole
 // block of a fragment; its sum starts at zero and joins the accumulators as acc += (xd * wd) * sum, the
-// factor being one number a lane (the lane's activation row) since a fragment's weight rows lie in one
-// block of 128.  (Fragments of 32 x 32, two instructions a block, read their operands half as often, and
+// factor being one number a lane (the lane's activation row) and fragment, since a fragment's weight
+// rows lie in one block of 128.  (Fragments of 32 x 32, two instructions a block, read their operands half as often, and
 // measured 263 us where these take 237, 4096 rows of 8192 x 8192: their sums are four times as long on
 // the way.)
 //
@@ -113,7 +113,11 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
     constexpr int SCALE_STAGES = f8_scale_stages<WN, WM, D>();
     constexpr int OUT = SILU ? TN * 8 : TN * 16;  // outputs of a wave
     using Codes = std::conditional_t<sizeof(T) == 4, F8Widened, F8Codes>;
-    static_assert(128 % (TN * 16) == 0 && (!SILU || TN % 2 == 0), "a wave's weight rows lie in one block");
+    // Where a wave's weight rows do not divide a block, fragment i's block is its first or its last one's.
+    constexpr bool CROSSES = 128 % (TN * 16) != 0;
+    static_assert(!SILU || (!CROSSES && TN % 2 == 0), "a wave's gate rows lie in one block, and its up rows");
+    static_assert(TN * 16 <= 128, "a wave's weight rows lie in two blocks at most");
+    constexpr int FACTORS = CROSSES ? TN : SILU ? 2 : 1;  // of an activation row
     static_assert(ROWS / 8 % W == 0 && f8_scale_rows<WN, WM, TM>() / 64 < W && (W != 8 || D == 2),
                   "every wave has the same number of copies");
     extern __shared__ __attribute__((aligned(16))) uint8_t f8_smem[];
@@ -170,12 +174,12 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
     const uint32_t lds = f8_lds_address(f8_smem);
     const uint32_t lds_sx = lds + D * ROWS * 128;
     // Scales, a copy of four bytes a lane: the waves w < SX / 64 those of rows 64w .., the others word i the
-    // scale of the weight block of wave i / 2 (gate's and up's where they are fused); past the matrix: the
-    // last block, of rows that are not stored.
+    // scale of a weight block of wave i / 2 (gate's and up's where they are fused, else the first and the last
+    // fragment's); past the matrix: the last block, of rows that are not stored.
     constexpr int SX = f8_scale_rows<WN, WM, TM>(), SW = f8_scale_words<WN, WM, TM>();
     const int last_block = (a.n_out - 1) / 128;
     auto weight_scale = [&](int i) __attribute__((always_inline)) {
-        const int b = (n0 + (i / 2 % WN) * OUT) / 128;
+        const int b = (n0 + (i / 2 % WN) * OUT + (!SILU && i % 2 ? OUT - 16 : 0)) / 128;
         return (uint32_t)((b < last_block ? b : last_block) + (SILU && i % 2 ? last_block + 1 : 0));
     };
     const int sx_row = m0 + 64 * wave + lane;
@@ -221,8 +225,9 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
 
     // A step's products in PARTS parts of its activation rows; the weights' fragments serve them all.
     Codes av[TN], bv[PM];
-    float c0[PM] = {}, c1[PM] = {};
+    float factor[FACTORS][PM] = {};
     float sx[PM], w0 = 0.f, w1 = 0.f;
+    const int in_first = (128 - out0 % 128) / 16;  // fragments in the wave's first block
     auto load_from = [&](int s, int h, int from) __attribute__((always_inline)) {
         if (h == 0)
 #pragma unroll
@@ -233,14 +238,14 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
 #pragma unroll
         for (int j = 0; j < PM; ++j) sx[j] = at[(wm * TM + h * PM + j) * 16 + l16];
         w0 = at[SX + 2 * wn];
-        if (SILU) w1 = at[SX + 2 * wn + 1];
+        if (FACTORS > 1) w1 = at[SX + 2 * wn + 1];
     };
     auto ready = [&](int, int) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < PM; ++j) {
-            c0[j] = sx[j] * w0;
-            c1[j] = SILU ? sx[j] * w1 : c0[j];
-        }
+        for (int j = 0; j < PM; ++j)
+#pragma unroll
+            for (int i = 0; i < FACTORS; ++i)
+                factor[i][j] = sx[j] * (CROSSES ? (i < in_first ? w0 : w1) : i ? w1 : w0);
     };
     // A sum joins the accumulators LAG instructions after it was asked for, in this order
     // (scheduling fences): the lanes then work while the matrix cores do.  The last LAG join in finish().
@@ -248,7 +253,7 @@ __global__ __launch_bounds__(64 * WN * WM) void f8_linear_kernel(F8LinearArgs a)
     f8_f32x4 t[LAG + 1] = {};
     auto join = [&](int h, int p) __attribute__((always_inline)) {
         const int i = p / PM, j = p % PM;
-        const float c = SILU && i >= TN / 2 ? c1[j] : c0[j];
+        const float c = factor[CROSSES ? i : SILU ? i / (TN / 2) : 0][j];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc[i][h * PM + j][e] = __builtin_fmaf(c, t[p % (LAG + 1)][e], acc[i][h * PM + j][e]);
@@ -527,13 +532,18 @@ hipError_t launch_type(const DeviceInfo& dev, const F8LinearArgs& a, hipStream_t
     // inputs, in us: 16-bit results 59, 30, 23 and 16; float32 results 57, 46, 29 and 19.  Measured for
     // 6144 x 4096 in bfloat16, in that order of tiles: 128 rows 49.6, 30.4, 23.4, 16.9; 256 rows 58.6, 30.5,
     // 23.3, 30.9; 512 rows 58.3, 30.9, 44.2, 45.4; 4096 rows 121, 176, 254, 333.
+    // A fifth tile of 192 weight rows (16-bit products; a wave's 48 rows lie in two blocks, so with factors for each
+    // fragment) costs 53, more than three quarters of the largest's 59 as it reads more for a product; it is for
+    // calls that end between whole rounds of that one: 6144 x 4096, 4096 rows, 384 tiles 120 us, 512 of these 112;
+    // 4096 x 12288, 2048 rows, 128 tiles 153 us, 176 of these 131; 10240 x 4096, 2048 rows 120 us, so 103.
     constexpr bool WIDE = sizeof(T) == 4;
     constexpr int BIG = WIDE ? 4 : 8;
-    const int64_t bn[4] = {256, 128, 128, 64}, bm[4] = {32 * BIG, 128, 64, 64};
-    const int64_t cost[4] = {WIDE ? 57 : 59, WIDE ? 46 : 30, WIDE ? 29 : 23, WIDE ? 19 : 16};
+    constexpr bool THIRD = !WIDE && !SILU;
+    const int64_t bn[5] = {256, 128, 128, 64, 192}, bm[5] = {32 * BIG, 128, 64, 64, 256};
+    const int64_t cost[5] = {WIDE ? 57 : 59, WIDE ? 46 : 30, WIDE ? 29 : 23, WIDE ? 19 : 16, 53};
     int best = 0;
     int64_t least = INT64_MAX;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (THIRD ? 5 : 4); ++i) {
         const int64_t tiles = (a.n_out * cols + bn[i] - 1) / bn[i] * ((a.m + bm[i] - 1) / bm[i]);
         const int64_t time = (tiles + cus - 1) / cus * cost[i];
         if (time < least) {
@@ -545,8 +555,11 @@ hipError_t launch_type(const DeviceInfo& dev, const F8LinearArgs& a, hipStream_t
         case 0: return launch_tile<4, 2, 4, BIG, 2, SILU, T>(a, stream);
         case 1: return launch_tile<2, 2, 4, 4, 4, SILU, T>(a, stream);
         case 2: return launch_tile<4, 1, 2, 4, 6, SILU, T>(a, stream);
-        default: return launch_tile<2, 2, 2, 2, 6, SILU, T>(a, stream);
+        case 3: return launch_tile<2, 2, 2, 2, 6, SILU, T>(a, stream);
+        default: break;
     }
+    if constexpr (THIRD) return launch_tile<4, 2, 3, 8, 2, SILU, T>(a, stream);
+    return hipErrorInvalidValue;  // not reached
 }
 
 template <class T>

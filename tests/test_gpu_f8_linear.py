@@ -148,6 +148,14 @@ def test_exact_sums(q8, m, n, k):
         assert torch.equal(lib.f8_linear(*args, dtype=dtype).cpu(), want.to(dtype))
 
 
+@pytest.mark.parametrize("m,n,k", [(2000, 6131, 400), (1793, 6001, 112), (4097, 6140, 128)])
+def test_products_whose_rows_cross_blocks(q8, m, n, k):
+    """Sizes between whole rounds of the largest tiles: waves of 48 weight rows, in two blocks of scales."""
+    test_exact_sums(q8, m, n, k)
+    for kind in ("bfloat16", "float16"):
+        test_linear(q8, m, n, k, kind)
+
+
 def test_every_code(q8):
     """Each of the 254 finite codes of either operand at its value, in every block position."""
     lib, torch, dev = q8
