@@ -189,18 +189,30 @@ __global__ __launch_bounds__(kPartThreads) void f8_zero_rows_kernel(T* __restric
         out[i / cols * ld + i % cols] = (T)0.f;
 }
 
-// Results of ranges [ranges][rows][k] added in their order.
+// Results of ranges [ranges][rows][k] added in their order.  dx's are added by further blocks of the launch of
+// dw's small tiles, which leave CUs free (2001 x 1040, 77 rows in float32: a launch of its own for it, the call
+// 32.5 us; so, 27.6; fused 1536 x 2048, 130 rows in binary16: 31.6, so 29.0).
+struct F8AddRangesArgs {
+    const float* sums;
+    void* out;
+    int64_t rows, ld;
+    int ranges, k;
+    bool vec;
+};
 template <class T>
-__global__ __launch_bounds__(kPartThreads) void f8_add_ranges_kernel(const float* __restrict__ sums, int ranges, int64_t rows,
-                                                                    int k, T* __restrict__ out, int64_t ld, bool vec) {
-    const int64_t per_row = k / 4, total = rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPartThreads) {
+__device__ __forceinline__ void f8_add_ranges(const F8AddRangesArgs& a, int64_t first, int64_t step) {
+    const int64_t per_row = a.k / 4, total = a.rows * per_row;
+    for (int64_t i = first; i < total; i += step) {
         const int64_t row = i / per_row, col = 4 * (i - row * per_row);
-        const float* at = sums + row * k + col;
+        const float* at = a.sums + row * a.k + col;
         f8_f32x4 v = *reinterpret_cast<const f8_f32x4*>(at);
-        for (int r = 1; r < ranges; ++r) v += *reinterpret_cast<const f8_f32x4*>(at + r * rows * k);
-        f8_store4(out + row * ld + col, v, 4, vec);
+        for (int r = 1; r < a.ranges; ++r) v += *reinterpret_cast<const f8_f32x4*>(at + r * a.rows * a.k);
+        f8_store4(static_cast<T*>(a.out) + row * a.ld + col, v, 4, a.vec);
     }
+}
+template <class T>
+__global__ __launch_bounds__(kPartThreads) void f8_add_ranges_kernel(F8AddRangesArgs a) {
+    f8_add_ranges<T>(a, (int64_t)blockIdx.x * kPartThreads + threadIdx.x, (int64_t)gridDim.x * kPartThreads);
 }
 
 unsigned part_blocks(int64_t threads) {
@@ -479,6 +491,8 @@ struct F8WeightGradArgs {
     int ranges, range_steps;
     int64_t range_stride;
     bool vec;
+    F8AddRangesArgs dx;    // small tiles: what dx still has to add, by the blocks from dx_block on
+    unsigned dx_block;
 };
 
 template <int WK, int WN, int GN, int D>
@@ -502,6 +516,12 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wn = wave / WK;
+    if constexpr (W != 8) {
+        if (blockIdx.x >= a.dx_block) {
+            f8_add_ranges<T>(a.dx, (int64_t)(blockIdx.x - a.dx_block) * (64 * W) + tid, (int64_t)(gridDim.x - a.dx_block) * (64 * W));
+            return;
+        }
+    }
     const F8Tile tile = f8_tile_of_block((int)blockIdx.x, a.k_tiles, a.n_tiles * a.parts * a.ranges);
     if (!tile.inside) return;  // block-uniform, before any barrier
     const int range = tile.col / (a.n_tiles * a.parts), col = tile.col - range * (a.n_tiles * a.parts);
@@ -672,8 +692,10 @@ hipError_t launch_weight_grad_tile(F8WeightGradArgs a, hipStream_t stream) {
     a.k_tiles = (a.k + BK - 1) / BK;
     a.n_tiles = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)a.k_tiles * a.n_tiles * a.parts * a.ranges;
-    if (f8_grid(tiles) * (64 * WK * WN) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)f8_grid(tiles)), dim3(64 * WK * WN), lds, stream, a);
+    a.dx_block = (unsigned)f8_grid(tiles);
+    const int64_t blocks = f8_grid(tiles) + (a.dx.sums ? part_blocks(a.dx.rows * (a.dx.k / 4)) : 0);
+    if (blocks * (64 * WK * WN) >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * WK * WN), lds, stream, a);
     return hipGetLastError();
 }
 
@@ -693,9 +715,8 @@ hipError_t zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, hipStrea
 }
 
 template <class T>
-hipError_t add_ranges(const float* sums, int ranges, int64_t rows, int64_t k, void* out, int64_t ld, hipStream_t stream) {
-    hipLaunchKernelGGL(f8_add_ranges_kernel<T>, dim3(part_blocks(rows * (k / 4))), dim3(kPartThreads), 0, stream, sums,
-                       ranges, rows, (int)k, static_cast<T*>(out), ld, rows_aligned<T>(out, ld, 4));
+hipError_t add_ranges(const F8AddRangesArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL(f8_add_ranges_kernel<T>, dim3(part_blocks(a.rows * (a.k / 4))), dim3(kPartThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -710,7 +731,10 @@ hipError_t backward(const uint8_t* wq, const float* wd, int64_t n, int parts, in
     uint8_t* base = static_cast<uint8_t*>(workspace);
     uint16_t* planes = reinterpret_cast<uint16_t*>(base + ws.d_off);
     uint16_t* values = reinterpret_cast<uint16_t*>(base + ws.x_off);
-    float* sums = reinterpret_cast<float*>(base + ws.sums_off);
+    float* dx_sums = reinterpret_cast<float*>(base + ws.sums_off);
+    float* dw_sums = reinterpret_cast<float*>(base + ws.dw_sums_off);
+    const q8v::F8GradPlan dx_plan = q8v::f8_dx_plan(m, n, parts, k, type), dw_plan = q8v::f8_dw_plan(m, n, parts, k, type);
+    F8AddRangesArgs add{};  // what dx still has to add: by the tiles' launch of dw if that is of small tiles, else by one of its own
     const int kb = (int)((k + 127) / 128);
     hipError_t e = hipSuccess;
 
@@ -743,14 +767,15 @@ hipError_t backward(const uint8_t* wq, const float* wd, int64_t n, int parts, in
         a.w = wq; a.wd = wd; a.dx = dx; a.lddx = lddx;
         a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k; a.kb = kb;
         a.vec = rows_aligned<T>(dx, lddx, 4);
-        const q8v::F8GradPlan plan = q8v::f8_dx_plan(m, n, parts, k, type);
+        const q8v::F8GradPlan plan = dx_plan;
         const int64_t steps = parts * TERMS * ((n + kGStep - 1) / kGStep);
         a.range_steps = (int)((steps + plan.ranges - 1) / plan.ranges);
         a.ranges = (int)((steps + a.range_steps - 1) / a.range_steps);
         if (a.ranges > 1) {
-            a.dx = sums; a.lddx = k; a.vec = true; a.range_stride = m * k;
-            if ((e = launch_input_grad_tile<2, 2, 2, 6, T, float>(a, stream)) != hipSuccess) return e;
-            e = add_ranges<T>(sums, a.ranges, m, k, dx, lddx, stream);
+            add = {dx_sums, dx, m, lddx, a.ranges, (int)k, a.vec};
+            a.dx = dx_sums; a.lddx = k; a.vec = true; a.range_stride = m * k;
+            e = launch_input_grad_tile<2, 2, 2, 6, T, float>(a, stream);
+            if (e == hipSuccess && (!dw || dw_plan.big)) e = add_ranges<T>(add, stream);
         } else {
             e = plan.big ? launch_input_grad_tile<4, 2, 8, 2, T>(a, stream) : launch_input_grad_tile<2, 2, 2, 6, T>(a, stream);
         }
@@ -762,14 +787,16 @@ hipError_t backward(const uint8_t* wq, const float* wd, int64_t n, int parts, in
         a.x = values; a.x_plane = p.rows * k; a.dw = dw; a.lddw = lddw;
         a.n = (int)n; a.parts = parts; a.m = (int)m; a.k = (int)k;
         a.vec = rows_aligned<T>(dw, lddw, 4);
-        const q8v::F8GradPlan plan = q8v::f8_dw_plan(m, n, parts, k, type);
+        const q8v::F8GradPlan plan = dw_plan;
+        if (!plan.big) a.dx = add;
         const int64_t steps = TERMS * (TERMS + 1) / 2 * (p.rows / kGStep);
         a.range_steps = (int)((steps + plan.ranges - 1) / plan.ranges);
         a.ranges = (int)((steps + a.range_steps - 1) / a.range_steps);
         if (a.ranges > 1) {
-            a.dw = sums; a.lddw = k; a.vec = true; a.range_stride = parts * n * k;
+            const F8AddRangesArgs dw_add{dw_sums, dw, parts * n, lddw, a.ranges, (int)k, a.vec};
+            a.dw = dw_sums; a.lddw = k; a.vec = true; a.range_stride = parts * n * k;
             if ((e = launch_weight_grad_tile<2, 2, 1, 4, T, float>(a, stream)) != hipSuccess) return e;
-            e = add_ranges<T>(sums, a.ranges, parts * n, k, dw, lddw, stream);
+            e = add_ranges<T>(dw_add, stream);
         } else {
             e = plan.big ? launch_weight_grad_tile<4, 2, 2, 2, T>(a, stream) : launch_weight_grad_tile<2, 2, 1, 4, T>(a, stream);
         }

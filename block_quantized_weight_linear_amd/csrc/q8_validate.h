@@ -553,10 +553,11 @@ inline F8GradPlan f8_dw_plan(int64_t m, int64_t n_part, int parts, int64_t k, in
 
 // Workspace of the backward calls: the gradients of the products as planes of bf16 parts
 // [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, the inputs as planes
-// [terms][rows][k] (columns of a part and rows in whole steps), and the ranges' sums of dx, then of dw.
+// [terms][rows][k] (columns of a part and rows in whole steps), and the ranges' sums of dx and of dw (dx's are
+// added while dw's are made).
 struct F8BackwardWorkspace {
     int64_t ldd;
-    size_t d_off, x_off, sums_off, total;
+    size_t d_off, x_off, sums_off, dw_sums_off, total;
 };
 inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
     F8BackwardWorkspace w{};
@@ -570,7 +571,8 @@ inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int par
     size_t off = 0;
     w.d_off = off;    off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
     w.x_off = off;    off = round_up(off + 2 * terms * rows * size_t(k), 256);
-    w.sums_off = off; off = round_up(off + sizeof(float) * (dx_sums > dw_sums ? dx_sums : dw_sums), 256);
+    w.sums_off = off; off = round_up(off + sizeof(float) * dx_sums, 256);
+    w.dw_sums_off = off; off = round_up(off + sizeof(float) * dw_sums, 256);
     w.total = off ? off : 256;
     return w;
 }

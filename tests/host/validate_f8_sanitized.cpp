@@ -87,6 +87,8 @@ int main() {
                             EXPECT(dw.ranges >= 1 && dw.ranges <= kF8MaxRanges && (!dw.big || dw.ranges == 1), 1);
                             if (dx.ranges > 1) EXPECT(l.total - l.sums_off >= size_t(4 * dx.ranges * m * k), 1);
                             if (dw.ranges > 1) EXPECT(l.total - l.sums_off >= size_t(4 * dw.ranges * parts * n * k), 1);
+                            if (dx.ranges > 1) EXPECT(l.dw_sums_off - l.sums_off >= size_t(4 * dx.ranges * m * k), 1);
+                            if (dw.ranges > 1) EXPECT(l.total - l.dw_sums_off >= size_t(4 * dw.ranges * parts * n * k), 1);
                         }
                 // the largest sizes stay within 64 bits
                 EXPECT(f8_backward_workspace_bytes(int64_t(1) << 17, kF8MaxDim / parts, parts, int64_t(1) << 17, type) >
