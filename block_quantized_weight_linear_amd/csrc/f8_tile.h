@@ -22,10 +22,12 @@ static __device__ const f8_i32x4 f8_zeros = {0, 0, 0, 0};
 
 // One wave-wide direct-to-LDS copy from a scalar base: lane l copies the 16 (4) bytes at
 // base + off to lds + 16*l (lds + 4*l).  base and lds are wave-uniform; a write of M0 needs one
-// wait state before the copy reads it.  M0 is left written: the compiler keeps nothing there and writes it
-// itself where an instruction of its own reads it (with M0 saved around each copy the copies between a
-// wave's products took two instructions more).  It counts as one
-// vector-memory load.
+// wait state before the copy reads it.  M0 is left written and declared so, which makes the compiler write it
+// anew before an instruction of its own that reads it (saved around each copy instead, the copies between a
+// wave's products took two instructions more).  clang warns that a reserved register is not saved for the
+// caller, which is what is wanted here.  It counts as one vector-memory load.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void f8_copy16(const uint8_t* base, uint32_t off, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
@@ -33,7 +35,7 @@ __device__ __forceinline__ void f8_copy16(const uint8_t* base, uint32_t off, uin
         "global_load_lds_dwordx4 %0, %1"
         :
         : "v"(off), "s"(base), "s"(lds)
-        : "memory");
+        : "m0", "memory");
 }
 __device__ __forceinline__ void f8_copy4(const uint8_t* base, uint32_t off, uint32_t lds) {
     asm volatile(
@@ -42,7 +44,7 @@ __device__ __forceinline__ void f8_copy4(const uint8_t* base, uint32_t off, uint
         "global_load_lds_dword %0, %1"
         :
         : "v"(off), "s"(base), "s"(lds)
-        : "memory");
+        : "m0", "memory");
 }
 // Four bytes a lane from addresses of their own.
 __device__ __forceinline__ void f8_copy4_from(const float* src, uint32_t lds) {
@@ -52,7 +54,7 @@ __device__ __forceinline__ void f8_copy4_from(const float* src, uint32_t lds) {
         "global_load_lds_dword %0, off"
         :
         : "v"(src), "s"(lds)
-        : "memory");
+        : "m0", "memory");
 }
 // The same where valid, zeros where not (the cut last step of an operand).
 __device__ __forceinline__ void f8_copy16_or_zeros(const uint8_t* base, uint32_t off, bool valid, uint32_t lds) {
@@ -64,8 +66,9 @@ __device__ __forceinline__ void f8_copy16_or_zeros(const uint8_t* base, uint32_t
         "global_load_lds_dwordx4 %0, off"
         :
         : "v"(src), "s"(lds)
-        : "memory");
+        : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ uint32_t f8_lds_address(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
