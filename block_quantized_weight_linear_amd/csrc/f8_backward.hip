@@ -132,15 +132,16 @@ __device__ __forceinline__ void f8_gradient_planes(const F8PlanesArgs& a, int64_
         if constexpr (KIND == kSplit) {
             store_parts<TERMS>(at, a.m * a.ldo, h);
         } else {
-            // the gate's and up's gradients beside each other, each a value of type T
+            // the gate's and up's gradients beside each other, in float32: rounded to T, binary16 ones would have its
+            // range too, 65504 and 2^-24, which the results may lie within where these do not
             float g[8], u[8], dg[8], du[8];
             load_row8(gu + row * a.ldgu, col, a.n, a.vec, g);
             load_row8(gu + row * a.ldgu + a.n, col, a.n, a.vec && a.n % 8 == 0, u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float s = 1.0f / (1.0f + __expf(-g[e]));
-                dg[e] = (float)f8_round<T>(h[e] * u[e] * (s * (1.0f + g[e] * (1.0f - s))));
-                du[e] = (float)f8_round<T>(h[e] * (g[e] * s));
+                dg[e] = h[e] * u[e] * (s * (1.0f + g[e] * (1.0f - s)));
+                du[e] = h[e] * (g[e] * s);
             }
             store_parts<TERMS>(at, a.m * a.ldo, dg);
             store_parts<TERMS>(at + a.ldo / 2, a.m * a.ldo, du);

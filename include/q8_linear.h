@@ -535,8 +535,10 @@ q8_status f8_linear_backward(const uint8_t* wq, const float* wd, int64_t n, int6
 /*
  * The gradients of f8_linear_fused_gate_up_silu's inputs from dh and the gate and up products
  * that it kept.  With s = 1 / (1 + exp(-g)):
- *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s,  each rounded to `type` once;
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s,  in float32;
  *   dx = [dg du] . W          dw = [dg du]^T . x
+ * dg and du enter the products as as many bf16 parts as f8_linear_backward takes gradients of `type`
+ * as: rounded to bf16 with bf16, to within 2^-17 with binary16, exactly with float32.
  *   gu : [m][ldgu], ldgu >= 2f;  dh : [m][lddh], lddh >= f, both of element type `type`
  *   dx : NULL, or [m][lddx] out, lddx >= k;  dw : NULL, or [2f][lddw] out, lddw >= k
  * Arithmetic, workspace (f8_linear_fused_gate_up_silu_backward_workspace_bytes) and rules as for
