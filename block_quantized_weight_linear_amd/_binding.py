@@ -662,6 +662,13 @@ def f8_quantize_weight(w, pow2: bool = False, q=None, d=None):
     return _f8_quantize(lib.f8_quantize_weight, w, "w", 128, pow2, q, d)
 
 
+def _f8_asked(want, name):
+    """Whether an output that is asked for by True is: anything else that is no tensor is a caller's mistake."""
+    if want not in (True, False, None):
+        raise ValueError(f"{name} must be True, False or a device tensor, got {type(want).__name__}")
+    return bool(want)
+
+
 def f8_linear(wq, wd, xq, xd, dtype=torch.float32, out=None):
     """y = x . W^T [m][n] in `dtype` from e4m3 codes wq [n][k] and xq [m][k] and their scales
     (f8_quantize_weight, f8_quantize_act)."""
@@ -689,7 +696,7 @@ def f8_linear_fused_gate_up_silu(wq, wd, xq, xd, dtype=torch.float32, keep_gate_
     gu = None
     if isinstance(keep_gate_up, torch.Tensor):
         gu = _rows_out(keep_gate_up, m, 2 * f, "keep_gate_up", out.dtype, dev)
-    elif keep_gate_up:
+    elif _f8_asked(keep_gate_up, "keep_gate_up"):
         gu = torch.empty((m, 2 * f), dtype=out.dtype, device=dev)
     _call(dev, lib.f8_linear_fused_gate_up_silu, wq.data_ptr(), wd.data_ptr(), f, k, xq.data_ptr(), xd.data_ptr(), m,
           out.data_ptr(), kind, _f8_ld(out, f), None if gu is None else gu.data_ptr(),
@@ -711,7 +718,7 @@ def _f8_gradient(want, m, width, name, dtype, device):
     """The tensor that a gradient goes to: new (True), the caller's, or none (False)."""
     if isinstance(want, torch.Tensor):
         return _rows_out(want, m, width, name, dtype, device)
-    return torch.empty((m, width), dtype=dtype, device=device) if want else None
+    return torch.empty((m, width), dtype=dtype, device=device) if _f8_asked(want, name) else None
 
 
 def _f8_backward(fn, parts, wq, wd, xq, xd, gu, d, dx, dw, workspace, need):
