@@ -651,7 +651,8 @@ def _f8_quantize(fn, x, name, block_rows, pow2, q, d):
 def f8_quantize_act(x, pow2: bool = False, q=None, d=None):
     """e4m3 codes [m][k] and float32 scales [m][ceil(k/128)] of rows x [m][k] (float32,
     float16 or bfloat16): one scale for every 128 inputs, amax/448 or (pow2) the least power
-    of two that is not below it."""
+    of two that is not below it.  Outside autograd, as all calls here: what requires a gradient
+    gets it from the backward calls."""
     return _f8_quantize(lib.f8_quantize_act, x, "x", 1, pow2, q, d)
 
 

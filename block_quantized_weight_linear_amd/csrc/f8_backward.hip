@@ -56,7 +56,8 @@ constexpr int kTerms = sizeof(T) == 4 ? 3 : __is_same(T, __bf16) ? 1 : 2;
 // ------------------------------------------------------------------------------ bf16 parts
 
 // v as TERMS bf16 parts, each the rest rounded to nearest even: of 24 bits the first leaves 16, the
-// second 7, so that three parts are a float32 and two a binary16 exactly (remainders are exact).
+// second 7, so that three parts are a float32 and two a binary16 exactly (remainders are exact; a float32 below
+// 2^-110 has bits below bf16's least, 2^-133, which are lost).
 // What is not finite stays in the first part; the parts of a number that would round to infinity are
 // cut off instead, so that no sum of its first parts passes it.
 template <int TERMS>

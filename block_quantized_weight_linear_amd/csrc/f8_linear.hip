@@ -11,10 +11,13 @@
 // the way.)
 //
 // The instruction aligns the products of eight inputs at the largest of them and cuts them off
-// 2^-13 below it before they join its float32 sum (measured with pairs of products; sums of random
-// codes are off by 2^-16 of their size).  That is far below a 16-bit result's rounding, and above a
-// float32 one's: with float32 results the codes are widened to bf16, which holds them exactly, and
-// multiplied by v_mfma_f32_16x16x32_bf16, at half the rate, whose sums of them are off by 2^-26.
+// 2^-13 below it before they join its float32 sum (measured with pairs of products).  Random codes lose 2e-5
+// of an output's size so, whatever k (in the norm; 8e-5 where one activation in 128 is 60 times the others), where the
+// rounding of a binary16 result is 2.1e-4 and of a bf16 one 1.7e-3.  At worst it is 7 * 2^-13 of the largest product
+// of every eight, less than half a step of bf16 (2^-8) and more than one of binary16 (2^-11) even where nothing
+// cancels; where large products cancel, it may be all that is left.  Both 16-bit types take it for the rate.  A
+// float32 result does not: its codes are widened to bf16, which holds them exactly, and multiplied by
+// v_mfma_f32_16x16x32_bf16, at half the rate, whose sums of them are off by 2^-26.
 //
 // Tile rows reach LDS by direct copies of 16 bytes a lane, two stages.  Within a row the eight
 // 16-byte chunks are stored at chunk ^ (row % 8), so that the fragments' reads (16 rows, one chunk of

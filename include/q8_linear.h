@@ -470,8 +470,8 @@ typedef enum q8_float_type { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2 } q8_float_type
  *   pow2 = 0 : scale = a / 448, code = e4m3(clamp(x * (448 / a), -448, 448))
  *   pow2 = 1 : scale = the least power of two that is at least a / 448, code = e4m3(x / scale)
  * Quotients and products are rounded to float32 once each, codes to nearest even: the result is
- * bit-exact.  a < 2^-116: codes and scale 0.  A block that holds a NaN or an infinity: codes and
- * scale NaN.
+ * bit-exact.  a < 2^-116: scale 0 and codes zeros of their elements' signs.  A block that holds a NaN or
+ * an infinity: codes and scale NaN.
  *   x : [m][ldx] (w: [n][ldw]) of element type `type`, 16-byte aligned with rows of a multiple of
  *       16 bytes (Q8_ERR_ALIGN otherwise)
  *   q : codes out [m][k]     d : scales out (above)
@@ -487,9 +487,12 @@ q8_status f8_quantize_weight(const void* w, int32_t type, int64_t n, int64_t k, 
  *   y      : [m][ldy] out, element type `type`, ldy >= n
  * acc += (xd * wd) * sum in float32 over the blocks, one rounding to `type` at the end.  With 16-bit
  * results a block's sum runs on the 8-bit matrix cores, which cut a product off at 2^-13 of the largest
- * of the eight that they add at once (sums of random codes are off by 2^-16 of their size, whatever k);
- * with float32 results on the bf16 ones, which are of float32 accuracy.  For one m the order of every sum
- * is fixed by the sizes; it is not the same for every m.
+ * of the eight that they add at once.  Sums of random codes are off by 2e-5 of their size, whatever k, a
+ * tenth of a binary16 result's rounding; a sum whose eights each have one product that is far above the
+ * others by up to 2^-10 of the products' magnitudes, which is more than binary16's half step (2^-11), and may
+ * be all that is left where the large products cancel.  Results of float32 run on the bf16 matrix cores and
+ * are of float32 accuracy whatever the codes.  For one m the order of every sum is fixed by the sizes; it is
+ * not the same for every m.
  */
 q8_status f8_linear(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq, const float* xd,
                     int64_t m, void* y, int32_t type, int64_t ldy, void* stream);
@@ -522,7 +525,8 @@ size_t f8_linear_fused_gate_up_silu_backward_workspace_bytes(int64_t m, int64_t 
  *               workspaces of their own.
  * Products run on the bf16 matrix cores with float32 accumulation and one rounding at the end.
  * Codes are exact in bf16.  Gradients of bf16 are taken as they are, binary16 ones as two bf16
- * parts and float32 ones as three, exactly; a value of x (code * scale) is rounded to as many
+ * parts and float32 ones as three, exactly (of float32 numbers below 2^-110 what lies below bf16's least,
+ * 2^-133, is left out); a value of x (code * scale) is rounded to as many
  * parts for dw: to bf16 with bf16 gradients (scales that are powers of two: not at all), to
  * within 2^-16 with binary16, exactly as a float32 with float32.  Of the products of parts those
  * below 2^-16 (binary16) and 2^-24 (float32) of the whole are left out.
