@@ -4,9 +4,11 @@
 // with d the gradient of the products (the call's own, or behind SiLU(gate) * up its two parts
 // beside each other) and x the inputs' values.
 //
-// An e4m3 code is exact in bf16.  A float operand is a sum of bf16 parts (one for bf16 gradients,
-// two for binary16, three for float32), laid out as planes by a first launch; a product runs over
-// the planes (dw: over the pairs of planes that matter) as if they were further terms of its sum.
+// An e4m3 code is exact in bf16.  A float operand is a sum of bf16 parts (a gradient one of bf16, two of
+// binary16, three of float32; a value of x two, beside float32 gradients three), laid out as planes by a first
+// launch; a product runs over the planes (dw: over the pairs of planes that matter) as if they were further terms
+// of its sum.  (x's values as one part beside bf16 gradients made dw of 4096 rows of the fused 24576 x 4096 off by
+// 2.9e-3 where its own rounding and dg's give 2.3e-3, in 620 us where two take 1234.)
 //
 // Both sums run over an axis that is not the contiguous one of W (dx), or of both operands (dw).
 // Fragments are turned on their way from LDS: ds_read_b64_tr_b16 gives a lane of 16 the four rows of its
@@ -49,9 +51,16 @@ __device__ __forceinline__ u32x2 read_turned8(const uint8_t* p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((Lds)(uint32_t)(uintptr_t)p));
 }
 
-// The bf16 parts of a float operand: 1 (bf16), 2 (binary16), 3 (float32).
+// The bf16 parts of a gradient of type T, 1 (bf16), 2 (binary16) or 3 (float32), of a value of x beside it, and the
+// pairs of them whose products count.
 template <class T>
-constexpr int kTerms = sizeof(T) == 4 ? 3 : __is_same(T, __bf16) ? 1 : 2;
+constexpr int kType = sizeof(T) == 4 ? Q8_F32 : __is_same(T, __bf16) ? Q8_BF16 : Q8_F16;
+template <class T>
+constexpr int kTerms = q8v::f8_terms(kType<T>);
+template <class T>
+constexpr int kValueTerms = q8v::f8_value_terms(kType<T>);
+template <class T>
+constexpr int kPairs = q8v::f8_pairs(kType<T>);
 
 // ------------------------------------------------------------------------------ bf16 parts
 
@@ -106,7 +115,7 @@ __device__ __forceinline__ void store_parts(uint16_t* at, int64_t plane, const f
 }
 
 // What the products read, in one launch: the gradient's planes by the first blocks, the inputs' by the others.
-// Bound by memory (behind 4096 rows of SiLU(gate) * up, 12288 wide, in bf16: 550 MB in 94 us, 5.9 TB/s).
+// Bound by memory (behind 4096 rows of SiLU(gate) * up, 12288 wide, in bf16: 585 MB in 99 us, 5.9 TB/s).
 struct F8PlanesArgs {
     const void* d;    // the call's gradient [m][n]; kind kNoPlanes: it is its own plane
     const void* gu;   // kind kBehindSilu: gate and up products [m][2n]
@@ -180,8 +189,8 @@ __global__ __launch_bounds__(kPartThreads) void f8_planes_kernel(F8PlanesArgs a)
             return;
         }
     }
-    f8_input_planes<TERMS>(a, (int64_t)(blockIdx.x - a.d_blocks) * kPartThreads + threadIdx.x,
-                           (int64_t)(gridDim.x - a.d_blocks) * kPartThreads);
+    f8_input_planes<kValueTerms<T>>(a, (int64_t)(blockIdx.x - a.d_blocks) * kPartThreads + threadIdx.x,
+                                    (int64_t)(gridDim.x - a.d_blocks) * kPartThreads);
 }
 
 template <class T>
@@ -507,7 +516,7 @@ constexpr size_t weight_grad_lds_bytes() {
 
 // WK x WN waves, a wave 64 columns x 64 GN rows of dw.  A step is 64 activation rows; a tile's operands lie
 // in LDS as runs of 64 columns, [64 rows][128 bytes] each.  Its sums stay in the instruction's accumulators: the same
-// size 620 us, 1.33 PFLOP/s, matrix cores busy 60% of the cycles at a clock that they pull down to 1.8 - 2.0 GHz.
+// size 1234 us for its two pairs of planes, 1.34 PFLOP/s, matrix cores busy 60% of the cycles at a clock that they pull down to 1.8 - 2.0 GHz.
 template <int WK, int WN, int GN, int D, class T, class O>
 __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGradArgs a) {
     constexpr int W = WK * WN, BK = WK * 64, BN = WN * GN * 64;
@@ -556,10 +565,11 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     }
     const uint32_t lds = f8_lds_address(f8_smem);
     const int steps = (a.m + kGStep - 1) / kGStep;
-    // the pairs of planes whose products count: (0, 0), then (0, 1), (1, 0), then (0, 2), (1, 1), (2, 0)
+    // the pairs of planes (d's, x's) whose products count: (0, 0), then (0, 1), (1, 0), then (0, 2), (1, 1), (2, 0); of
+    // one part of d the first two
     auto d_of = [](int pair) { return pair < 2 ? 0 : pair == 2 ? 1 : pair - 3; };
     auto x_of = [](int pair) { return pair < 2 ? pair : pair == 2 ? 0 : 5 - pair; };
-    constexpr int PAIRS = kTerms<T> * (kTerms<T> + 1) / 2;
+    constexpr int PAIRS = kPairs<T>;
     struct Place {
         int step = 0, s = 0, pair = 0;
         const uint8_t *x, *d;
@@ -568,16 +578,14 @@ __global__ __launch_bounds__(64 * WK * WN) void f8_weight_grad_kernel(F8WeightGr
     const uint8_t* d0 = reinterpret_cast<const uint8_t*>(a.d + part * a.part_cols);
     const int64_t x_next = (int64_t)2 * kGStep * a.k, d_next = (int64_t)2 * kGStep * a.ldd;
     auto advance = [&](Place& p, int step) __attribute__((always_inline)) {
-        const bool on = step != p.step, next = PAIRS > 1 && on && p.s == steps - 1;
+        const bool on = step != p.step, next = on && p.s == steps - 1;
         p.step = step;
         p.s = next ? 0 : p.s + (on ? 1 : 0);
         p.x += on ? x_next : 0;
         p.d += on ? d_next : 0;
-        if constexpr (PAIRS > 1) {
-            p.pair += next ? 1 : 0;
-            p.x = next ? x0 + 2 * x_of(p.pair) * a.x_plane : p.x;
-            p.d = next ? d0 + 2 * d_of(p.pair) * a.d_plane : p.d;
-        }
+        p.pair += next ? 1 : 0;
+        p.x = next ? x0 + 2 * x_of(p.pair) * a.x_plane : p.x;
+        p.d = next ? d0 + 2 * d_of(p.pair) * a.d_plane : p.d;
     };
     auto copy_x = [&](const Place& p, int j, int to) __attribute__((always_inline)) {
         f8_copy16(p.x, xoff[j], lds + (uint32_t)(to * STAGE + (wave + W * j) * 1024));
@@ -795,7 +803,7 @@ hipError_t backward(const uint8_t* wq, const float* wd, int64_t n, int parts, in
         a.vec = rows_aligned<T>(dw, lddw, 4);
         const q8v::F8GradPlan plan = dw_plan;
         if (!plan.big) a.dx = add;
-        const int64_t steps = TERMS * (TERMS + 1) / 2 * (p.rows / kGStep);
+        const int64_t steps = kPairs<T> * (p.rows / kGStep);
         a.range_steps = (int)((steps + plan.ranges - 1) / plan.ranges);
         a.ranges = (int)((steps + a.range_steps - 1) / a.range_steps);
         if (a.ranges > 1) {

@@ -518,9 +518,11 @@ inline q8_status check_f8_linear(const void* wq, const void* wd, int64_t n_out, 
     return Q8_OK;
 }
 
-// bf16 parts that a value of a gradient's type is taken as, and the pairs of parts whose
-// products the weights' gradient adds.
-inline int f8_terms(int32_t type) { return type == Q8_F32 ? 3 : type == Q8_F16 ? 2 : 1; }
+// bf16 parts that a value of a gradient's type is taken as, those of an input's value (code * scale) beside it, and the
+// pairs of parts whose products the weights' gradient adds.
+constexpr int f8_terms(int32_t type) { return type == Q8_F32 ? 3 : type == Q8_F16 ? 2 : 1; }
+constexpr int f8_value_terms(int32_t type) { return type == Q8_F32 ? 3 : 2; }
+constexpr int f8_pairs(int32_t type) { return type == Q8_F32 ? 6 : type == Q8_F16 ? 3 : 2; }
 
 // How a gradient's product runs: on tiles of 256 x 256 where they fill half of the device, else on tiles of
 // `rows` x 128 whose sums, if the tiles are few, are cut into ranges that run beside each other and are
@@ -547,13 +549,12 @@ inline F8GradPlan f8_dx_plan(int64_t m, int64_t n_part, int parts, int64_t k, in
     return f8_grad_plan(m, 1, k, 64, parts * f8_terms(type) * ((n_part + kF8Step - 1) / kF8Step));
 }
 inline F8GradPlan f8_dw_plan(int64_t m, int64_t n_part, int parts, int64_t k, int32_t type) {
-    const int64_t pairs = f8_terms(type) * (f8_terms(type) + 1) / 2;
-    return f8_grad_plan(n_part, parts, k, 128, pairs * ((m + kF8Step - 1) / kF8Step));
+    return f8_grad_plan(n_part, parts, k, 128, f8_pairs(type) * ((m + kF8Step - 1) / kF8Step));
 }
 
 // Workspace of the backward calls: the gradients of the products as planes of bf16 parts
 // [terms][m][ldd], a part of the matrix's rows from column ldd / parts on, the inputs as planes
-// [terms][rows][k] (columns of a part and rows in whole steps), and the ranges' sums of dx and of dw (dx's are
+// [value terms][rows][k] (columns of a part and rows in whole steps), and the ranges' sums of dx and of dw (dx's are
 // added while dw's are made).
 struct F8BackwardWorkspace {
     int64_t ldd;
@@ -570,7 +571,7 @@ inline F8BackwardWorkspace f8_backward_layout(int64_t m, int64_t n_part, int par
     const size_t dw_sums = dw_ranges > 1 ? dw_ranges * size_t(parts * n_part) * size_t(k) : 0;
     size_t off = 0;
     w.d_off = off;    off = round_up(off + 2 * terms * size_t(m) * size_t(w.ldd), 256);
-    w.x_off = off;    off = round_up(off + 2 * terms * rows * size_t(k), 256);
+    w.x_off = off;    off = round_up(off + 2 * size_t(f8_value_terms(type)) * rows * size_t(k), 256);
     w.sums_off = off; off = round_up(off + sizeof(float) * dx_sums, 256);
     w.dw_sums_off = off; off = round_up(off + sizeof(float) * dw_sums, 256);
     w.total = off ? off : 256;

@@ -526,10 +526,9 @@ size_t f8_linear_fused_gate_up_silu_backward_workspace_bytes(int64_t m, int64_t 
  * Products run on the bf16 matrix cores with float32 accumulation and one rounding at the end.
  * Codes are exact in bf16.  Gradients of bf16 are taken as they are, binary16 ones as two bf16
  * parts and float32 ones as three, exactly (of float32 numbers below 2^-110 what lies below bf16's least,
- * 2^-133, is left out); a value of x (code * scale) is rounded to as many
- * parts for dw: to bf16 with bf16 gradients (scales that are powers of two: not at all), to
- * within 2^-16 with binary16, exactly as a float32 with float32.  Of the products of parts those
- * below 2^-16 (binary16) and 2^-24 (float32) of the whole are left out.
+ * 2^-133, is left out); a value of x (code * scale) enters dw as two
+ * such parts, to within 2^-17, and with float32 gradients as three, exactly as a float32.  Of the products of
+ * parts those below 2^-16 (binary16) and 2^-24 (float32) of the whole are left out.
  */
 q8_status f8_linear_backward(const uint8_t* wq, const float* wd, int64_t n, int64_t k, const uint8_t* xq,
                              const float* xd, int64_t m, const void* dy, int32_t type, int64_t lddy, void* dx,

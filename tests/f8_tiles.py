@@ -23,7 +23,8 @@ def forward_tile(m, n_out, kind, fused):
     return tiles[time.index(min(time))]
 
 
-TERMS = {"bfloat16": 1, "float16": 2, "float32": 3}
+TERMS = {"bfloat16": 1, "float16": 2, "float32": 3}  # parts of a gradient
+PAIRS = {"bfloat16": 2, "float16": 3, "float32": 6}  # products of its parts with those of x's values
 
 
 def _plan(rows, parts, cols, tile_rows, steps):
@@ -38,4 +39,4 @@ def dx_form(m, n, k, kind, parts):
 
 
 def dw_form(m, n, k, kind, parts):
-    return _plan(n, parts, k, 128, TERMS[kind] * (TERMS[kind] + 1) // 2 * _up(m, 64))
+    return _plan(n, parts, k, 128, PAIRS[kind] * _up(m, 64))
